@@ -273,6 +273,126 @@ bpa_status bpa_select_blocks_noalloc(const void* q, const void* k, int32_t dtype
                                      int32_t block_size, int32_t top_n,
                                      int32_t* block_idx_out, void* stream);
 
+/* ---- paged 8-bit key / value cache --------------------------------------------------------
+ *
+ * The step of a program that answers with a trained model: plan the step, append the new
+ * tokens' keys and values, attend over them (the last two once per layer).
+ *
+ *   The cache holds pages of page_size tokens.  Code (page, head, token, channel) of k_cache is
+ *   an e4m3 number (8 bits: sign, 4 exponent bits with bias 7, 3 mantissa bits; largest 448; no
+ *   infinities) and stands for code * k_scale[page, head]; likewise v_cache with dv channels.
+ *   Element (page, h, t, c) sits at base + page*sp + h*sh + t*st + c for strides (sp, sh, st) in
+ *   elements (= bytes), so both [pages, Hkv, page_size, d] and [pages, page_size, Hkv, d] fit.
+ *   Scales are finite, float32 [num_pages, Hkv], contiguous; bpa_cache_append writes powers of
+ *   two, or 0 for a page whose rows are all zero (its codes are then all zero).
+ *   Request r holds tokens 0..kv_lens[r]-1; token p sits in page page_table[r, p / page_size] at
+ *   offset p % page_size.  Table entries past the request's pages are never read.
+ *   Packed rows: the step's rows of all requests stand one after another, rows
+ *   cu_q[r]..cu_q[r+1]-1 belong to request r; a buffer of T rows may have more (a padded batch):
+ *   rows from cu_q[R] on are neither read nor written.
+ *
+ * A fault that only the device can see (a page id outside [0, num_pages), a length past the
+ * table, a slot outside the cache) is recorded as BPA_ERR_DEVICE_CHECK for bpa_check; the
+ * kernels skip what they cannot address, and what they write for that request is unspecified.
+ * The functions below are an addition of this library; the pages that the other entry points
+ * follow have no counterpart.  BPA_VERSION counts the versions of bpa_attn_desc only. */
+typedef struct bpa_cache_desc {
+    uint32_t struct_size;      /* = sizeof(bpa_cache_desc); zero-initialise the rest */
+    int32_t dtype;             /* bpa_dtype of the tensors beside the cache: k, v / q, o */
+    int32_t Hkv, d, dv;        /* kv heads; head dims of k and v (1..512; dv 0 selects d) */
+    int32_t page_size;         /* tokens per page, 1..1024 */
+    int32_t num_pages;         /* page_size * num_pages <= 2^30 */
+    int32_t reserved;          /* must be 0 */
+    void* k_cache;             /* e4m3 */
+    void* v_cache;
+    int64_t k_cache_strides[3];   /* (page, head, token), >= 0 */
+    int64_t v_cache_strides[3];
+    float* k_scale;            /* [num_pages, Hkv] */
+    float* v_scale;
+} bpa_cache_desc;
+
+/* The packed query rows of one step and the masks (as in bpa_attn_desc, the causal / window
+ * diagonal of a request's row i at position p = kv_lens[r] - (rows of r) + i). */
+typedef struct bpa_cache_batch {
+    uint32_t struct_size;      /* = sizeof(bpa_cache_batch); zero-initialise the rest */
+    int32_t R, T, Hq;          /* requests, packed rows (<= 2^30), q heads (a multiple of Hkv, <= 65535) */
+    int32_t max_pages;         /* columns of page_table; page_size * max_pages <= 2^30 */
+    int32_t max_q;             /* no request has more rows than this; 0 selects T.  It guides the
+                                * choice of kernel; a larger request is still computed in full */
+    const void* q;             /* [T, Hq, d] */
+    int64_t q_strides[2];      /* (row, head) of q, last dim contiguous */
+    int64_t o_strides[2];      /* (row, head) of o */
+    const int32_t* page_table; /* [R, max_pages], contiguous */
+    const int32_t* kv_lens;    /* [R] tokens in the cache, the step's own included */
+    const int32_t* cu_q;       /* [R + 1] first row of each request, ascending */
+    float scale;               /* <= 0 selects d^-0.5 */
+    int32_t causal;            /* nonzero: keys up to p */
+    int32_t window_left;       /* inclusive; -1 = unbounded */
+    int32_t window_right;
+    const float* sink;         /* [Hq] sink logits or NULL */
+} bpa_cache_batch;
+
+/* Block tables and slot maps of one step, built on the device.
+ *   Request r holds ctx_lens[r] tokens in its first ceil(ctx_lens[r] / page_size) table entries
+ *   and brings new_lens[r] rows.  The pages that it lacks come off the end of the free list
+ *   (free_pages[0 .. *free_count - 1]), requests in ascending order, each request's pages in
+ *   ascending position, and are written into page_table.  A request that lacks none, or
+ *   whose pages and those of all requests before it fit the free list, is granted:
+ *     kv_lens[r] = ctx + new,  ctx_lens_out[r] = ctx + new,  its rows' slot_map = page *
+ *     page_size + offset, positions = place in the sequence.
+ *   Otherwise it has to wait: kv_lens[r] = 0, ctx_lens_out[r] = ctx, slots and positions -1 (its
+ *   rows keep their place in the packed tensors: append skips them, attention gives them 0).
+ *   cu_q[0..R] is the running sum of new_lens; slots and positions of rows behind cu_q[R] are
+ *   -1.  *free_count_out = what is left.  A request's pages are given back by writing its ids at
+ *   free_pages[count..] and adding to the count, between steps.
+ *   ctx_lens_out may be ctx_lens, free_count_out may be free_count (so a captured step advances
+ *   by itself); no other buffers may overlap.  positions may be NULL.
+ *   A negative length, a request longer than its table row, rows past T, a count outside
+ *   [0, num_pages] (clamped) or a bad id in the list: BPA_ERR_DEVICE_CHECK, the request waits
+ *   (a bad id: its slots are -1).
+ *   1 <= R <= 8192, 0 <= T <= 2^30, 1 <= page_size <= 1024, page_size * num_pages and page_size *
+ *   max_pages <= 2^30, free_pages has num_pages entries.
+ *   Workspace: 256 bytes (the status word).  One launch. */
+bpa_status bpa_cache_plan(int32_t R, int32_t T, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                          const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* free_pages,
+                          const int32_t* free_count, int32_t* page_table, int32_t* kv_lens, int32_t* cu_q,
+                          int32_t* slot_map, int32_t* positions, int32_t* ctx_lens_out,
+                          int32_t* free_count_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Writes T rows of new keys k [T, Hkv, d] and values v [T, Hkv, dv] ((row, head) strides, last
+ * dim contiguous) into the slots of slot_map [T] (-1: the row is skipped).
+ *   Rows with consecutive slots in one page form a run; a page takes one run per call (slot maps
+ *   of bpa_cache_plan do; where a map writes a page twice in one call, that page's contents are
+ *   unspecified).  For each run, head and tensor:
+ *     s_new = the smallest power of two s >= 2^-100 with amax <= 448 s, amax the largest finite
+ *             magnitude of the run's rows (0 if amax is 0);
+ *     a run at offset 0 opens the page: scale = s_new; otherwise scale = max(scale, s_new), and
+ *     where it grew, the rows before the run are requantised: code' = e4m3(code * (scale_old / scale));
+ *     the run's codes are e4m3(x * (1 / scale)), round to nearest even (exact but for that one
+ *     rounding with power-of-two scales).  Infinities and NaN are stored as NaN.
+ *   Rows of the page past the run are left as they were.
+ *   max_new: no request brings more rows than this (0: unknown); it guides the choice of kernel.
+ *   Workspace: 256 bytes (the status word). */
+bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const void* v,
+                            const int64_t k_strides[2], const int64_t v_strides[2], const int32_t* slot_map,
+                            int32_t T, int32_t max_new, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace bpa_cache_attn needs (a multiple of 256); 0 if a descriptor is invalid. */
+size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cache_batch* batch);
+
+/* Attention of the packed rows over the cache: for row i of request r, head h, kv head
+ * g = h / (Hq / Hkv), position p = kv_lens[r] - (rows of r) + i:
+ *     z_k = scale * <q[row, h, :], K[k, g, :]>   over k in [0, kv_lens[r]) with
+ *           (!causal || k <= p) && (window_left < 0 || k >= p - window_left)
+ *           && (window_right < 0 || k <= p + window_right)
+ *     m, l, o as in bpa_fwd (a sink joins m and l); a row with no allowed key gives o = 0 and
+ *     m = -inf, l = 0 (with a sink: m = sink, l = 1).
+ * o [T, Hq, dv]; m, l float32 [Hq, T], contiguous, both or neither NULL.  Slots past
+ * kv_lens[r] may hold anything, NaN included.  A value that is not finite among a request's own
+ * tokens makes that request's outputs of that kv head NaN wherever the value is read. */
+bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* batch, void* o, float* m, float* l,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads the status word of a workspace used by an earlier call (blocking
  * copy; synchronise the stream first).  BPA_OK, BPA_ERR_TIMEOUT or
  * BPA_ERR_DEVICE_CHECK; BPA_ERR_CUDA if the copy itself fails. */

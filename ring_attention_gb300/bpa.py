@@ -53,6 +53,30 @@ class bpa_attn_desc(ctypes.Structure):
     ]
 
 
+class bpa_cache_desc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_cache_strides", ctypes.c_int64 * 3), ("v_cache_strides", ctypes.c_int64 * 3),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class bpa_cache_batch(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("R", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("max_q", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 2), ("o_strides", ctypes.c_int64 * 2),
+        ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+        ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
+        ("window_left", ctypes.c_int32), ("window_right", ctypes.c_int32),
+        ("sink", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -90,6 +114,14 @@ def lib() -> ctypes.CDLL:
         L.bpa_select_blocks_noalloc.restype = ctypes.c_int
         L.bpa_set_phase_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i32]
         L.bpa_set_phase_events.restype = None
+        cp, bp, i64p = ctypes.POINTER(bpa_cache_desc), ctypes.POINTER(bpa_cache_batch), ctypes.POINTER(ctypes.c_int64)
+        L.bpa_cache_plan.argtypes = [i32] * 5 + [P] * 12 + [sz, P]
+        L.bpa_cache_plan.restype = ctypes.c_int
+        L.bpa_cache_append.argtypes = [cp, P, P, i64p, i64p, P, i32, i32, P, sz, P]
+        L.bpa_cache_append.restype = ctypes.c_int
+        L.bpa_cache_attn_workspace_size.argtypes, L.bpa_cache_attn_workspace_size.restype = [cp, bp], sz
+        L.bpa_cache_attn.argtypes = [cp, bp, P, P, P, P, sz, P]
+        L.bpa_cache_attn.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -302,3 +334,191 @@ def bpa_debug_wait_timeout(workspace_buf: torch.Tensor, limit_ns: int, stream=No
     st = lib().bpa_debug_wait_timeout(workspace_buf.data_ptr(), workspace_buf.numel(), int(limit_ns),
                                       _stream_ptr(stream))
     _raise_if(st, "bpa_debug_wait_timeout")
+
+
+# ---- paged 8-bit key / value cache --------------------------------------------------------------
+def _i32_buffer(t, name, shape, device=None):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor, got {t.dtype} {list(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+class _Launch:
+    """The device of a call made current, and its stream: ``stream``, or torch's current one there.
+    Buffers that the call makes for itself on another stream than torch's are marked for it."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        here = torch.cuda.current_stream(self.device)
+        self.other = self.stream if self.stream is not None and self.stream.cuda_stream != here.cuda_stream else None
+        self.ptr = here.cuda_stream if self.stream is None else self.stream.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+
+def make_cache_desc(k_cache, v_cache, k_scale, v_scale, dtype) -> bpa_cache_desc:
+    """Fill a bpa_cache_desc from the cache's tensors (no data is touched): k_cache [pages, Hkv,
+    page_size, d], v_cache [pages, Hkv, page_size, dv] (uint8 or float8_e4m3fn, last dim
+    contiguous; a [pages, page_size, Hkv, d] cache is passed as its transpose(1, 2)), scales
+    float32 [pages, Hkv].  dtype: of the tensors beside the cache."""
+    D = bpa_cache_desc()
+    D.struct_size = ctypes.sizeof(bpa_cache_desc)
+    if dtype == torch.bfloat16:
+        D.dtype = BPA_BF16
+    elif dtype == torch.float32:
+        D.dtype = BPA_FP32
+    else:
+        raise TypeError(f"tensors must be bfloat16 or float32, got {dtype}")
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dim() != 4 or c.dtype not in (torch.uint8, torch.float8_e4m3fn) or (c.stride(3) != 1 and c.shape[3] != 1):
+            raise ValueError(f"{name} must be a 4-D [pages, Hkv, page_size, channels] tensor of uint8 or "
+                             "float8_e4m3fn with contiguous channels")
+    pages, Hkv, P, d = k_cache.shape
+    if v_cache.shape[:3] != k_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache must share pages, heads and page size")
+    for name, c in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if c.dtype != torch.float32 or c.shape != (pages, Hkv) or not c.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [{pages}, {Hkv}] tensor")
+    if not (k_cache.device == v_cache.device == k_scale.device == v_scale.device):
+        raise ValueError("the cache's tensors must be on one device")
+    D.Hkv, D.d, D.dv, D.page_size, D.num_pages = Hkv, d, v_cache.shape[3], P, pages
+    D.k_cache, D.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    D.k_cache_strides[:] = k_cache.stride()[:3]
+    D.v_cache_strides[:] = v_cache.stride()[:3]
+    D.k_scale, D.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    return D
+
+
+def _rows_strides(t, name, shape, dtype, device):
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on {device}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if t.stride(2) != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    return t.stride()[:2]
+
+
+def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, page_size, T, ctx_lens_out=None,
+                   free_count_out=None, kv_lens=None, cu_q=None, slot_map=None, positions=None, workspace_buf=None,
+                   stream=None):
+    """Block tables and slot maps of one step: page_table [R, max_pages] gets the new pages' ids
+    (from the end of free_pages [num_pages], of which free_count [1] are free), and returned are
+    (kv_lens [R], cu_q [R + 1], slot_map [T], positions [T], ctx_lens_out [R], free_count_out [1]),
+    all int32.  ctx_lens_out=ctx_lens and free_count_out=free_count update in place."""
+    if ctx_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("ctx_lens must be [R], page_table [R, max_pages], free_pages [num_pages]")
+    dev, R, T = ctx_lens.device, ctx_lens.shape[0], int(T)
+    if page_table.shape[0] != R:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows for {R} requests")
+    max_pages, num_pages = page_table.shape[1], free_pages.shape[0]
+    ins = [_i32_buffer(t, name, shape, dev) for t, name, shape in (
+        (ctx_lens, "ctx_lens", (R,)), (new_lens, "new_lens", (R,)), (free_pages, "free_pages", (num_pages,)),
+        (free_count, "free_count", (1,)), (page_table, "page_table", (R, max_pages)))]
+    given = [(kv_lens, "kv_lens", (R,)), (cu_q, "cu_q", (R + 1,)), (slot_map, "slot_map", (T,)),
+             (positions, "positions", (T,)), (ctx_lens_out, "ctx_lens_out", (R,)),
+             (free_count_out, "free_count_out", (1,))]
+    for t, name, shape in given:
+        if t is not None:
+            _i32_buffer(t, name, shape, dev)
+    with _Launch(dev, stream) as at:
+        outs = [at.empty(shape, torch.int32) if t is None else t for t, name, shape in given]
+        ws = at.empty(256, torch.uint8) if workspace_buf is None else workspace_buf
+        st = lib().bpa_cache_plan(R, T, int(page_size), num_pages, max_pages, *ins, *[t.data_ptr() for t in outs],
+                                  ws.data_ptr(), ws.numel(), at.ptr)
+    _raise_if(st, "bpa_cache_plan")
+    return tuple(outs)
+
+
+def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_new=0, workspace_buf=None,
+                     stream=None):
+    """Write rows k [T, Hkv, d], v [T, Hkv, dv] into the cache's slots slot_map [T] (-1: skipped),
+    updating k_cache, v_cache, k_scale, v_scale in place."""
+    D = make_cache_desc(k_cache, v_cache, k_scale, v_scale, k.dtype)
+    dev, T = k_cache.device, k.shape[0]
+    ks = (ctypes.c_int64 * 2)(*_rows_strides(k, "k", (T, D.Hkv, D.d), k.dtype, dev))
+    vs = (ctypes.c_int64 * 2)(*_rows_strides(v, "v", (T, D.Hkv, D.dv), k.dtype, dev))
+    slots = _i32_buffer(slot_map, "slot_map", (T,), dev)
+    with _Launch(dev, stream) as at:
+        ws = at.empty(256, torch.uint8) if workspace_buf is None else workspace_buf
+        st = lib().bpa_cache_append(ctypes.byref(D), k.data_ptr(), v.data_ptr(), ks, vs, slots, T, int(max_new),
+                                    ws.data_ptr(), ws.numel(), at.ptr)
+    _raise_if(st, "bpa_cache_append")
+
+
+def make_cache_batch(q, page_table, kv_lens, cu_q, *, max_q=0, causal=True, window=(-1, -1), scale=None,
+                     sink=None) -> bpa_cache_batch:
+    """Fill a bpa_cache_batch (all but o_strides) from the step's tensors (no data is touched)."""
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("q must be [T, Hq, d], page_table [R, max_pages]")
+    B = bpa_cache_batch()
+    B.struct_size = ctypes.sizeof(bpa_cache_batch)
+    T, Hq, d = q.shape
+    R, dev = page_table.shape[0], q.device
+    B.R, B.T, B.Hq, B.max_pages, B.max_q = R, T, Hq, page_table.shape[1], int(max_q)
+    B.q = q.data_ptr()
+    B.q_strides[:] = _rows_strides(q, "q", (T, Hq, d), q.dtype, dev)
+    B.page_table = _i32_buffer(page_table, "page_table", (R, page_table.shape[1]), dev)
+    B.kv_lens = _i32_buffer(kv_lens, "kv_lens", (R,), dev)
+    B.cu_q = _i32_buffer(cu_q, "cu_q", (R + 1,), dev)
+    B.scale = 0.0 if scale is None else float(scale)
+    B.causal = int(bool(causal))
+    B.window_left, B.window_right = (-1, -1) if window is None else (int(window[0]), int(window[1]))
+    if sink is not None:
+        if sink.dtype != torch.float32 or sink.shape != (Hq,) or not sink.is_contiguous() or sink.device != dev:
+            raise ValueError("sink must be a contiguous float32 [Hq] tensor on q's device")
+        B.sink = sink.data_ptr()
+    return B
+
+
+def bpa_cache_attn_workspace_size(cache: bpa_cache_desc, batch: bpa_cache_batch) -> int:
+    return int(lib().bpa_cache_attn_workspace_size(ctypes.byref(cache), ctypes.byref(batch)))
+
+
+def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, cu_q, *, o=None, m=None, l=None,
+                   workspace_buf=None, stream=None, **kw):
+    """Attention of packed rows q [T, Hq, d] over the cache.  Returns (o, m, l): o [T, Hq, dv]; m and
+    l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  Keywords: max_q (the most rows
+    of a request, guides the choice of kernel), causal, window, scale, sink."""
+    D = make_cache_desc(k_cache, v_cache, k_scale, v_scale, q.dtype)
+    B = make_cache_batch(q, page_table, kv_lens, cu_q, **kw)
+    T, Hq, dev = B.T, B.Hq, k_cache.device
+    if q.shape[2] != D.d or q.device != dev:
+        raise ValueError("q must have k_cache's head dim and device")
+    for t, name in ((m, "m"), (l, "l")):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (Hq, T) or not t.is_contiguous() or
+                              t.device != dev):
+            raise ValueError(f"{name} must be a contiguous float32 [Hq, T] tensor on q's device")
+    if o is not None:
+        B.o_strides[:] = _rows_strides(o, "o", (T, Hq, D.dv), q.dtype, dev)
+    with _Launch(dev, stream) as at:
+        if o is None:
+            o = at.empty((T, Hq, D.dv), q.dtype)
+            B.o_strides[:] = o.stride()[:2]
+        m = at.empty((Hq, T), torch.float32) if m is None else m
+        l = at.empty((Hq, T), torch.float32) if l is None else l
+        need = bpa_cache_attn_workspace_size(D, B)
+        if need == 0:
+            _raise_if(BPA_ERR_INVALID_ARG, "bpa_cache_attn_workspace_size")
+        ws = at.empty(need, torch.uint8) if workspace_buf is None else workspace_buf
+        st = lib().bpa_cache_attn(ctypes.byref(D), ctypes.byref(B), o.data_ptr(), m.data_ptr(), l.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), at.ptr)
+    _raise_if(st, "bpa_cache_attn")
+    return o, m, l

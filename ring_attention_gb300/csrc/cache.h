@@ -1,0 +1,80 @@
+// cache.h - the paged 8-bit key / value cache: validated calls and kernel launchers of libbpa.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bpa.h"
+
+namespace bpa {
+
+constexpr int kPlanMaxR = 8192;      // requests of one plan: their lengths and offsets sit in shared memory
+
+struct PlanArgs {
+    int R, T, P, num_pages, max_pages;
+    const int32_t *ctx, *add, *free_pages, *free_count;
+    int32_t *table, *kv_lens, *cu_q, *slots, *positions, *ctx_out, *count_out;
+    uint32_t* status;
+};
+
+struct AppendArgs {
+    int dtype, Hkv, d, dv, P, num_pages, T;
+    const void *k, *v;
+    int64_t ks[2], vs[2];            // (row, head) strides
+    uint8_t *kc, *vc;
+    int64_t kcs[3], vcs[3];          // (page, head, token) strides
+    float *kscale, *vscale;          // [num_pages, Hkv]
+    const int32_t* slots;
+    int max_new;
+    uint32_t* status;
+};
+
+struct CacheAttnArgs {
+    int dtype, R, T, Hq, Hkv, G, d, dv, P, num_pages, max_pages, max_q;
+    float scale;
+    int causal, wl, wr;              // wl, wr: -1 = unbounded
+    const void* q;
+    int64_t qs[2], os[2];            // (row, head) strides
+    void* o;
+    float *m, *l;                    // [Hq, T] or null
+    const uint8_t *kc, *vc;
+    int64_t kcs[3], vcs[3];
+    const float *kscale, *vscale;
+    const int32_t *table, *kv_lens, *cu_q;
+    const float* sink;
+    uint32_t* status;
+};
+
+#ifdef __CUDACC__
+// Rows and keys of request r, made safe to address: rows clamped to [0, T], the length to the table.
+struct Req {
+    int row0, n, len;                // first packed row, rows, keys
+    bool bad;                        // the length did not fit
+};
+__device__ __forceinline__ Req request_of(const CacheAttnArgs& a, int r) {
+    Req q;
+    q.row0 = min(max(__ldg(a.cu_q + r), 0), a.T);
+    q.n = max(min(__ldg(a.cu_q + r + 1), a.T) - q.row0, 0);
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.P;
+    const int len = __ldg(a.kv_lens + r);
+    q.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), cap));
+    q.bad = len != q.len;
+    return q;
+}
+// Keys [lo, hi] that the masks leave row i of a request (empty: lo > hi).
+__device__ __forceinline__ void row_keys(const CacheAttnArgs& a, const Req& q, int i, int& lo, int& hi) {
+    const int p = q.len - q.n + i;
+    lo = 0;
+    hi = q.len - 1;
+    if (a.causal) hi = min(hi, p);
+    if (a.wr >= 0) hi = static_cast<int>(min(static_cast<int64_t>(hi), static_cast<int64_t>(p) + a.wr));
+    if (a.wl >= 0) lo = static_cast<int>(max(static_cast<int64_t>(0), static_cast<int64_t>(p) - a.wl));
+}
+#endif
+
+cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s);
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_attn_simt(const CacheAttnArgs& a, cudaStream_t s);   // any shape
+
+}  // namespace bpa

@@ -1,0 +1,559 @@
+"""GPU parity of the paged 8-bit cache (plan, append, attention) against its 64-bit definitions.
+
+Plans and appended codes and scales are whole numbers and powers of two: they must be equal.
+Attention is compared element by element with a tolerance from arithmetic (``check_attention``):
+with A = sum p |v| / l (the same attention over |v|) and Z = the largest sum_c |q_c k_c| * scale,
+  * scores: exact products summed in float32 over d terms, at most d + 4 steps of 2^-23 of the
+    partial sums (the tensor cores truncate): dz = (d + 4) 2^-23 Z, plus 2^-21 for the exponential;
+  * each weight moves by dz relatively, in the numerator and in the denominator, and is rounded to
+    16 bits for the product with v: half a bf16 step, 2^-8 (float32 paths keep two halves: 2^-21);
+  * sums over n keys in float32: n 2^-23;
+  * the output is rounded once: 2^-8 |o| in bf16, 2^-24 |o| in float32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as ora
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bpa():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from ring_attention_gb300 import build
+    build.build()
+    from ring_attention_gb300 import bpa as mod
+    return mod
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ---- plan ------------------------------------------------------------------------------------------
+def make_plan(rng, ctx, new, P, spare, pad=0):
+    ctx, new = np.asarray(ctx), np.asarray(new)
+    have, total = -(-ctx // P), -(-(ctx + new) // P)
+    num = max(1, int(total.sum()) + max(spare, -int((total - have).sum())))
+    ids = rng.permutation(num)
+    table = np.full((len(ctx), max(1, int(total.max()) + 1)), -1)
+    at = 0
+    for r, n in enumerate(have):
+        table[r, :n] = ids[at:at + n]
+        at += n
+    free = np.zeros(num, int)
+    free[:num - at] = ids[at:]
+    return dict(ctx=ctx, new=new, table=table, free=free, count=num - at, P=P, T=int(new.sum()) + pad)
+
+
+def run_plan(bpa, c, **kw):
+    table = i32(c["table"])
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")     # stale: the call clears it
+    got = bpa.bpa_cache_plan(i32(c["ctx"]), i32(c["new"]), table, i32(c["free"]), i32([c["count"]]), page_size=c["P"],
+                             T=c["T"], workspace_buf=ws, **kw)
+    torch.cuda.synchronize()
+    kv, cu, slots, pos, ctx, left = (t.cpu().numpy() for t in got)
+    return (kv, cu, slots, pos, ctx, table.cpu().numpy(), int(left[0])), ws
+
+
+def check_plan(bpa, c):
+    got, ws = run_plan(bpa, c)
+    bpa.bpa_check(ws)
+    for g, w, name in zip(got, ora.plan(**c), ("kv_lens", "cu_q", "slots", "positions", "ctx", "table", "count")):
+        np.testing.assert_array_equal(g, w, err_msg=name)
+
+
+PLANS = {
+    "one": ([0], [1], 16, 0, 0), "one_idle": ([5], [0], 16, 3, 0), "page_full": ([16], [1], 16, 1, 0),
+    "page_exact": ([15], [1], 16, 0, 2), "empty_rows": ([0, 0, 7], [0, 3, 0], 4, 2, 5),
+    "page_of_one": ([2, 0, 9], [4, 1, 2], 1, 0, 1), "odd_page": ([2, 50, 9], [40, 1, 22], 7, 3, 0),
+    "no_pages_left": ([3, 4, 0], [1, 1, 1], 4, -9, 0),     # only the first has room in its page
+}
+
+
+@pytest.mark.parametrize("name", PLANS)
+def test_plan_small(bpa, name):
+    check_plan(bpa, make_plan(np.random.default_rng(1), *PLANS[name]))
+
+
+@pytest.mark.parametrize("R,hi,P,spare,pad", [(256, 1, 64, 10, 0), (1500, 4, 16, -100, 77), (61, 700, 16, 5, 100),
+                                              (33, 900, 64, -40, 0), (8192, 2, 32, 0, 3)])
+def test_plan_ragged(bpa, R, hi, P, spare, pad):
+    rng = np.random.default_rng(R)
+    check_plan(bpa, make_plan(rng, rng.integers(0, 500, R), rng.integers(0, hi + 1, R), P, spare, pad))
+
+
+def test_plan_advances_in_place_under_a_graph(bpa):
+    c = make_plan(np.random.default_rng(3), [0, 14, 31], [1, 1, 1], 16, 12)
+    c["table"] = np.concatenate([c["table"], np.full((3, 4), -1)], 1)
+    ctx, new, table, free, count = i32(c["ctx"]), i32(c["new"]), i32(c["table"]), i32(c["free"]), i32([c["count"]])
+    kw = dict(page_size=16, T=3, ctx_lens_out=ctx, free_count_out=count)
+    state = (c["ctx"], c["table"], c["count"])
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        outs = bpa.bpa_cache_plan(ctx, new, table, free, count, **kw)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs = bpa.bpa_cache_plan(ctx, new, table, free, count, **kw)
+        for _ in range(4):
+            g.replay()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        kv, cu, slots, pos, *rest = ora.plan(state[0], c["new"], state[1], c["free"], state[2], 16, 3)
+        state = rest
+    for got, want in zip(outs[:4] + (ctx, table, count), (kv, cu, slots, pos) + tuple(state)):
+        np.testing.assert_array_equal(got.cpu().numpy().reshape(np.shape(want)), want)
+
+
+def test_plan_reports_bad_inputs(bpa):
+    base = make_plan(np.random.default_rng(4), [4, 9, 3], [2, 3, 1], 4, 3)
+    good = ora.plan(**base)
+    for field, r, value in (("ctx", 1, -3), ("new", 1, -1), ("new", 1, 4000)):
+        c = {**base, field: np.array(base[field])}
+        c[field][r] = value
+        got, ws = run_plan(bpa, c)
+        with pytest.raises(bpa.BpaError):
+            bpa.bpa_check(ws)
+        assert got[0][1] == 0 and got[4][1] == c["ctx"][1]       # the request waits
+        assert got[0][0] == good[0][0]                           # the one before it does not
+        np.testing.assert_array_equal(got[2][:2], good[2][:2])
+    for T in (5, 4):                                             # too few rows: the last request waits
+        got, ws = run_plan(bpa, {**base, "T": T})
+        with pytest.raises(bpa.BpaError):
+            bpa.bpa_check(ws)
+        assert got[0][2] == 0 and got[1].max() <= T
+    c = {**base, "free": np.full_like(base["free"], 10 ** 6)}
+    got, ws = run_plan(bpa, c)
+    with pytest.raises(bpa.BpaError):
+        bpa.bpa_check(ws)
+    assert got[5].max() < len(c["free"]) and got[2].max() < 4 * len(c["free"])
+
+
+# ---- append ----------------------------------------------------------------------------------------
+def random_cache(rng, pages, Hkv, P, c, spread=1.0):
+    """Codes with the values +-[0, 448] and power-of-two scales, as append leaves them."""
+    codes = rng.integers(0, 256, (pages, Hkv, P, c)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    x = rng.standard_normal((pages, Hkv, P, c))
+    scale = np.exp2(np.round(rng.standard_normal((pages, Hkv)) * spread) - 7)
+    codes = ora.e4m3_round(np.clip(x / scale[:, :, None, None], -448, 448))
+    return codes, scale.astype(np.float32)
+
+
+def slots_for(rng, ctx, new, P, pages):
+    """(slots, table) of requests with pages of their own."""
+    ids = rng.permutation(pages)
+    width = max(1, max(-(-(a + b) // P) for a, b in zip(ctx, new)))
+    table, at, slots = np.full((len(ctx), width), -1), 0, []
+    for r, (a, b) in enumerate(zip(ctx, new)):
+        n = -(-(a + b) // P)
+        table[r, :n] = ids[at:at + n]
+        at += n
+        slots += [table[r, p // P] * P + p % P for p in range(a, a + b)]
+    return np.array(slots, np.int64), table
+
+
+def as_dtype(x, dtype):
+    t = torch.from_numpy(np.asarray(x, np.float32)).to(dtype)
+    return t.cuda(), t.double().numpy()
+
+
+def run_append(bpa, k, v, slots, kc, vc, ks, vs, max_new=0, nhd=False):
+    dk, dvv = (torch.from_numpy(c).cuda() for c in (kc, vc))
+    if nhd:
+        dk, dvv = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (dk, dvv))
+    sk, sv = (torch.from_numpy(c).cuda() for c in (ks, vs))
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    bpa.bpa_cache_append(k, v, i32(slots), dk, dvv, sk, sv, max_new=max_new, workspace_buf=ws)
+    torch.cuda.synchronize()
+    return (dk.cpu().numpy(), sk.cpu().numpy(), dvv.cpu().numpy(), sv.cpu().numpy()), ws
+
+
+def check_append(bpa, rng, ctx, new, Hkv, d, dv, P, dtype, *, mag=1.0, nhd=False, strided=False, max_new=None, pad=0):
+    pages = sum(-(-(a + b) // P) for a, b in zip(ctx, new)) + 3
+    slots, _ = slots_for(rng, ctx, new, P, pages)
+    slots = np.concatenate([slots, np.full(pad, -1)])
+    T = len(slots)
+    kc, ks = random_cache(rng, pages, Hkv, P, d)
+    vc, vs = random_cache(rng, pages, Hkv, P, dv)
+    mags = np.exp2(rng.integers(-3, 4, (T, 1, 1))) * mag
+    tk, xk = as_dtype(rng.standard_normal((T, Hkv, d)) * mags, dtype)
+    tv, xv = as_dtype(rng.standard_normal((T, Hkv, dv)) * mags, dtype)
+    if strided:       # rows of a fused [T, Hkv, d + dv + 5] projection
+        both = torch.zeros(T, Hkv, d + dv + 5, dtype=dtype, device="cuda")
+        both[:, :, :d], both[:, :, d:d + dv] = tk, tv
+        tk, tv = both[:, :, :d], both[:, :, d:d + dv]
+    got, ws = run_append(bpa, tk, tv, slots, kc, vc, ks, vs, max(new) if max_new is None else max_new, nhd)
+    bpa.bpa_check(ws)
+    for x, c, s, gc, gs in ((xk, kc, ks, got[0], got[1]), (xv, vc, vs, got[2], got[3])):
+        wc, wsc = ora.append(x, slots, c, s)
+        np.testing.assert_array_equal(gs, wsc)
+        np.testing.assert_array_equal(gc, wc)
+
+
+APPENDS = [   # ctx, new, Hkv, d, dv, P
+    ([0], [1], 1, 64, 64, 16), ([15], [1], 2, 128, 128, 16), ([16, 3], [1, 1], 8, 128, 64, 16),
+    ([0, 5, 60, 130], [70, 1, 9, 64], 2, 128, 128, 64), ([7, 0, 31], [40, 33, 0], 2, 80, 80, 32),
+    ([1, 2], [300, 5], 1, 256, 64, 128), ([3, 0], [11, 25], 3, 33, 7, 5), ([0, 2], [9, 3], 2, 1, 1, 1),
+    ([100, 0], [3, 1000], 2, 64, 512, 256),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", APPENDS, ids=lambda c: f"d{c[3]}_{c[4]}_P{c[5]}_T{sum(c[1])}")
+def test_append_equals_the_definition(bpa, case, dtype):
+    ctx, new, Hkv, d, dv, P = case
+    check_append(bpa, np.random.default_rng(d + P), ctx, new, Hkv, d, dv, P, dtype)
+
+
+@pytest.mark.parametrize("kw", [dict(nhd=True), dict(strided=True), dict(max_new=0), dict(max_new=1), dict(pad=9),
+                                dict(mag=1e-30), dict(mag=1e30)],
+                         ids=["nhd", "strided", "unknown_max", "wrong_max", "padded", "tiny", "huge"])
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [90, 1, 17, 64]], ids=["step", "prompt"])
+def test_append_layouts(bpa, kw, new):
+    check_append(bpa, np.random.default_rng(5), [9, 0, 130, 64], new, 2, 128, 64, 64, torch.bfloat16, **kw)
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_append_zeros_infinities_and_nan(bpa, rows):
+    rng = np.random.default_rng(6)
+    kc, ks = random_cache(rng, 4, 2, 16, 32)
+    ks[1] = 0                                     # a page of zeros so far
+    kc[1] = 0
+    x = rng.standard_normal((rows, 2, 32)).astype(np.float32)
+    x[0, 0, :3] = [np.inf, -np.inf, np.nan]
+    x[:, 1] = 0                                   # head 1: nothing but zeros
+    slots = np.concatenate([np.arange(16 + 5, 32), np.arange(48, 64)])[:rows]
+    (gc, gs, vc, vs), ws = run_append(bpa, torch.from_numpy(x).cuda(), torch.from_numpy(x).cuda(), slots, kc, kc, ks, ks)
+    wc, wsc = ora.append(x.astype(np.float64), slots, kc, ks)
+    np.testing.assert_array_equal(gs, wsc)
+    nan = (wc & 0x7F) == 0x7F
+    np.testing.assert_array_equal((gc & 0x7F) == 0x7F, nan)
+    np.testing.assert_array_equal(gc[~nan], wc[~nan])
+    np.testing.assert_array_equal(vc, gc)
+    assert gs[1, 1] == 0 and (gc[1, 0, 5, :3] & 0x7F == 0x7F).all()
+
+
+def test_append_skips_and_reports(bpa):
+    rng = np.random.default_rng(7)
+    kc, ks = random_cache(rng, 4, 1, 16, 16)
+    x = torch.randn(4, 1, 16, device="cuda")
+    slots = [-1, 3, 64, 2 ** 30]                  # two behind the cache's end
+    (gc, gs, *_), ws = run_append(bpa, x, x, slots, kc, kc, ks, ks)
+    with pytest.raises(bpa.BpaError):
+        bpa.bpa_check(ws)
+    wc, wsc = ora.append(f64(x), [-1, 3, -1, -1], kc, ks)
+    np.testing.assert_array_equal(gc, wc)
+    np.testing.assert_array_equal(gs, wsc)
+    (gc, *_), ws = run_append(bpa, x[:0], x[:0], [], kc, kc, ks, ks)
+    bpa.bpa_check(ws)
+    np.testing.assert_array_equal(gc, kc)
+
+
+# ---- attention ---------------------------------------------------------------------------------------
+def make_step(rng, ctx, new, Hq, Hkv, d, dv, P, pad=0, spread=1.0, qmag=1.0):
+    pages = sum(-(-(a + b) // P) for a, b in zip(ctx, new)) + 2
+    slots, table = slots_for(rng, ctx, new, P, pages)
+    kc, ks = random_cache(rng, pages, Hkv, P, d, spread)
+    vc, vs = random_cache(rng, pages, Hkv, P, dv, spread)
+    for r, (a, b) in enumerate(zip(ctx, new)):    # behind the last token: stale rows, NaN among them
+        if (a + b) % P:
+            last = table[r, (a + b) // P]
+            kc[last, :, (a + b) % P:] = 0x7F
+            vc[last, :, (a + b) % P:] = 0x7F
+    return dict(q=rng.standard_normal((len(slots) + pad, Hq, d)) * qmag, kc=kc, vc=vc, ks=ks, vs=vs, table=table,
+                kv=np.add(ctx, new), cu=np.concatenate([[0], np.cumsum(new)]), max_q=max(new))
+
+
+def on_gpu(c, dtype, nhd=False):
+    k, v = torch.from_numpy(c["kc"]).cuda(), torch.from_numpy(c["vc"]).cuda()
+    if nhd:
+        k, v = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (k, v))
+    return (as_dtype(c["q"], dtype)[0], k, v, torch.from_numpy(c["ks"]).cuda(), torch.from_numpy(c["vs"]).cuda(),
+            i32(c["table"]), i32(c["kv"]), i32(c["cu"]))
+
+
+def check_attention(c, dtype, o, m, l, rows=None, **kw):
+    q = as_dtype(c["q"], dtype)[1]
+    args = (c["kc"], c["vc"] & 0x7F, c["ks"], c["vs"], c["table"], c["kv"], c["cu"])
+    A = ora.attention(q, *args, **kw)[0]
+    wo, wm, wl = ora.attention(q, c["kc"], c["vc"], *args[2:], **kw)
+    d, n = q.shape[2], int(max(c["kv"].max(), 1))
+    scale = kw.get("scale") or d ** -0.5
+    val = np.nan_to_num(np.abs(ora.e4m3_values()[c["kc"]])) * c["ks"][:, :, None, None]
+    Z = max(np.abs(q[:, h]).max(0, initial=0) @ val[:, h // (q.shape[1] // val.shape[1])].max((0, 1))
+            for h in range(q.shape[1])) * scale
+    dz = (d + 4) * 2.0 ** -23 * Z + 2.0 ** -21
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    weight = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -21
+    valid = ~np.isnan(wl[0])
+    go, gm, gl = f64(o)[valid], f64(m)[:, valid], f64(l)[:, valid]
+    wo, A, wm, wl = wo[valid], A[valid], wm[:, valid], wl[:, valid]
+    assert (np.abs(go - wo) <= half * np.abs(wo) + (2 * dz + weight + n * 2.0 ** -23) * A * (1 + half)).all()
+    np.testing.assert_array_equal(np.isneginf(gm), np.isneginf(wm))
+    fin = np.isfinite(wm)
+    assert (np.abs(gm[fin] - wm[fin]) <= dz + 2.0 ** -22 * np.abs(wm[fin])).all()
+    assert (np.abs(gl - wl) <= (2 * dz + n * 2.0 ** -23 + 2.0 ** -21) * wl).all()
+    return valid
+
+
+def run_and_check(bpa, c, dtype, nhd=False, **kw):
+    sink = kw.get("sink")
+    t = on_gpu(c, dtype, nhd)
+    T, Hq = c["q"].shape[:2]
+    marker = 77.0
+    o = torch.full((T, Hq, c["vc"].shape[3]), marker, dtype=dtype, device="cuda")
+    m, l = (torch.full((Hq, T), marker, device="cuda") for _ in range(2))
+    dev = {**kw, "sink": None if sink is None else torch.from_numpy(sink.astype(np.float32)).cuda()}
+    need = bpa.bpa_cache_attn_workspace_size(
+        bpa.make_cache_desc(*t[1:5], dtype), bpa.make_cache_batch(t[0], *t[5:], max_q=c["max_q"], **dev))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    bpa.bpa_cache_attn(*t, max_q=c["max_q"], o=o, m=m, l=l, workspace_buf=ws, **dev)
+    torch.cuda.synchronize()
+    bpa.bpa_check(ws)
+    valid = check_attention(c, dtype, o, m, l, **kw)
+    assert (o[~valid] == marker).all() and (m[:, ~valid] == marker).all() and (l[:, ~valid] == marker).all()
+    return o, m, l
+
+
+DTYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+
+SHAPES = [   # ctx, new, Hq, Hkv, d, dv, P
+    ([0], [1], 1, 1, 64, 64, 16), ([700], [1], 32, 8, 128, 128, 64), ([0, 1, 63, 64, 300], [1] * 5, 8, 2, 128, 128, 64),
+    ([15, 16, 17, 511], [1] * 4, 8, 2, 64, 64, 16), ([40, 90], [1, 1], 16, 1, 128, 64, 32),
+    ([130, 7], [1, 1], 7, 1, 80, 80, 16), ([260, 3], [1, 1], 6, 2, 192, 64, 128), ([300, 33], [1, 1], 4, 4, 256, 256, 16),
+    ([100, 0, 31], [3, 8, 1], 8, 2, 128, 128, 16), ([20, 200], [6, 2], 64, 4, 64, 64, 64),
+    ([90, 5], [1, 2], 3, 1, 33, 7, 5), ([9, 14], [1, 1], 2, 1, 512, 512, 8), ([50, 0], [1, 2], 2, 2, 96, 112, 48),
+    ([0, 100, 37], [70, 40, 1], 4, 2, 128, 128, 64), ([64, 0], [33, 130], 8, 2, 64, 64, 32),
+]
+
+
+@DTYPES
+@pytest.mark.parametrize("case", SHAPES, ids=lambda c: f"H{c[2]}_{c[3]}_d{c[4]}_{c[5]}_P{c[6]}_q{max(c[1])}")
+def test_attention_matches_the_definition(bpa, case, dtype):
+    run_and_check(bpa, make_step(np.random.default_rng(sum(case[0]) + case[4]), *case), dtype)
+
+
+MASKS = {"window": dict(window=(20, -1)), "window_0": dict(window=(0, -1)), "not_causal": dict(causal=False),
+         "band": dict(causal=False, window=(10, 5)), "right": dict(causal=False, window=(-1, 0)),
+         "scale": dict(scale=0.3), "wide": dict(window=(2 ** 31 - 1, 2 ** 31 - 1), causal=False)}
+
+
+@DTYPES
+@pytest.mark.parametrize("new", [[1, 1, 1], [5, 1, 0], [100, 3, 17]], ids=["step", "draft", "prompt"])
+@pytest.mark.parametrize("mask", MASKS)
+def test_attention_masks(bpa, mask, new, dtype):
+    c = make_step(np.random.default_rng(8), [200, 0, 63], new, 8, 2, 64, 64, 16, pad=2)
+    run_and_check(bpa, c, dtype, **MASKS[mask])
+
+
+@DTYPES
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 3, 0]], ids=["step", "prompt"])
+def test_attention_sink_and_empty_rows(bpa, new, dtype):
+    rng = np.random.default_rng(9)
+    for sink in (None, rng.standard_normal(4) * 3):
+        c = make_step(rng, [90, 0, 30], new, 4, 2, 128, 128, 32, pad=3)
+        c["kv"] = c["kv"].copy()
+        c["kv"][1] = 0                            # a request that waits: its rows have no keys
+        run_and_check(bpa, c, dtype, sink=sink)
+        c["kv"][0] = min(5, new[0])               # fewer keys than rows: the first rows have none
+        run_and_check(bpa, c, dtype, sink=sink)
+
+
+@DTYPES
+@pytest.mark.parametrize("new", [[1, 1], [60, 2]], ids=["step", "prompt"])
+def test_attention_page_scales_far_apart(bpa, new, dtype):
+    # scales from 2^-37 to 2^23 within a request; a page of zeros has scale 0
+    c = make_step(np.random.default_rng(10), [150, 70], new, 4, 2, 64, 64, 16)
+    c["ks"][:] = 2.0 ** -7
+    c["vs"][:] = np.exp2(np.random.default_rng(11).integers(-30, 30, c["vs"].shape) - 7.0).astype(np.float32)
+    c["vs"][c["table"][0, 2]] = 0
+    c["vc"][c["table"][0, 2]] = 0
+    run_and_check(bpa, c, dtype)
+    # and the rows of one that is far below the others, alone behind a window
+    run_and_check(bpa, c, dtype, window=(3, -1))
+
+
+@DTYPES
+@pytest.mark.parametrize("qmag", [1e-6, 30.0, 1e4], ids=str)
+def test_attention_score_ranges(bpa, qmag, dtype):
+    run_and_check(bpa, make_step(np.random.default_rng(12), [200, 65], [1, 2], 8, 2, 128, 128, 64, qmag=qmag), dtype)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [100, 30]], ids=["step", "prompt"])
+def test_attention_layouts(bpa, new):
+    c = make_step(np.random.default_rng(13), [130, 31], new, 8, 2, 128, 64, 64)
+    want = run_and_check(bpa, c, torch.bfloat16)
+    got = run_and_check(bpa, c, torch.bfloat16, nhd=True)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    # q and o as slices of wider rows; k and v interleaved in one allocation
+    t = on_gpu(c, torch.bfloat16)
+    T = c["q"].shape[0]
+    wide = torch.zeros(T, 8, 128 + 8, dtype=torch.bfloat16, device="cuda")
+    wide[:, :, :128] = t[0]
+    kv = torch.zeros(t[1].shape[0], 2, 64, 2 * 128, dtype=torch.uint8, device="cuda")
+    kv[..., :128], kv[..., 128:192] = t[1], t[2]
+    out = torch.zeros(T, 8, 72, dtype=torch.bfloat16, device="cuda")
+    o, m, l = bpa.bpa_cache_attn(wide[:, :, :128], kv[..., :128], kv[..., 128:192], *t[3:], max_q=c["max_q"],
+                                 o=out[:, :, :64])
+    torch.cuda.synchronize()
+    for a, b in zip((o, m, l), want):
+        assert torch.equal(a, b)
+    assert not out[:, :, 64:].any()
+
+
+def test_attention_odd_strides_and_bases(bpa):
+    # a cache whose rows start at odd bytes, q and o at odd elements: another path, the same answer
+    c = make_step(np.random.default_rng(14), [130, 31], [2, 1], 4, 2, 64, 64, 16)
+    t = on_gpu(c, torch.bfloat16)
+    k = torch.zeros(t[1].shape[:3] + (65,), dtype=torch.uint8, device="cuda")
+    k[..., 1:] = t[1]
+    q = torch.zeros(t[0].shape[:2] + (65,), dtype=torch.bfloat16, device="cuda")
+    q[..., 1:] = t[0]
+    out = torch.zeros(t[0].shape[:2] + (65,), dtype=torch.bfloat16, device="cuda")
+    o, m, l = bpa.bpa_cache_attn(q[..., 1:], k[..., 1:], *t[2:], max_q=2, o=out[..., 1:])
+    torch.cuda.synchronize()
+    check_attention(c, torch.bfloat16, o, m, l)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 30]], ids=["step", "prompt"])
+def test_attention_reports_bad_pages_and_lengths(bpa, new):
+    rng = np.random.default_rng(15)
+    for bad in (-1, 10 ** 6, "len"):
+        c = make_step(rng, [130, 31], new, 4, 2, 64, 64, 16)
+        good = c["table"].copy()
+        if bad == "len":
+            c["kv"] = c["kv"].copy()
+            c["kv"][0] = 10 ** 6
+        else:
+            c["table"][0, 3] = bad
+        t = on_gpu(c, torch.bfloat16)
+        need = bpa.bpa_cache_attn_workspace_size(bpa.make_cache_desc(*t[1:5], torch.bfloat16),
+                                                 bpa.make_cache_batch(t[0], *t[5:], max_q=max(new)))
+        ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        o, m, l = bpa.bpa_cache_attn(*t, max_q=max(new), workspace_buf=ws)
+        torch.cuda.synchronize()
+        with pytest.raises(bpa.BpaError):
+            bpa.bpa_check(ws)
+        # the other request is not touched by it
+        c["table"], c["kv"] = good, np.add([130, 31], new)
+        rows = slice(new[0], None)
+        other = {**c, "q": c["q"][rows], "table": c["table"][1:], "kv": c["kv"][1:], "cu": c["cu"][1:] - new[0]}
+        check_attention(other, torch.bfloat16, o[rows], m[:, rows], l[:, rows])
+
+
+def test_attention_cache_past_32_bits(bpa):
+    # 5 GB of keys: pages whose bytes lie past 2^32
+    c = make_step(np.random.default_rng(16), [600, 100], [1, 3], 4, 2, 128, 64, 64)
+    t = on_gpu(c, torch.bfloat16)
+    num = (5 << 30) // (2 * 64 * 128)
+    ids = torch.randperm(num - 270000, device="cuda")[:t[1].shape[0]] + 270000
+    big = [torch.empty(num, 2, 64, x.shape[3], dtype=torch.uint8, device="cuda") for x in t[1:3]]
+    scales = [torch.zeros(num, 2, device="cuda") for _ in range(2)]
+    for dst, src in zip(big + scales, t[1:5]):
+        dst[ids] = src
+    table = torch.where(t[5] >= 0, ids[t[5].long().clamp(min=0)].int(), t[5]).contiguous()
+    assert int(ids.min()) * 2 * 64 * 128 > 1 << 32
+    o, m, l = bpa.bpa_cache_attn(t[0], *big, *scales, table, *t[6:], max_q=3)
+    torch.cuda.synchronize()
+    check_attention(c, torch.bfloat16, o, m, l)
+
+
+def test_attention_long_contexts_against_bpa_fwd(bpa):
+    # codes times power-of-two scales are exact in bf16: the same attention without a cache
+    g = torch.Generator(device="cuda").manual_seed(17)
+    S, Hq, Hkv, d, P = 2048, 8, 2, 128, 64
+    k, v = (torch.randn(1, S, Hkv, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    q = torch.randn(1, S, Hq, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    kc, vc = (torch.zeros(S // P + 1, Hkv, P, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(S // P + 1, Hkv, device="cuda") for _ in range(2))
+    bpa.bpa_cache_append(k[0], v[0], torch.arange(S, dtype=torch.int32, device="cuda"), kc, vc, ks, vs, max_new=S)
+    dk, dv = ((c[:-1].view(torch.float8_e4m3fn).float() * s[:-1, :, None, None]).transpose(1, 2).reshape(1, S, Hkv, d)
+              .bfloat16() for c, s in ((kc, ks), (vc, vs)))
+    want, wm, wl = bpa.bpa_fwd(q, dk.contiguous(), dv.contiguous(), causal=True)
+    table = torch.arange(S // P, dtype=torch.int32, device="cuda")[None].contiguous()
+    for rows in (1, 7, 300, S):
+        o, m, l = bpa.bpa_cache_attn(q[0, S - rows:], kc, vc, ks, vs, table, i32([S]), i32([0, rows]), max_q=rows)
+        torch.cuda.synchronize()
+        # both round weights and outputs to bf16: |o| is at most 1 or so here, the sum of both sides' steps
+        assert (o.float() - want[0, S - rows:].float()).abs().max() <= 2 * (2.0 ** -8 + 2.0 ** -8) * want[0].abs().max()
+        assert torch.allclose(m, wm[0, :, S - rows:], atol=1e-4, rtol=1e-5)
+        assert torch.allclose(l, wl[0, :, S - rows:], rtol=1e-3)
+        assert (dk.double() - k.double()).abs().max() <= 2.0 ** -4 * k.abs().max()
+
+
+# ---- the step of a serving loop ---------------------------------------------------------------------
+@DTYPES
+def test_serving_steps_together(bpa, dtype):
+    """Prompts, then generated tokens: plan, append, attend on one stream, a captured graph from the
+    third step on; every state and output against the definitions run side by side."""
+    rng = np.random.default_rng(18)
+    R, Hq, Hkv, d, dv, P, pages, width = 4, 8, 2, 64, 32, 16, 30, 9
+    new = np.array([40, 1, 17, 33])
+    table, ctx, count = np.full((R, width), -1), np.zeros(R, int), pages
+    free = rng.permutation(pages)
+    kc, vc = np.zeros((pages, Hkv, P, d), np.uint8), np.zeros((pages, Hkv, P, dv), np.uint8)
+    ks, vs = np.zeros((pages, Hkv), np.float32), np.zeros((pages, Hkv), np.float32)
+    dt, dctx, dfree, dcount = i32(table), i32(ctx), i32(free), i32([count])
+    dk, dvv, dks, dvs = (torch.from_numpy(x).cuda() for x in (kc, vc, ks, vs))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = None
+    for step in range(8):
+        T = int(new.sum()) if step == 0 else R
+        q, k, v = (rng.standard_normal((T, h, c)) * 2.0 ** (step % 3) for h, c in ((Hq, d), (Hkv, d), (Hkv, dv)))
+        (tq, xq), (tk, xk), (tv, xv) = (as_dtype(x, dtype) for x in (q, k, v))
+
+        def call(tq, tk, tv, tnew):
+            plan = bpa.bpa_cache_plan(dctx, tnew, dt, dfree, dcount, page_size=P, T=tq.shape[0], ctx_lens_out=dctx,
+                                      free_count_out=dcount)
+            bpa.bpa_cache_append(tk, tv, plan[2], dk, dvv, dks, dvs, max_new=int(new.max()))
+            return plan + bpa.bpa_cache_attn(tq, dk, dvv, dks, dvs, dt, plan[0], plan[1], max_q=int(new.max()))
+
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            if step < 2:
+                outs = call(tq, tk, tv, i32(new))
+            elif graph is None:
+                statics = [tq.clone(), tk.clone(), tv.clone(), i32(new)]
+                graph = torch.cuda.CUDAGraph()
+                torch.cuda.synchronize()
+                with torch.cuda.graph(graph, stream=side):
+                    outs = call(*statics)
+                graph.replay()
+            else:
+                for a, b in zip(statics, (tq, tk, tv, i32(new))):
+                    a.copy_(b)
+                graph.replay()
+        torch.cuda.synchronize()
+        kv, cu, slots, pos, ctx, table, count = ora.plan(ctx, new, table, free, count, P, T)
+        for got, want in zip(outs[:4] + (dctx, dt, dcount), (kv, cu, slots, pos, ctx, table, [count])):
+            np.testing.assert_array_equal(got.cpu().numpy(), want)
+        kc, ks = ora.append(xk, slots, kc, ks)
+        vc, vs = ora.append(xv, slots, vc, vs)
+        for got, want in ((dk, kc), (dvv, vc), (dks, ks), (dvs, vs)):
+            np.testing.assert_array_equal(got.cpu().numpy(), want)
+        c = dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=table, kv=kv, cu=cu)
+        check_attention(c, dtype, *outs[6:])
+        new = np.array([1, 1, 1, 1])
+
+
+def test_two_calls_at_once(bpa):
+    """Two streams, a workspace each: the answers of calls made one after the other."""
+    cs = [make_step(np.random.default_rng(19 + i), [900, 300], [1, 2], 8, 2, 128, 128, 64) for i in range(2)]
+    ts = [on_gpu(c, torch.bfloat16) for c in cs]
+    want = [bpa.bpa_cache_attn(*t, max_q=2) for t in ts]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        got = [bpa.bpa_cache_attn(*t, max_q=2, stream=s) for t, s in zip(ts, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
