@@ -88,13 +88,15 @@ def append(x, slots, codes, scale):
 
 
 def attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_lens, cu_q, *, causal=True, window=(-1, -1),
-              scale=None, sink=None):
-    """q [T, Hq, d] float64 over the cache.  Returns (o, m, l); rows behind cu_q[-1] are NaN."""
+              scale=None, sink=None, heaviest=False):
+    """q [T, Hq, d] float64 over the cache.  Returns (o, m, l); rows behind cu_q[-1] are NaN.
+    heaviest: also the largest softmax weight times v scale of each row, [T, Hq, 1]."""
     T, Hq, d = q.shape
     Hkv, P, dv = k_codes.shape[1], k_codes.shape[2], v_codes.shape[3]
     val = e4m3_values()
     scale = d ** -0.5 if scale is None else scale
     o, m, l = np.full((T, Hq, dv), np.nan), np.full((Hq, T), np.nan), np.full((Hq, T), np.nan)
+    heavy = np.zeros((T, Hq, 1))
     wl, wr = window
     for r in range(len(kv_lens)):
         L, a, b = int(kv_lens[r]), int(cu_q[r]), int(cu_q[r + 1])
@@ -123,4 +125,6 @@ def attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_lens, cu_q, *, ca
                 w = np.exp(z - top)
                 den = w.sum() + (np.exp(float(sink[h]) - top) if sink is not None else 0)
                 o[t, h], m[h, t], l[h, t] = (w @ V[ok]) / den, top, den
-    return o, m, l
+                if w.size:
+                    heavy[t, h] = (w * v_scale[pages, g].astype(np.float64).repeat(P)[:L][ok]).max() / den
+    return (o, m, l, heavy) if heaviest else (o, m, l)

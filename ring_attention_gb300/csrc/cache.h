@@ -77,4 +77,15 @@ cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_cache_attn_simt(const CacheAttnArgs& a, cudaStream_t s);   // any shape
 
+// Matrix-instruction kernels for few rows: head dims in steps of 16 up to 256, pages of 16, 32 or a
+// multiple of 64 tokens; they read the cache through tensor maps (channel, token, head, page) with
+// boxes of `cols_k` / `cols_v` channels and `rows` tokens.
+struct CacheBox {
+    int cols_k, cols_v, rows;
+};
+bool cache_attn_mma_supported(const CacheAttnArgs& a);
+size_t cache_attn_mma_workspace(const CacheAttnArgs& a);
+CacheBox cache_attn_mma_box(const CacheAttnArgs& a);
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, cudaStream_t s);
+
 }  // namespace bpa

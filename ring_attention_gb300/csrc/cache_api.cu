@@ -82,6 +82,39 @@ bpa_status check_cache_pointers(const bpa_cache_desc* c) {
     return BPA_OK;
 }
 
+// A cache as a 4-D map (channel, token, head, page) of bytes; false where its layout does not suit TMA
+// (16-byte aligned base, strides in multiples of 16 bytes).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool make_cache_map(CUtensorMap* map, const uint8_t* base, const CacheAttnArgs& a, int channels, const int64_t st[3],
+                    int box_cols, int box_rows) {
+    static const EncodeTiledFn enc = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+    }();
+    if (!enc || (reinterpret_cast<uintptr_t>(base) & 15)) return false;
+    const int extent[3] = {a.P, a.Hkv, a.num_pages};
+    const int64_t given[3] = {st[2], st[1], st[0]};
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(a.P),
+                          static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.num_pages)};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        const int64_t s = extent[i] == 1 ? 16 : given[i];   // a dimension of extent 1 never steps
+        if (s < 16 || s % 16 || s >= int64_t{1} << 40) return false;
+        strides[i] = static_cast<cuuint64_t>(s);
+    }
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1, 1};
+    cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bpa_status make_attn(const bpa_cache_desc* c, const bpa_cache_batch* b, CacheAttnArgs& a) {
     int dv = 0;
     bpa_status st = check_cache(c, dv);
@@ -211,7 +244,7 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
 size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cache_batch* batch) {
     CacheAttnArgs a;
     if (make_attn(cache, batch, a) != BPA_OK) return 0;
-    return kHeader;
+    return cache_attn_mma_workspace(a);
 }
 
 bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* batch, void* o, float* m, float* l,
@@ -223,12 +256,20 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
     if (!a.table || !a.kv_lens || !a.cu_q || (a.T && (!a.q || !o)))
         return fail(BPA_ERR_INVALID_ARG, "q, o, page_table, kv_lens or cu_q is NULL");
     if (!m != !l) return fail(BPA_ERR_INVALID_ARG, "m and l: both or neither");
-    if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
+    if ((st = check_ws(workspace, workspace_bytes, cache_attn_mma_workspace(a))) != BPA_OK) return st;
     a.o = o;
     a.m = m;
     a.l = l;
     a.status = static_cast<uint32_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.T > 0 && cache_attn_mma_supported(a)) {
+        const CacheBox box = cache_attn_mma_box(a);
+        CUtensorMap maps[2];
+        if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows) &&
+            make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows))
+            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), s),
+                               "cache attention launch");
+    }
     st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
     if (st != BPA_OK || a.T == 0) return st;
     return cuda_status(launch_cache_attn_simt(a, s), "cache attention launch");

@@ -8,6 +8,9 @@ with A = sum p |v| / l (the same attention over |v|) and Z = the largest sum_c |
   * each weight moves by dz relatively, in the numerator and in the denominator, and is rounded to
     16 bits for the product with v: half a bf16 step, 2^-8 (float32 paths keep two halves: 2^-21);
   * sums over n keys in float32: n 2^-23;
+  * weights are fp16 numbers with the row's largest (weight times v scale, H) at 2^9 or more: fp16's
+    smallest step is 2^-24, so each of the n weights is off by at most 2^-25 = 2^-34 of the largest,
+    whatever its own size, times |v| <= 448: n 2^-34 448 H;
   * the output is rounded once: 2^-8 |o| in bf16, 2^-24 |o| in float32.
 """
 import numpy as np
@@ -282,7 +285,7 @@ def on_gpu(c, dtype, nhd=False):
 def check_attention(c, dtype, o, m, l, rows=None, **kw):
     q = as_dtype(c["q"], dtype)[1]
     args = (c["kc"], c["vc"] & 0x7F, c["ks"], c["vs"], c["table"], c["kv"], c["cu"])
-    A = ora.attention(q, *args, **kw)[0]
+    A, _, _, H = ora.attention(q, *args, heaviest=True, **kw)
     wo, wm, wl = ora.attention(q, c["kc"], c["vc"], *args[2:], **kw)
     d, n = q.shape[2], int(max(c["kv"].max(), 1))
     scale = kw.get("scale") or d ** -0.5
@@ -295,7 +298,9 @@ def check_attention(c, dtype, o, m, l, rows=None, **kw):
     valid = ~np.isnan(wl[0])
     go, gm, gl = f64(o)[valid], f64(m)[:, valid], f64(l)[:, valid]
     wo, A, wm, wl = wo[valid], A[valid], wm[:, valid], wl[:, valid]
-    assert (np.abs(go - wo) <= half * np.abs(wo) + (2 * dz + weight + n * 2.0 ** -23) * A * (1 + half)).all()
+    off = (2 * dz + weight + n * 2.0 ** -23) * A + n * 2.0 ** -34 * 448 * H[valid]
+    bad = ~(np.abs(go - wo) <= half * np.abs(wo) + off * (1 + half))
+    assert not bad.any(), f"{bad.sum()} of {bad.size} outputs, the first {go[bad][0]} for {wo[bad][0]}, A {A[bad][0]}"
     np.testing.assert_array_equal(np.isneginf(gm), np.isneginf(wm))
     fin = np.isfinite(wm)
     assert (np.abs(gm[fin] - wm[fin]) <= dz + 2.0 ** -22 * np.abs(wm[fin])).all()
