@@ -1,28 +1,30 @@
 // cache_attn_mma.cu - attention of few query rows over the paged 8-bit cache (generation, drafts).
 //
-// An item is 16 RT query rows (row = token-in-request * G + q head in the group, so every row
+// An item is up to 64 query rows (row = token-in-request * G + q head in the group, so every row
 // reads the same keys) of one request and kv head; its keys are walked in tiles of 64.  Codes are
-// exact in fp16, so both products run on fp16 matrix instructions with float32 sums:
-//   S = Q K^T   with each row of Q scaled by a power of two into fp16's range (bf16 rows lose
+// exact in fp16, so both products run on fp16 matrix instructions with float32 sums, keys and
+// channels on the side of 16 and query rows on the side of 8 (a group of few heads wastes little):
+//   S^T = K Q^T  with each row of Q scaled by a power of two into fp16's range (bf16 rows lose
 //               nothing above 2^-22 of the row's largest value; float32 rows go in as two halves);
 //   z = S * (k scale of the page) * (row's scale), in log2 units; m and l from exp2(z - m), float32;
-//   O += W V    with W = exp2(z + log2(v scale) - M + 9) in fp16, M the running maximum of
+//   O^T += V^T W^T  with W = exp2(z + log2(v scale) - M + 9) in fp16, M the running maximum of
 //               z + log2(v scale): the weight that a page's codes really have, so pages whose scales
 //               lie far apart keep their precision.  M moves only when it grows by more than 6 (W <=
 //               2^15); a weight below 2^-33 of the largest is dropped.  float32: W as two halves.
 //
-// Bounded by the bytes of K and V.  So the CTAs are persistent (two per SM) and each takes an equal
-// share of all tiles of all items, whatever the lengths; a share may begin and end inside an item.
-// Pieces of items go to the workspace as (m, l, O) and a second, small launch joins them in
-// ascending order (its launch overlaps the first kernel: programmatic dependent launch), so nothing
-// is added in an order that changes.  Per CTA one warp copies tiles by TMA (a page's rows at a
-// time, swizzled) into a ring of stages and passes the page's scales beside them; four warps
-// take 16 keys of a tile each (RT = 1), or each row tile's share of them.
+// Bounded by the bytes of K and V.  So the CTAs are persistent and each takes an equal share of all
+// tiles of all items, whatever the lengths (an item counts kExtra tiles more, about what its start
+// and end cost); a share may begin and end inside an item.  Pieces of items go to the workspace as
+// (m, l, O) and a second, small launch joins them in ascending order (its launch overlaps the first
+// kernel: programmatic dependent launch), so nothing is added in an order that changes.  Per CTA one
+// warp copies tiles by TMA (a page's rows at a time, swizzled) into a ring of stages and passes the
+// page's scales beside them; four warps take 16 keys of a tile each, or more of the keys for a part
+// of the rows.
 //
 // Layouts without bank conflicts or shuffles: channels are permuted between Q and K so that a lane's
 // 16 consecutive bytes of a key feed four products, and keys (n odd: n ^ 4 within eight) so that
-// the score fragment is the weight fragment and V's rows are read 16 bytes at a time; pairs of V's
-// rows are interleaved by byte permutes on the way to fp16.
+// V's rows are read 16 bytes at a time; pairs of V's rows are interleaved by byte permutes on the way
+// to fp16, and W turns from a result into an operand by two 8 x 8 transpositions.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -38,6 +40,7 @@ namespace {
 constexpr int kTile = 64;             // keys per stage
 constexpr int kNW = 4;                // consumer warps
 constexpr int kThreads = 32 * (kNW + 1);
+constexpr int kExtra = 1;             // tiles that an item's start and end count for in a share
 constexpr int kBatch = 8;             // tiles whose page ids and scales are fetched together
 constexpr float kOff = 9.f;           // log2 of the largest fp16 weight right after M moved
 constexpr float kLazy = 6.f;          // M moves when it grows by more
@@ -53,30 +56,36 @@ static_assert(sizeof(Rec) == 48, "record");
 
 struct Work {
     CacheAttnArgs a;
-    int RT, ctas;
+    int rows_per, RT, ctas;           // rows of an item, row tiles of 8 NT, CTAs
     int vec_o;                        // o takes 16-byte stores
     Rec* recs;                        // [ctas]
-    float2* ml;                       // [2 ctas][16 RT] (m in log2 units, l)
-    float* part;                      // [2 ctas][16 RT][DVP] relative to m
+    float2* ml;                       // [2 ctas][rows_per] (m in log2 units, l)
+    float* part;                      // [2 ctas][rows_per][DVP] relative to m
 };
 
 struct Meta {
     int key0, len, n, row0, hk, i0, flags, pad;
     float ks[4], vs[4];               // scales of the tile's four 16-key chunks
 };
-enum { F_FIRST = 1, F_LAST = 2, F_LEAD = 4, F_TRAIL = 8 };
+enum { F_FIRST = 1, F_LAST = 2, F_LEAD = 4, F_TRAIL = 8, F_END = 16 };
 
-template <int DP, int DVP, bool SPLIT>
+// DP, DVP: head dims of k and v padded to 64, 128 or 256; NT: query rows of a warp / 8; SPLIT: float32
+template <int DP, int DVP, int NT, bool SPLIT>
 struct Cfg {
     static constexpr int RBK = DP < 128 ? DP : 128, RBV = DVP < 128 ? DVP : 128;   // bytes of a swizzled row
     static constexpr int HK = DP / RBK, HV = DVP / RBV;                            // 128-byte halves
     static constexpr int K_BYTES = kTile * DP, V_BYTES = kTile * DVP, STAGE = K_BYTES + V_BYTES;
-    static constexpr bool Q_REGS = !SPLIT && DP <= 128;
-    static constexpr int QF = DP / 16 * 512 * (SPLIT ? 2 : 1);                     // fragments of a row tile
-    static constexpr int MERGE = 2 * (16 * DVP + 16 * 4) * 4;                      // two warps' states
-    static constexpr int NS = DP + DVP <= 128 ? 8 : DP + DVP <= 192 ? 6 : DP + DVP <= 256 ? (SPLIT ? 4 : 5) : 4;
-    static constexpr int OCC = DP <= 128 ? 2 : 1;
-    static int smem(int RT) { return 1024 + NS * STAGE + MERGE + NS * (int)sizeof(Meta) + 256 + (Q_REGS ? 0 : RT * QF); }
+    static constexpr bool Q_REGS = !SPLIT && DP * NT <= 256;
+    static constexpr int QF = DP / 16 * NT * 256 * (SPLIT ? 2 : 1);                // fragments of a row tile
+    static constexpr int QS = Q_REGS ? 0 : QF * (NT == 1 ? 1 : 4);                 // ... of all row tiles
+    static constexpr int STATE = 8 * NT * DVP + 8 * NT * 4;                        // floats of a warp's state
+    static constexpr int MERGE = 2 * STATE * 4;
+    static constexpr int OCC = DP <= 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 1);
+    static constexpr int FIXED = 1024 + MERGE + 256 + QS;
+    static constexpr int FIT = (233472 / OCC - 1024 - 128 - FIXED) / (STAGE + (int)sizeof(Meta));
+    static constexpr int NS = FIT > 8 ? 8 : FIT;
+    static constexpr int SMEM = FIXED + NS * (STAGE + (int)sizeof(Meta));
+    static_assert(NS >= 2, "stages");
 };
 
 BPA_DEV uint32_t cvt2(uint32_t two) {      // two e4m3 codes -> fp16 pair, exact
@@ -90,27 +99,22 @@ BPA_DEV uint32_t cvt2_hi(uint32_t four) {
     return h;
 }
 BPA_DEV void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the transpose of an 8 x 8 matrix of fp16 in fragment layout
+BPA_DEV uint32_t transposed(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 BPA_DEV uint32_t h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 BPA_DEV float2 h2f(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-BPA_DEV uint4 lds128(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
-BPA_DEV uint2 lds64(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-    return v;
-}
 // byte offset of byte `col` of row `row` in a TMA-swizzled tile with rows of RB (64 or 128) bytes
 template <int RB>
 BPA_DEV uint32_t swz(int row, int col) {
@@ -134,18 +138,18 @@ BPA_DEV Tiles tiles_of(const CacheAttnArgs& a, const Req& q, int rg, int rows_pe
     if (lo > hi) return {0, 1};
     return {lo / kTile, hi / kTile - lo / kTile + 1};
 }
-BPA_DEV long long tiles_of_request(const CacheAttnArgs& a, const Req& q, int rows_per) {
+BPA_DEV long long cost_of_request(const CacheAttnArgs& a, const Req& q, int rows_per) {
     if (q.n == 0) return 0;
     long long n = 0;
     const int groups = (q.n * a.G + rows_per - 1) / rows_per;
-    for (int rg = 0; rg < groups; ++rg) n += tiles_of(a, q, rg, rows_per).n;
+    for (int rg = 0; rg < groups; ++rg) n += tiles_of(a, q, rg, rows_per).n + kExtra;
     return n * a.Hkv;
 }
 
-template <int DP, int DVP, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
+template <int DP, int DVP, int NT, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     k_cache_attn_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Work w) {
-    using C = Cfg<DP, DVP, SPLIT>;
+    using C = Cfg<DP, DVP, NT, SPLIT>;
     using E = typename std::conditional<SPLIT, float, __nv_bfloat16>::type;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
 
     const CacheAttnArgs& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-    const int rows_per = 16 * w.RT;
+    const int rows_per = w.rows_per;
     Rec* rec = w.recs + cta;
     uint32_t* status = &rec->flags;
     if (threadIdx.x == 0) {
@@ -182,11 +186,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- this CTA's share of the tiles: [begin, end) of the running sum over the requests
+    // ---- this CTA's share: [begin, end) of the running sum of tiles and kExtra over the items
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min(a.R, static_cast<int>(threadIdx.x) * per),
               r1 = min(a.R, r0 + per);
     long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += tiles_of_request(a, request_of(a, r), rows_per);
+    for (int r = r0; r < r1; ++r) mine += cost_of_request(a, request_of(a, r), rows_per);
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -201,13 +205,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
         total += s_scan[i];
     }
     before += x - mine;
-    // with fewer tiles than CTAs the first ones take one each, so the pieces of an item lie side by side
+    // a share is never empty among the CTAs that take part, so the pieces of an item lie side by side
     const int parts = static_cast<int>(min(total, static_cast<long long>(w.ctas)));
     const long long begin = cta < parts ? total * cta / parts : total, end = cta < parts ? total * (cta + 1) / parts : total;
     if (begin < end && begin >= before && begin < before + mine) {
         long long at = before;
         for (int r = r0; r < r1; ++r) {
-            const long long n = tiles_of_request(a, request_of(a, r), rows_per);
+            const long long n = cost_of_request(a, request_of(a, r), rows_per);
             if (begin < at + n) {
                 s_r = r;
                 s_off = begin - at;
@@ -232,21 +236,23 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
             if (rq.bad && lane == 0) report(status, ST_CHECK, 0xCD1);
             int groups = (rq.n * a.G + rows_per - 1) / rows_per;
             long long off = s_off;
-            const long long per_head = tiles_of_request(a, rq, rows_per) / a.Hkv;
+            const long long per_head = cost_of_request(a, rq, rows_per) / a.Hkv;
             int hk = static_cast<int>(off / per_head), rg = 0;
             off -= hk * per_head;
             Tiles tl = tiles_of(a, rq, 0, rows_per);
-            while (off >= tl.n) {
-                off -= tl.n;
+            while (off >= tl.n + kExtra) {
+                off -= tl.n + kExtra;
                 tl = tiles_of(a, rq, ++rg, rows_per);
             }
-            int t = static_cast<int>(off);
             while (left > 0 && ok) {
-                const int te = static_cast<int>(min(static_cast<long long>(tl.n), t + left));
+                // [off, to) of the item's cost; its first kExtra are no tiles
+                const long long to = min(static_cast<long long>(tl.n + kExtra), off + left);
+                const int t = max(static_cast<int>(off) - kExtra, 0), te = max(static_cast<int>(to) - kExtra, 0);
                 const bool lead = t > 0, trail = te < tl.n;
                 const int i0 = rg * rows_per;
                 const int kind = lead ? F_LEAD : trail ? F_TRAIL : 0;
-                if (lead) {
+                if (t == te) {
+                } else if (lead) {
                     out.lead = 1;
                     out.lead_ends = !trail;
                 } else if (trail) {
@@ -314,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
                         }
                     }
                 }
-                left -= te - t;
-                t = 0;
+                left -= to - off;
+                off = 0;
                 if (left > 0) {        // the next item: row group, head, request
                     if (++rg == groups) {
                         rg = 0;
@@ -335,6 +341,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
                     }
                     tl = tiles_of(a, rq, rg, rows_per);
                 }
+            }
+        }
+        if (ok) {                          // one more stage, without a tile: the end
+            ok = __all_sync(0xffffffffu, mbar_wait(EMPTY(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD2));
+            if (ok && lane == 0) {
+                meta[stage].flags = F_END;
+                mbar_arrive(FULL(stage));
             }
         }
         // the copies in flight end before the CTA does: the consumers wait for them, and after a timeout
@@ -358,11 +371,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
     // ---- consumers
     const int rt = warp % w.RT, slices = kNW / w.RT, slice = warp / w.RT;
     const int g = lane >> 2, j = lane & 3;
-    const uint32_t my_q = q_at + rt * C::QF + lane * 16;
-    uint32_t qf[C::Q_REGS ? DP / 16 : 1][4];
-    float acc[DVP / 8][4];
-    float m0, m1, M0, M1, l0, l1, f0 = 0.f, f1 = 0.f;
-    int lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, in_lo = 0, in_hi = 0, any_lo = 0, any_hi = 0;
+    uint8_t* my_q = smem + (q_at - sb) + rt * C::QF + lane * 8;
+    uint32_t qf[C::Q_REGS ? DP / 16 : 1][NT][2];
+    float acc[DVP / 16][NT][4];
+    // rows 2j + e of n-tile nt: running (m, l) of this lane's keys, M of the row, its factor and keys
+    float m[NT][2], l[NT][2], M[NT][2], f[NT][2];
+    int lo[NT][2], hi[NT][2], in_lo = 0, in_hi = 0, any_lo = 0, any_hi = 0;
     int stage = 0;
     uint32_t phase = 0, join_phase = 0;
     // a barrier of the consumers whose wait is bounded
@@ -373,29 +387,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
         join_phase ^= 1;
         return __all_sync(0xffffffffu, met) != 0;
     };
-    for (long long t = begin; t < end; ++t) {
+    for (;;) {
         if (!__all_sync(0xffffffffu, mbar_wait(FULL(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD4))) return;
         const Meta* mt = meta + stage;
         const int flags = mt->flags, key0 = mt->key0, len = mt->len;
+        if (flags & F_END) return;
         if (flags & F_FIRST) {
-            // ---- a new item: this warp's 16 rows of q as fp16 fragments, scaled by a power of two
+            // ---- a new item: this warp's rows of q as fp16 fragments, scaled by a power of two
             const Req rq = {mt->row0, mt->n, len, false};
-            const int hk = mt->hk, nr = rq.n * a.G;
-            float fac[2];
+            const int hk = mt->hk, nr = rq.n * a.G, first = mt->i0 + rt * 8 * NT;
+            in_lo = any_hi = 0;
+            in_hi = any_lo = INT_MAX;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int ri = mt->i0 + rt * 16 + g + 8 * half;
+            for (int nt = 0; nt < NT; ++nt) {
+                const int ri = first + 8 * nt + g;          // the row whose channels this lane loads
                 const bool there = ri < nr;
                 const int tok = there ? ri / a.G : 0;
-                int lo = 0, hi = INT_MAX;          // a row that is not there masks nothing (q = 0: z = 0)
-                if (there) row_keys(a, rq, tok, lo, hi);
-                if (half == 0) {
-                    lo0 = lo;
-                    hi0 = hi;
-                } else {
-                    lo1 = lo;
-                    hi1 = hi;
-                }
                 const E* q = static_cast<const E*>(a.q) + static_cast<int64_t>(rq.row0 + tok) * a.qs[0] +
                              static_cast<int64_t>(hk * a.G + (there ? ri - tok * a.G : 0)) * a.qs[1];
                 float v[DP / 16][4];
@@ -412,151 +419,159 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // largest value into [2^7, 2^8); 0 and values that are not finite stay as they are
-                const int e = top > 0.f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 - 7 : 0;
-                const float up = __uint_as_float(static_cast<uint32_t>(127 - min(max(e, -126), 126)) << 23);
-                fac[half] = __uint_as_float(static_cast<uint32_t>(127 + min(max(e, -126), 126)) << 23) * a.scale * kLog2e;
+                int x = top > 0.f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 - 7 : 0;
+                x = min(max(x, -126), 126);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+                const float fac = __uint_as_float(static_cast<uint32_t>(127 + x) << 23) * a.scale * kLog2e;
 #pragma unroll
                 for (int s = 0; s < DP / 16; ++s) {
                     const float x0 = v[s][0] * up, x1 = v[s][1] * up, x2 = v[s][2] * up, x3 = v[s][3] * up;
                     const uint32_t p0 = h2(x0, x1), p1 = h2(x2, x3);
                     if constexpr (C::Q_REGS) {
-                        qf[s][half] = p0;
-                        qf[s][2 + half] = p1;
+                        qf[s][nt][0] = p0;
+                        qf[s][nt][1] = p1;
                     } else {
-                        const uint32_t at = my_q + s * 512 * (SPLIT ? 2 : 1) + half * 4;
-                        st_shared_u32(at, p0);
-                        st_shared_u32(at + 8, p1);
+                        uint2* at = reinterpret_cast<uint2*>(my_q + (s * NT + nt) * 256 * (SPLIT ? 2 : 1));
+                        at[0] = make_uint2(p0, p1);
                         if (SPLIT) {
                             const float2 y0 = h2f(p0), y1 = h2f(p1);
-                            st_shared_u32(at + 512, h2(x0 - y0.x, x1 - y0.y));
-                            st_shared_u32(at + 520, h2(x2 - y1.x, x3 - y1.y));
+                            at[32] = make_uint2(h2(x0 - y0.x, x1 - y0.y), h2(x2 - y1.x, x3 - y1.y));
                         }
                     }
                 }
-            }
-            f0 = fac[0];
-            f1 = fac[1];
-            in_lo = max(lo0, lo1);                 // keys that no row masks, keys that some row allows
-            in_hi = min(hi0, hi1);
-            any_lo = min(lo0, lo1);
-            any_hi = max(hi0, hi1);
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
+                for (int e = 0; e < 2; ++e) {
+                    f[nt][e] = __shfl_sync(0xffffffffu, fac, (2 * j + e) * 4);
+                    const int r2 = first + 8 * nt + 2 * j + e;
+                    lo[nt][e] = 0;                           // a row that is not there masks nothing (z = 0)
+                    hi[nt][e] = INT_MAX;
+                    if (r2 < nr) {
+                        row_keys(a, rq, r2 / a.G, lo[nt][e], hi[nt][e]);
+                        any_lo = min(any_lo, lo[nt][e]);
+                        any_hi = max(any_hi, hi[nt][e]);
+                    }
+                    in_lo = max(in_lo, lo[nt][e]);           // keys that no row masks, keys that some row allows
+                    in_hi = min(in_hi, hi[nt][e]);
+                    m[nt][e] = M[nt][e] = -INFINITY;
+                    l[nt][e] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
                 in_lo = max(in_lo, __shfl_xor_sync(0xffffffffu, in_lo, o));
                 in_hi = min(in_hi, __shfl_xor_sync(0xffffffffu, in_hi, o));
                 any_lo = min(any_lo, __shfl_xor_sync(0xffffffffu, any_lo, o));
                 any_hi = max(any_hi, __shfl_xor_sync(0xffffffffu, any_hi, o));
             }
-            any_hi = min(any_hi, len - 1);
+            any_hi = first < nr ? min(any_hi, len - 1) : -1;
             in_hi = min(in_hi, len - 1);
-            if (mt->i0 + rt * 16 >= nr) any_hi = -1;   // no rows at all
-            m0 = m1 = M0 = M1 = -INFINITY;
-            l0 = l1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < DVP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            for (int i = 0; i < DVP / 16; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.f;
             __syncwarp();
         }
-        const uint32_t kt = sb + stage * C::STAGE, vt = kt + C::K_BYTES;
+        const uint8_t *kt = smem + stage * C::STAGE, *vt = kt + C::K_BYTES;
         for (int ch = slice; ch < 4; ch += slices) {
             const int base = key0 + 16 * ch;
             if (base > any_hi || base + 15 < any_lo) continue;
-            // ---- S = Q K^T for 16 keys; n of a fragment is key n (even) or n ^ 4 (odd) of its eight
+            // ---- S^T = K Q^T for 16 keys: row r of a fragment is key r (even) or r ^ 4 (odd) of its eight
             const int kr = (g & 1) ? (g ^ 4) : g;
-            float s[2][2][4];
+            float s[NT][2][4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) (&s[0][0][0])[i] = 0.f;
+            for (int i = 0; i < 8 * NT; ++i) (&s[0][0][0])[i] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < DP / 64; ++kk) {
+                const uint8_t* kp = kt + (kk >> 1) * kTile * C::RBK;
+                const uint4 ka = *reinterpret_cast<const uint4*>(kp + swz<C::RBK>(16 * ch + kr, (kk & 1) * 64 + 16 * j));
+                const uint4 kb = *reinterpret_cast<const uint4*>(kp + swz<C::RBK>(16 * ch + 8 + kr, (kk & 1) * 64 + 16 * j));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint4 kv = lds128(kt + (kk >> 1) * kTile * C::RBK +
-                                            swz<C::RBK>(16 * ch + 8 * nt + kr, (kk & 1) * 64 + 16 * j));
-                    const uint32_t word[4] = {kv.x, kv.y, kv.z, kv.w};
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t fr[4] = {cvt2(wa[u]), cvt2(wb[u]), cvt2_hi(wa[u]), cvt2_hi(wb[u])};
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t b0 = cvt2(word[u]), b1 = cvt2_hi(word[u]);
+                    for (int nt = 0; nt < NT; ++nt) {
                         if constexpr (C::Q_REGS) {
-                            mma(s[nt][u & 1], qf[kk * 4 + u], b0, b1);
+                            mma(s[nt][u & 1], fr, qf[kk * 4 + u][nt][0], qf[kk * 4 + u][nt][1]);
                         } else {
-                            const uint32_t at = my_q + (kk * 4 + u) * 512 * (SPLIT ? 2 : 1);
-                            const uint4 qa = lds128(at);
-                            const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w};
-                            mma(s[nt][u & 1], fa, b0, b1);
+                            const uint2* at = reinterpret_cast<const uint2*>(my_q + ((kk * 4 + u) * NT + nt) * 256 * (SPLIT ? 2 : 1));
+                            const uint2 qa = at[0];
+                            mma(s[nt][u & 1], fr, qa.x, qa.y);
                             if (SPLIT) {
-                                const uint4 qb = lds128(at + 512);
-                                const uint32_t fb[4] = {qb.x, qb.y, qb.z, qb.w};
-                                mma(s[nt][u & 1], fb, b0, b1);
+                                const uint2 qb = at[32];
+                                mma(s[nt][u & 1], fr, qb.x, qb.y);
                             }
                         }
                     }
                 }
             }
-            // ---- scores, maxima
+            // ---- scores; z[nt][e], z[nt][2 + e]: row 2j + e, keys kr and 8 + kr
             const float ks = mt->ks[ch], vs = mt->vs[ch];
-            const float a0 = f0 * ks, a1 = f1 * ks;
-            float z[2][4];
+            const bool edge = base < in_lo || base + 15 > in_hi;
+            const float lv = __log2f(vs);
+            float z[NT][4], u[NT][2];
+            bool move = false;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                z[nt][0] = (s[nt][0][0] + s[nt][1][0]) * a0;
-                z[nt][1] = (s[nt][0][1] + s[nt][1][1]) * a0;
-                z[nt][2] = (s[nt][0][2] + s[nt][1][2]) * a1;
-                z[nt][3] = (s[nt][0][3] + s[nt][1][3]) * a1;
-            }
-            if (base < in_lo || base + 15 > in_hi) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int ka = base + 8 * nt + 2 * j, kb = base + 8 * nt + ((2 * j + 1) ^ 4);
-                    const bool la = ka >= len, lb = kb >= len;
-                    if (la || ka < lo0 || ka > hi0) z[nt][0] = -INFINITY;
-                    if (lb || kb < lo0 || kb > hi0) z[nt][1] = -INFINITY;
-                    if (la || ka < lo1 || ka > hi1) z[nt][2] = -INFINITY;
-                    if (lb || kb < lo1 || kb > hi1) z[nt][3] = -INFINITY;
+                for (int e = 0; e < 2; ++e) {
+                    const float fk = f[nt][e] * ks;
+                    float z0 = (s[nt][0][e] + s[nt][1][e]) * fk, z1 = (s[nt][0][2 + e] + s[nt][1][2 + e]) * fk;
+                    if (edge) {
+                        const int k0 = base + kr, k1 = base + 8 + kr;
+                        if (k0 >= len || k0 < lo[nt][e] || k0 > hi[nt][e]) z0 = -INFINITY;
+                        if (k1 >= len || k1 < lo[nt][e] || k1 > hi[nt][e]) z1 = -INFINITY;
+                    }
+                    z[nt][e] = z0;
+                    z[nt][2 + e] = z1;
+                    // m, l of this lane's keys (the row's eight lanes are joined at the end of the item)
+                    const float c = fmaxf(z0, z1), n = fmaxf(m[nt][e], c), ref = n == -INFINITY ? 0.f : n;
+                    l[nt][e] = l[nt][e] * ex2(m[nt][e] - ref) + (ex2(z0 - ref) + ex2(z1 - ref));
+                    m[nt][e] = n;
+                    u[nt][e] = c + lv;
+                    move |= u[nt][e] > M[nt][e] + kLazy;
                 }
             }
-            float c0 = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
-            float c1 = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
-            c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, 1));
-            c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, 1));
-            c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, 2));
-            c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, 2));
-            // ---- m, l
-            const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
-            const float e0 = n0 == -INFINITY ? 0.f : n0, e1 = n1 == -INFINITY ? 0.f : n1;
-            l0 = l0 * ex2(m0 - e0) + ((ex2(z[0][0] - e0) + ex2(z[0][1] - e0)) + (ex2(z[1][0] - e0) + ex2(z[1][1] - e0)));
-            l1 = l1 * ex2(m1 - e1) + ((ex2(z[0][2] - e1) + ex2(z[0][3] - e1)) + (ex2(z[1][2] - e1) + ex2(z[1][3] - e1)));
-            m0 = n0;
-            m1 = n1;
             if (!(vs > 0.f)) continue;             // a page of zeros: nothing to add (its scale is 0)
             // ---- weights in fp16, relative to M
-            const float lv = __log2f(vs), u0 = c0 + lv, u1 = c1 + lv;
-            if (__any_sync(0xffffffffu, u0 > M0 + kLazy || u1 > M1 + kLazy)) {
-                const float N0 = fmaxf(M0, u0), N1 = fmaxf(M1, u1);
-                const float x0 = M0 == -INFINITY ? 0.f : ex2(M0 - N0), x1 = M1 == -INFINITY ? 0.f : ex2(M1 - N1);
+            if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-                for (int i = 0; i < DVP / 8; ++i) {
-                    acc[i][0] *= x0;
-                    acc[i][1] *= x0;
-                    acc[i][2] *= x1;
-                    acc[i][3] *= x1;
-                }
-                M0 = N0;
-                M1 = N1;
-            }
-            const float t0 = (M0 == -INFINITY ? 0.f : M0 - lv) - kOff, t1 = (M1 == -INFINITY ? 0.f : M1 - lv) - kOff;
-            uint32_t wf[4], wl[4];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float x[2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const float y0 = ex2(z[nt][0] - t0), y1 = ex2(z[nt][1] - t0), y2 = ex2(z[nt][2] - t1),
-                            y3 = ex2(z[nt][3] - t1);
-                wf[2 * nt] = h2(y0, y1);
-                wf[2 * nt + 1] = h2(y2, y3);
-                if (SPLIT) {
-                    const float2 r0 = h2f(wf[2 * nt]), r1 = h2f(wf[2 * nt + 1]);
-                    wl[2 * nt] = h2(y0 - r0.x, y1 - r0.y);
-                    wl[2 * nt + 1] = h2(y2 - r1.x, y3 - r1.y);
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) u[nt][e] = fmaxf(u[nt][e], __shfl_xor_sync(0xffffffffu, u[nt][e], o));
+                        const float N = fmaxf(M[nt][e], u[nt][e]);
+                        x[e] = M[nt][e] == -INFINITY ? 0.f : ex2(M[nt][e] - N);
+                        M[nt][e] = N;
+                    }
+#pragma unroll
+                    for (int i = 0; i < DVP / 16; ++i) {
+                        acc[i][nt][0] *= x[0];
+                        acc[i][nt][1] *= x[1];
+                        acc[i][nt][2] *= x[0];
+                        acc[i][nt][3] *= x[1];
+                    }
                 }
             }
-            // ---- O += W V: this lane's four keys, CV consecutive channels
+            uint32_t wf[NT][2], wl[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float t0 = (M[nt][0] == -INFINITY ? 0.f : M[nt][0] - lv) - kOff;
+                const float t1 = (M[nt][1] == -INFINITY ? 0.f : M[nt][1] - lv) - kOff;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float y0 = ex2(z[nt][2 * k] - t0), y1 = ex2(z[nt][2 * k + 1] - t1);
+                    const uint32_t hh = h2(y0, y1);
+                    wf[nt][k] = transposed(hh);
+                    if (SPLIT) {
+                        const float2 r = h2f(hh);
+                        wl[nt][k] = transposed(h2(y0 - r.x, y1 - r.y));
+                    }
+                }
+            }
+            // ---- O^T += V^T W^T: this lane's four keys, CV consecutive channels (two rows of a fragment each)
             constexpr int CV = (DVP < 128 ? DVP : 128) / 8;          // 8 or 16
             const int key[4] = {2 * j, (2 * j + 1) ^ 4, 8 + 2 * j, 8 + ((2 * j + 1) ^ 4)};
 #pragma unroll
@@ -564,33 +579,42 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
                 uint32_t v[4][CV / 4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t at = vt + hv * kTile * C::RBV + swz<C::RBV>(16 * ch + key[i], CV * g);
+                    const uint8_t* at = vt + hv * kTile * C::RBV + swz<C::RBV>(16 * ch + key[i], CV * g);
                     if constexpr (CV == 16) {
-                        const uint4 x4 = lds128(at);
+                        const uint4 x4 = *reinterpret_cast<const uint4*>(at);
                         v[i][0] = x4.x;
                         v[i][1] = x4.y;
                         v[i][2] = x4.z;
                         v[i][3] = x4.w;
                     } else {
-                        const uint2 x2 = lds64(at);
+                        const uint2 x2 = *reinterpret_cast<const uint2*>(at);
                         v[i][0] = x2.x;
                         v[i][1] = x2.y;
                     }
+                }
+                if (base + 16 > len) {
                     // slots past the last token may hold anything: their weight is 0, NaN is not
-                    if (base + 16 > len && base + key[i] >= len)
 #pragma unroll
-                        for (int c = 0; c < CV / 4; ++c) v[i][c] = 0;
+                    for (int i = 0; i < 4; ++i)
+                        if (base + key[i] >= len)
+#pragma unroll
+                            for (int c = 0; c < CV / 4; ++c) v[i][c] = 0;
                 }
 #pragma unroll
                 for (int c = 0; c < CV / 4; ++c) {
                     const uint32_t ab0 = __byte_perm(v[0][c], v[1][c], 0x5140), ab1 = __byte_perm(v[0][c], v[1][c], 0x7362);
                     const uint32_t cd0 = __byte_perm(v[2][c], v[3][c], 0x5140), cd1 = __byte_perm(v[2][c], v[3][c], 0x7362);
-                    const uint32_t b0[4] = {cvt2(ab0), cvt2_hi(ab0), cvt2(ab1), cvt2_hi(ab1)};
-                    const uint32_t b1[4] = {cvt2(cd0), cvt2_hi(cd0), cvt2(cd1), cvt2_hi(cd1)};
+                    const uint32_t fa[4] = {cvt2(ab0), cvt2_hi(ab0), cvt2(cd0), cvt2_hi(cd0)};
+                    const uint32_t fb[4] = {cvt2(ab1), cvt2_hi(ab1), cvt2(cd1), cvt2_hi(cd1)};
+                    const int i = hv * (CV / 2) + 2 * c;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        mma(acc[hv * CV + 4 * c + e], wf, b0[e], b1[e]);
-                        if (SPLIT) mma(acc[hv * CV + 4 * c + e], wl, b0[e], b1[e]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma(acc[i][nt], fa, wf[nt][0], wf[nt][1]);
+                        mma(acc[i + 1][nt], fb, wf[nt][0], wf[nt][1]);
+                        if (SPLIT) {
+                            mma(acc[i][nt], fa, wl[nt][0], wl[nt][1]);
+                            mma(acc[i + 1][nt], fb, wl[nt][0], wl[nt][1]);
+                        }
                     }
                 }
             }
@@ -604,104 +628,114 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
         }
         if (!(flags & F_LAST)) continue;
 
-        // ---- the end of this CTA's share of the item: join the warps' slices, in a fixed order
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        // ---- the end of this CTA's share of the item: join the lanes, then the warps' slices, in a fixed order
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    const float x = __shfl_xor_sync(0xffffffffu, m[nt][e], o), y = __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+                    const float n = fmaxf(m[nt][e], x), ref = n == -INFINITY ? 0.f : n;
+                    // the same sum on both lanes, whichever is which
+                    l[nt][e] = __fadd_rn(__fmul_rn(l[nt][e], ex2(m[nt][e] - ref)), __fmul_rn(y, ex2(x - ref)));
+                    m[nt][e] = n;
+                }
         for (int st = slices >> 1; st >= 1; st >>= 1) {
-            float* buf = merge + ((slice & (st - 1)) * w.RT + rt) * (16 * DVP + 64);
+            float* buf = merge + ((slice & (st - 1)) * w.RT + rt) * C::STATE;
             if (slice >= st && slice < 2 * st) {
 #pragma unroll
-                for (int i = 0; i < DVP / 8; ++i)
-                    *reinterpret_cast<float4*>(buf + (i * 32 + lane) * 4) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                if (j == 0) {
-                    float* e = buf + 16 * DVP + g * 8;
-                    e[0] = m0;
-                    e[1] = l0;
-                    e[2] = M0;
-                    e[3] = m1;
-                    e[4] = l1;
-                    e[5] = M1;
-                }
+                for (int i = 0; i < DVP / 16; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        *reinterpret_cast<float4*>(buf + ((i * NT + nt) * 32 + lane) * 4) =
+                            make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+                if (g == 0)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<float4*>(buf + 8 * NT * DVP + (8 * nt + 2 * j + e) * 4) =
+                                make_float4(m[nt][e], l[nt][e], M[nt][e], 0.f);
             }
             if (!consumers_meet()) return;
             if (slice < st) {
-                const float* e = buf + 16 * DVP + g * 8;
-                const float bm0 = e[0], bl0 = e[1], bM0 = e[2], bm1 = e[3], bl1 = e[4], bM1 = e[5];
-                const float n0 = fmaxf(m0, bm0), n1 = fmaxf(m1, bm1);
-                if (n0 != -INFINITY) l0 = l0 * ex2(m0 - n0) + bl0 * ex2(bm0 - n0);
-                else l0 += bl0;
-                if (n1 != -INFINITY) l1 = l1 * ex2(m1 - n1) + bl1 * ex2(bm1 - n1);
-                else l1 += bl1;
-                m0 = n0;
-                m1 = n1;
-                const float N0 = fmaxf(M0, bM0), N1 = fmaxf(M1, bM1);
-                const float x0 = M0 == -INFINITY ? 0.f : ex2(M0 - N0), x1 = M1 == -INFINITY ? 0.f : ex2(M1 - N1);
-                const float y0 = bM0 == -INFINITY ? 0.f : ex2(bM0 - N0), y1 = bM1 == -INFINITY ? 0.f : ex2(bM1 - N1);
 #pragma unroll
-                for (int i = 0; i < DVP / 8; ++i) {
-                    const float4 v = *reinterpret_cast<const float4*>(buf + (i * 32 + lane) * 4);
-                    acc[i][0] = acc[i][0] * x0 + v.x * y0;
-                    acc[i][1] = acc[i][1] * x0 + v.y * y0;
-                    acc[i][2] = acc[i][2] * x1 + v.z * y1;
-                    acc[i][3] = acc[i][3] * x1 + v.w * y1;
+                for (int nt = 0; nt < NT; ++nt) {
+                    float x[2], y[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 b = *reinterpret_cast<const float4*>(buf + 8 * NT * DVP + (8 * nt + 2 * j + e) * 4);
+                        const float n = fmaxf(m[nt][e], b.x), ref = n == -INFINITY ? 0.f : n;
+                        l[nt][e] = l[nt][e] * ex2(m[nt][e] - ref) + b.y * ex2(b.x - ref);
+                        m[nt][e] = n;
+                        const float N = fmaxf(M[nt][e], b.z);
+                        x[e] = M[nt][e] == -INFINITY ? 0.f : ex2(M[nt][e] - N);
+                        y[e] = b.z == -INFINITY ? 0.f : ex2(b.z - N);
+                        M[nt][e] = N;
+                    }
+#pragma unroll
+                    for (int i = 0; i < DVP / 16; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(buf + ((i * NT + nt) * 32 + lane) * 4);
+                        acc[i][nt][0] = acc[i][nt][0] * x[0] + v.x * y[0];
+                        acc[i][nt][1] = acc[i][nt][1] * x[1] + v.y * y[1];
+                        acc[i][nt][2] = acc[i][nt][2] * x[0] + v.z * y[0];
+                        acc[i][nt][3] = acc[i][nt][3] * x[1] + v.w * y[1];
+                    }
                 }
-                M0 = N0;
-                M1 = N1;
             }
             if (!consumers_meet()) return;
         }
         if (slice) continue;
+        // this lane: rows 2j + e, channels CV g + 2i (+ 1) of each half
         constexpr int CV = (DVP < 128 ? DVP : 128) / 8;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = rt * 16 + g + 8 * half, ri = i0 + row;
-            if (ri >= nr) continue;
-            float m = half ? m1 : m0, l = half ? l1 : l0;
-            const float M = half ? M1 : M0;
-            if (flags & (F_LEAD | F_TRAIL)) {
-                const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
-                const float f = M == -INFINITY ? 0.f : ex2(M - kOff - (m == -INFINITY ? 0.f : m));
-                if (j == 0) w.ml[slot] = make_float2(m, l);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int hv = 0; hv < C::HV; ++hv)
+            for (int e = 0; e < 2; ++e) {
+                const int row = rt * 8 * NT + 8 * nt + 2 * j + e, ri = i0 + row;
+                if (ri >= nr) continue;
+                float mm = m[nt][e], ll = l[nt][e];
+                const float MM = M[nt][e];
+                if (flags & (F_LEAD | F_TRAIL)) {
+                    const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
+                    const float x = MM == -INFINITY ? 0.f : ex2(MM - kOff - (mm == -INFINITY ? 0.f : mm));
+                    if (g == 0) w.ml[slot] = make_float2(mm, ll);
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        float* o = w.part + slot * DVP + hv * 128 + CV * (2 * j + n);
+                    for (int hv = 0; hv < C::HV; ++hv)
 #pragma unroll
-                        for (int c = 0; c < CV; c += 4)
-                            *reinterpret_cast<float4*>(o + c) =
-                                make_float4(acc[hv * CV + c][2 * half + n] * f, acc[hv * CV + c + 1][2 * half + n] * f,
-                                            acc[hv * CV + c + 2][2 * half + n] * f, acc[hv * CV + c + 3][2 * half + n] * f);
-                    }
-                continue;
-            }
-            const int tok = ri / a.G, head = hk * a.G + ri - tok * a.G;
-            if (a.sink) {
-                const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(m, sk);
-                l = (m == -INFINITY ? l : l * ex2(m - nm)) + ex2(sk - nm);
-                m = nm;
-            }
-            if (a.m && j == 0) {
-                a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = m == -INFINITY ? m : m * kLn2;
-                a.l[static_cast<int64_t>(head) * a.T + row0 + tok] = l;
-            }
-            const float f = l == 0.f || M == -INFINITY ? (l != l ? l : 0.f) : ex2(M - kOff - m) / l;
-            E* o = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] + static_cast<int64_t>(head) * a.os[1];
+                        for (int c = 0; c < CV; c += 4) {
+                            const int i = hv * (CV / 2) + c / 2;
+                            *reinterpret_cast<float4*>(w.part + slot * DVP + hv * 128 + CV * g + c) =
+                                make_float4(acc[i][nt][e] * x, acc[i][nt][2 + e] * x, acc[i + 1][nt][e] * x, acc[i + 1][nt][2 + e] * x);
+                        }
+                    continue;
+                }
+                const int tok = ri / a.G, head = hk * a.G + ri - tok * a.G;
+                if (a.sink) {
+                    const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(mm, sk);
+                    ll = (mm == -INFINITY ? ll : ll * ex2(mm - nm)) + ex2(sk - nm);
+                    mm = nm;
+                }
+                if (a.m && g == 0) {
+                    a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = mm == -INFINITY ? mm : mm * kLn2;
+                    a.l[static_cast<int64_t>(head) * a.T + row0 + tok] = ll;
+                }
+                const float x = ll == 0.f || MM == -INFINITY ? (ll != ll ? ll : 0.f) : ex2(MM - kOff - mm) / ll;
+                E* o = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] + static_cast<int64_t>(head) * a.os[1];
 #pragma unroll
-            for (int hv = 0; hv < C::HV; ++hv)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int c0 = hv * 128 + CV * (2 * j + n);
+                for (int hv = 0; hv < C::HV; ++hv) {
+                    const int c0 = hv * 128 + CV * g;
                     if constexpr (!SPLIT) {
                         if (w.vec_o && c0 + CV <= a.dv) {
 #pragma unroll
                             for (int c = 0; c < CV; c += 8) {
                                 uint32_t p[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    p[e] = pack_bf16(acc[hv * CV + c + 2 * e][2 * half + n] * f, acc[hv * CV + c + 2 * e + 1][2 * half + n] * f);
+                                for (int q = 0; q < 4; ++q) {
+                                    const int i = hv * (CV / 2) + c / 2 + q;
+                                    p[q] = pack_bf16(acc[i][nt][e] * x, acc[i][nt][2 + e] * x);
+                                }
                                 *reinterpret_cast<uint4*>(o + c0 + c) = make_uint4(p[0], p[1], p[2], p[3]);
                             }
                             continue;
@@ -709,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, SPLIT>::OCC))
                     }
 #pragma unroll
                     for (int c = 0; c < CV; ++c)
-                        if (c0 + c < a.dv) o[c0 + c] = static_cast<E>(acc[hv * CV + c][2 * half + n] * f);
+                        if (c0 + c < a.dv) o[c0 + c] = static_cast<E>(acc[hv * (CV / 2) + c / 2][nt][(c & 1) * 2 + e] * x);
                 }
-        }
+            }
     }
 }
 
@@ -754,7 +788,7 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
     }
     n = min(n, w.ctas - c);
     const bool there = row < rec.nrows;
-    auto slot = [&](int k) { return (k ? 2 * (static_cast<int64_t>(c) + k) : 2 * static_cast<int64_t>(c) + 1) * (16 * w.RT) + row; };
+    auto slot = [&](int k) { return (k ? 2 * (static_cast<int64_t>(c) + k) : 2 * static_cast<int64_t>(c) + 1) * w.rows_per + row; };
     float m = -INFINITY, l = 0.f, acc[V];
     if (there)
         for (int k = lane; k < n; k += 32) m = fmaxf(m, w.ml[slot(k)].x);
@@ -840,7 +874,7 @@ int sm_count() {
 constexpr int kMaxSms = 160;          // the workspace is sized for this many
 
 struct Plan {
-    int DP, DVP, RT, occ, max_ctas;
+    int DP, DVP, NT, RT, rows_per, occ, max_ctas;
     size_t recs, ml, part, total;     // offsets behind the header
 };
 bool plan_of(const CacheAttnArgs& a, Plan& p) {
@@ -851,11 +885,13 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     if (p.DVP > p.DP) p.DP = p.DVP;
     if (p.DP == 256 && p.DVP == 64) p.DVP = 128;
     const int64_t rows = static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G;
+    p.NT = rows <= 8 ? 1 : 2;
     p.RT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.occ = p.DP <= 128 ? 2 : 1;
+    p.rows_per = 8 * p.NT * p.RT;
+    p.occ = p.DP <= 128 ? (p.NT == 1 ? 3 : 2) : (p.NT == 1 ? 2 : 1);
     p.max_ctas = kMaxSms * p.occ;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-    const size_t slots = 2 * static_cast<size_t>(p.max_ctas) * 16 * p.RT;
+    const size_t slots = 2 * static_cast<size_t>(p.max_ctas) * p.rows_per;
     p.recs = 256;
     p.ml = p.recs + up(sizeof(Rec) * p.max_ctas);
     p.part = p.ml + up(slots * sizeof(float2));
@@ -863,27 +899,27 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     return true;
 }
 
-template <int DP, int DVP, bool SPLIT>
+template <int DP, int DVP, int NT, bool SPLIT>
 cudaError_t launch(const Work& w, const CUtensorMap* maps, int rpb, cudaStream_t s) {
-    using C = Cfg<DP, DVP, SPLIT>;
-    auto kernel = k_cache_attn_mma<DP, DVP, SPLIT>;
+    using C = Cfg<DP, DVP, NT, SPLIT>;
+    auto kernel = k_cache_attn_mma<DP, DVP, NT, SPLIT>;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = uint64_t{1} << (dev & 63);
     if (!(done.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(4));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    kernel<<<w.ctas, kThreads, C::smem(w.RT), s>>>(maps[0], maps[1], w);
+    kernel<<<w.ctas, kThreads, C::SMEM, s>>>(maps[0], maps[1], w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, 16 * w.RT / rpb);
+    cfg.gridDim = dim3(w.ctas, w.rows_per / rpb);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = at;
@@ -916,9 +952,10 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     Work w;
     w.a = a;
     w.RT = p.RT;
+    w.rows_per = p.rows_per;
     // no more CTAs than the longest table rows have tiles
-    const int64_t groups = (static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G + 16 * p.RT - 1) / (16 * p.RT);
-    const int64_t most = ((static_cast<int64_t>(a.max_pages) * a.P + kTile - 1) / kTile) * a.Hkv * a.R * groups;
+    const int64_t groups = (static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G + p.rows_per - 1) / p.rows_per;
+    const int64_t most = ((static_cast<int64_t>(a.max_pages) * a.P + kTile - 1) / kTile + kExtra) * a.Hkv * a.R * groups;
     const int64_t ctas = static_cast<int64_t>(std::min(sm_count(), kMaxSms)) * p.occ;
     w.ctas = static_cast<int>(most < ctas ? most : ctas);
     w.recs = reinterpret_cast<Rec*>(ws + p.recs);
@@ -931,7 +968,8 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     const bool f32 = a.dtype == BPA_FP32;
 #define BPA_CACHE_CASE(DP_, DVP_) \
     if (p.DP == DP_ && p.DVP == DVP_) \
-        return f32 ? launch<DP_, DVP_, true>(w, maps, rpb, s) : launch<DP_, DVP_, false>(w, maps, rpb, s);
+        return p.NT == 1 ? f32 ? launch<DP_, DVP_, 1, true>(w, maps, rpb, s) : launch<DP_, DVP_, 1, false>(w, maps, rpb, s) \
+                         : f32 ? launch<DP_, DVP_, 2, true>(w, maps, rpb, s) : launch<DP_, DVP_, 2, false>(w, maps, rpb, s);
     BPA_CACHE_CASE(64, 64)
     BPA_CACHE_CASE(128, 64)
     BPA_CACHE_CASE(128, 128)
