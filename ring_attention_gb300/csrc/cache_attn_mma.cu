@@ -46,18 +46,17 @@ constexpr float kOff = 9.f;           // log2 of the largest fp16 weight right a
 constexpr float kLazy = 6.f;          // M moves when it grows by more
 
 struct Rec {                          // what a CTA leaves for the join
-    int lead, lead_ends;              // slot 0 holds a piece of an item begun by an earlier CTA; its last
-    int trail;                        // slot 1 holds the first piece of an item that goes on
+    int trail;                        // slot 1 holds the first of `trail` pieces of an item (0: none)
     int row0, hk, i0, nrows;          // that item
     uint32_t flags, where;            // this CTA's status
-    int pad[3];
+    int pad;
 };
-static_assert(sizeof(Rec) == 48, "record");
+static_assert(sizeof(Rec) == 32, "record");
 
 struct Work {
     CacheAttnArgs a;
-    int rows_per, RT, ctas;           // rows of an item, row tiles of 8 NT, CTAs
-    int vec_o;                        // o takes 16-byte stores
+    int rows_per, ctas;               // rows of an item, CTAs
+    int vec_q, vec_o;                 // four elements of q, two of o at a time
     Rec* recs;                        // [ctas]
     float2* ml;                       // [2 ctas][rows_per] (m in log2 units, l)
     float* part;                      // [2 ctas][rows_per][DVP] relative to m
@@ -79,7 +78,7 @@ struct Cfg {
     static constexpr int QF = DP / 16 * NT * 256 * (SPLIT ? 2 : 1);                // fragments of a row tile
     static constexpr int QS = Q_REGS ? 0 : QF * (NT == 1 ? 1 : 4);                 // ... of all row tiles
     static constexpr int STATE = 8 * NT * DVP + 8 * NT * 4;                        // floats of a warp's state
-    static constexpr int MERGE = 2 * STATE * 4;
+    static constexpr int MERGE = kNW * STATE * 4;
     static constexpr int OCC = DP <= 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 1);
     static constexpr int FIXED = 1024 + MERGE + 256 + QS;
     static constexpr int FIT = (233472 / OCC - 1024 - 128 - FIXED) / (STAGE + (int)sizeof(Meta));
@@ -88,6 +87,10 @@ struct Cfg {
     static_assert(NS >= 2, "stages");
 };
 
+// announces bytes without arriving
+BPA_DEV void mbar_expect_tx_only(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 BPA_DEV uint32_t cvt2(uint32_t two) {      // two e4m3 codes -> fp16 pair, exact
     uint32_t h;
     asm("{.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(h) : "r"(two));
@@ -124,6 +127,20 @@ BPA_DEV uint32_t swz(int row, int col) {
 
 BPA_DEV float ld_q(const float* p) { return __ldg(p); }
 BPA_DEV float ld_q(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+BPA_DEV void ld_q4(const float* p, float (&v)[4]) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = x.x;
+    v[1] = x.y;
+    v[2] = x.z;
+    v[3] = x.w;
+}
+BPA_DEV void ld_q4(const __nv_bfloat16* p, float (&v)[4]) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = __uint_as_float(x.x << 16);
+    v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16);
+    v[3] = __uint_as_float(x.y & 0xffff0000u);
+}
 
 // Key tiles of row group rg: first tile and count (at least one, so that rows without keys are
 // written too; such a tile holds no allowed key).
@@ -184,6 +201,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         rec->flags = rec->where = 0;
         __threadfence();
     }
+    if (threadIdx.x == 32 * kNW) {
+        tma_prefetch(&tmK);
+        tma_prefetch(&tmV);
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- this CTA's share: [begin, end) of the running sum of tiles and kExtra over the items
@@ -230,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         Rec out = {};
         bool ok = true;
         if (r >= 0) {
+            bool fresh = true;
             const int BR = min(a.P, kTile);
             const uint32_t copy = static_cast<uint32_t>(BR) * (DP + DVP);
             Req rq = request_of(a, r);
@@ -244,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                 off -= tl.n + kExtra;
                 tl = tiles_of(a, rq, ++rg, rows_per);
             }
+            long long at = begin;                          // the running sum at `off`
             while (left > 0 && ok) {
                 // [off, to) of the item's cost; its first kExtra are no tiles
                 const long long to = min(static_cast<long long>(tl.n + kExtra), off + left);
@@ -251,18 +274,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                 const bool lead = t > 0, trail = te < tl.n;
                 const int i0 = rg * rows_per;
                 const int kind = lead ? F_LEAD : trail ? F_TRAIL : 0;
-                if (t == te) {
-                } else if (lead) {
-                    out.lead = 1;
-                    out.lead_ends = !trail;
-                } else if (trail) {
-                    out.trail = 1;
+                if (t < te && trail && !lead) {
+                    // its pieces: up to the last CTA c with total c / parts < the end of the item's cost
+                    const long long at_end = at + (tl.n + kExtra - off);
+                    out.trail = static_cast<int>((at_end * parts + total - 1) / total) - cta;
                     out.row0 = rq.row0;
                     out.hk = hk;
                     out.i0 = i0;
                     out.nrows = min(rq.n * a.G - i0, rows_per);
                 }
                 const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
+                if (t < te) {                              // q of the item on its way to L2
+                    const int rows = min(rq.n * a.G - i0, rows_per), lines = (a.d * static_cast<int>(sizeof(E)) + 127) / 128;
+                    for (int i = lane; i < rows * lines; i += 32) {
+                        const int ri = i0 + i / lines, tok = ri / a.G;
+                        const E* q = static_cast<const E*>(a.q) + static_cast<int64_t>(rq.row0 + tok) * a.qs[0] +
+                                     static_cast<int64_t>(hk * a.G + ri - tok * a.G) * a.qs[1];
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(q) + 128 * (i % lines)));
+                    }
+                }
                 for (int b = t; b < te && ok; b += kBatch) {
                     // lane = tile of the batch * 4 + chunk of 16 keys
                     const int tile = b + (lane >> 2), chunk = lane & 3;
@@ -281,39 +311,51 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                         vs = __ldg(a.vscale + static_cast<int64_t>(id) * a.Hkv + hk);
                     }
                     const int cnt = min(kBatch, te - b);
-                    for (int j = 0; j < cnt; ++j) {
-                        ok = mbar_wait(EMPTY(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD2);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                        const bool turn = (lane >> 2) == j;
-                        const bool copies = turn && id >= 0 && (16 * chunk) % BR == 0;
+                    // tile jj of the batch into stage st
+                    auto copy_tile = [&](int jj, int st) {
+                        const bool copies = (lane >> 2) == jj && id >= 0 && (16 * chunk) % BR == 0;
                         const uint32_t n = __popc(__ballot_sync(0xffffffffu, copies));
+                        if (lane == 0) mbar_expect_tx_only(FULL(st), n * copy);
+                        __syncwarp();
+                        if (copies) {
+                            const uint32_t to_k = sb + st * C::STAGE + 16 * chunk * C::RBK;
+                            const uint32_t to_v = sb + st * C::STAGE + C::K_BYTES + 16 * chunk * C::RBV;
+                            const int tok = key % a.P;
+                            for (int h = 0; h < C::HK; ++h)
+                                tma_load_4d(to_k + h * kTile * C::RBK, &tmK, FULL(st), 128 * h, tok, hk, id);
+                            for (int h = 0; h < C::HV; ++h)
+                                tma_load_4d(to_v + h * kTile * C::RBV, &tmV, FULL(st), 128 * h, tok, hk, id);
+                        }
+                    };
+                    // the first tiles of the share are on their way before their pages' scales are here
+                    int ahead = 0;
+                    if (fresh) {
+                        for (; ahead < min(cnt, C::NS); ++ahead) copy_tile(ahead, ahead);
+                        fresh = false;
+                    }
+                    for (int jj = 0; jj < cnt; ++jj) {
+                        if (jj >= ahead) {
+                            ok = mbar_wait(EMPTY(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD2);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            copy_tile(jj, stage);
+                        }
                         Meta* m = meta + stage;
                         if (lane == 0) {
-                            m->key0 = (tl.first + b + j) * kTile;
+                            m->key0 = (tl.first + b + jj) * kTile;
                             m->len = rq.len;
                             m->n = rq.n;
                             m->row0 = rq.row0;
                             m->hk = hk;
                             m->i0 = i0;
-                            m->flags = kind | (b + j == t ? F_FIRST : 0) | (b + j == te - 1 ? F_LAST : 0);
+                            m->flags = kind | (b + jj == t ? F_FIRST : 0) | (b + jj == te - 1 ? F_LAST : 0);
                         }
-                        if (turn) {
+                        if ((lane >> 2) == jj) {
                             m->ks[chunk] = ks;
                             m->vs[chunk] = vs;
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_expect_tx(FULL(stage), n * copy);
-                        __syncwarp();
-                        if (copies) {
-                            const uint32_t at = sb + stage * C::STAGE;
-                            const int tok = key % a.P;
-                            for (int h = 0; h < C::HK; ++h)
-                                tma_load_4d(at + h * kTile * C::RBK + 16 * chunk * C::RBK, &tmK, FULL(stage), 128 * h, tok, hk, id);
-                            for (int h = 0; h < C::HV; ++h)
-                                tma_load_4d(at + C::K_BYTES + h * kTile * C::RBV + 16 * chunk * C::RBV, &tmV, FULL(stage),
-                                            128 * h, tok, hk, id);
-                        }
+                        if (lane == 0) mbar_arrive(FULL(stage));
                         if (++stage == C::NS) {
                             stage = 0;
                             phase ^= 1;
@@ -321,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                     }
                 }
                 left -= to - off;
+                at += to - off;
                 off = 0;
                 if (left > 0) {        // the next item: row group, head, request
                     if (++rg == groups) {
@@ -357,8 +400,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
             for (int s = 0; s < C::NS; ++s) mbar_wait(FULL(s), s < stage ? phase ^ 1 : phase, &never, status, 0xCD3);
         }
         if (lane == 0) {
-            rec->lead = out.lead;
-            rec->lead_ends = out.lead_ends;
             rec->trail = out.trail;
             rec->row0 = out.row0;
             rec->hk = out.hk;
@@ -369,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     }
 
     // ---- consumers
-    const int rt = warp % w.RT, slices = kNW / w.RT, slice = warp / w.RT;
+    int rt = 0, slices = kNW, slice = warp;        // row tile of the item, warps that share its keys, this one
     const int g = lane >> 2, j = lane & 3;
-    uint8_t* my_q = smem + (q_at - sb) + rt * C::QF + lane * 8;
+    uint8_t* my_q = nullptr;
     uint32_t qf[C::Q_REGS ? DP / 16 : 1][NT][2];
     float acc[DVP / 16][NT][4];
     // rows 2j + e of n-tile nt: running (m, l) of this lane's keys, M of the row, its factor and keys
@@ -395,7 +436,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         if (flags & F_FIRST) {
             // ---- a new item: this warp's rows of q as fp16 fragments, scaled by a power of two
             const Req rq = {mt->row0, mt->n, len, false};
-            const int hk = mt->hk, nr = rq.n * a.G, first = mt->i0 + rt * 8 * NT;
+            const int hk = mt->hk, nr = rq.n * a.G;
+            // as many row tiles as this item has: 1, 2 or 4 of the warps apart, the others on other keys
+            const int tiles = (min(nr - mt->i0, rows_per) + 8 * NT - 1) / (8 * NT), RT = tiles > 2 ? 4 : tiles;
+            rt = warp & (RT - 1);
+            slices = kNW / RT;
+            slice = warp / RT;
+            my_q = smem + (q_at - sb) + rt * C::QF + lane * 8;
+            const int first = mt->i0 + rt * 8 * NT;
             in_lo = any_hi = 0;
             in_hi = any_lo = INT_MAX;
 #pragma unroll
@@ -407,15 +455,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                              static_cast<int64_t>(hk * a.G + (there ? ri - tok * a.G : 0)) * a.qs[1];
                 float v[DP / 16][4];
                 float top = 0.f;
+                if (w.vec_q) {
 #pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                    const int c = (s >> 2) * 64 + 16 * j + 4 * (s & 3);
+                    for (int s = 0; s < DP / 16; ++s) {
+                        const int c = (s >> 2) * 64 + 16 * j + 4 * (s & 3);
+                        v[s][0] = v[s][1] = v[s][2] = v[s][3] = 0.f;
+                        if (there && c < a.d) ld_q4(q + c, v[s]);
+                    }
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[s][e] = there && c + e < a.d ? ld_q(q + c + e) : 0.f;
-                        top = fmaxf(top, fabsf(v[s][e]));
+                    for (int s = 0; s < DP / 16; ++s) {
+                        const int c = (s >> 2) * 64 + 16 * j + 4 * (s & 3);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[s][e] = there && c < a.d ? ld_q(q + c + e) : 0.f;
                     }
                 }
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s)
+                    top = fmaxf(fmaxf(top, fmaxf(fabsf(v[s][0]), fabsf(v[s][1]))), fmaxf(fabsf(v[s][2]), fabsf(v[s][3])));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // largest value into [2^7, 2^8); 0 and values that are not finite stay as they are
@@ -641,111 +698,121 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                     l[nt][e] = __fadd_rn(__fmul_rn(l[nt][e], ex2(m[nt][e] - ref)), __fmul_rn(y, ex2(x - ref)));
                     m[nt][e] = n;
                 }
-        for (int st = slices >> 1; st >= 1; st >>= 1) {
-            float* buf = merge + ((slice & (st - 1)) * w.RT + rt) * C::STATE;
-            if (slice >= st && slice < 2 * st) {
+        constexpr int CV = (DVP < 128 ? DVP : 128) / 8, F = DVP / 16;
+        float* state = merge + rt * C::STATE;              // slice k of the row tile: k * RT states further
+        const int RT = kNW / slices;
+        if (slices > 1) {
+            float* buf = state + slice * RT * C::STATE;
 #pragma unroll
-                for (int i = 0; i < DVP / 16; ++i)
+            for (int i = 0; i < F; ++i)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        *reinterpret_cast<float4*>(buf + ((i * NT + nt) * 32 + lane) * 4) =
-                            make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
-                if (g == 0)
+                for (int nt = 0; nt < NT; ++nt)
+                    *reinterpret_cast<float4*>(buf + ((i * NT + nt) * 32 + lane) * 4) =
+                        make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+            if (g == 0)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<float4*>(buf + 8 * NT * DVP + (8 * nt + 2 * j + e) * 4) =
-                                make_float4(m[nt][e], l[nt][e], M[nt][e], 0.f);
-            }
-            if (!consumers_meet()) return;
-            if (slice < st) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float x[2], y[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float4 b = *reinterpret_cast<const float4*>(buf + 8 * NT * DVP + (8 * nt + 2 * j + e) * 4);
-                        const float n = fmaxf(m[nt][e], b.x), ref = n == -INFINITY ? 0.f : n;
-                        l[nt][e] = l[nt][e] * ex2(m[nt][e] - ref) + b.y * ex2(b.x - ref);
-                        m[nt][e] = n;
-                        const float N = fmaxf(M[nt][e], b.z);
-                        x[e] = M[nt][e] == -INFINITY ? 0.f : ex2(M[nt][e] - N);
-                        y[e] = b.z == -INFINITY ? 0.f : ex2(b.z - N);
-                        M[nt][e] = N;
-                    }
-#pragma unroll
-                    for (int i = 0; i < DVP / 16; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(buf + ((i * NT + nt) * 32 + lane) * 4);
-                        acc[i][nt][0] = acc[i][nt][0] * x[0] + v.x * y[0];
-                        acc[i][nt][1] = acc[i][nt][1] * x[1] + v.y * y[1];
-                        acc[i][nt][2] = acc[i][nt][2] * x[0] + v.z * y[0];
-                        acc[i][nt][3] = acc[i][nt][3] * x[1] + v.w * y[1];
-                    }
-                }
-            }
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float4*>(buf + 8 * NT * DVP + (8 * nt + 2 * j + e) * 4) =
+                            make_float4(m[nt][e], l[nt][e], M[nt][e], 0.f);
             if (!consumers_meet()) return;
         }
-        if (slice) continue;
-        // this lane: rows 2j + e, channels CV g + 2i (+ 1) of each half
-        constexpr int CV = (DVP < 128 ? DVP : 128) / 8;
+        // every warp of a row tile writes its share of the channels
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            float x[2][kNW];                               // factors of the slices' sums, per row
+            float* part[2];
+            E* out[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = rt * 8 * NT + 8 * nt + 2 * j + e, ri = i0 + row;
-                if (ri >= nr) continue;
-                float mm = m[nt][e], ll = l[nt][e];
-                const float MM = M[nt][e];
-                if (flags & (F_LEAD | F_TRAIL)) {
-                    const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
-                    const float x = MM == -INFINITY ? 0.f : ex2(MM - kOff - (mm == -INFINITY ? 0.f : mm));
-                    if (g == 0) w.ml[slot] = make_float2(mm, ll);
+                part[e] = nullptr;
+                out[e] = nullptr;
+                float mm = m[nt][e], ll = l[nt][e], MS[kNW] = {M[nt][e], -INFINITY, -INFINITY, -INFINITY};
+                if (slices > 1) {
+                    float4 b[kNW];
+                    mm = -INFINITY;
 #pragma unroll
-                    for (int hv = 0; hv < C::HV; ++hv)
+                    for (int k = 0; k < kNW; ++k) {
+                        b[k] = k < slices ? *reinterpret_cast<const float4*>(state + k * RT * C::STATE + 8 * NT * DVP +
+                                                                             (8 * nt + 2 * j + e) * 4)
+                                          : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                        mm = fmaxf(mm, b[k].x);
+                        MS[k] = b[k].z;
+                    }
+                    ll = 0.f;
 #pragma unroll
-                        for (int c = 0; c < CV; c += 4) {
-                            const int i = hv * (CV / 2) + c / 2;
-                            *reinterpret_cast<float4*>(w.part + slot * DVP + hv * 128 + CV * g + c) =
-                                make_float4(acc[i][nt][e] * x, acc[i][nt][2 + e] * x, acc[i + 1][nt][e] * x, acc[i + 1][nt][2 + e] * x);
+                    for (int k = 0; k < kNW; ++k) ll += b[k].y * ex2(b[k].x - (mm == -INFINITY ? 0.f : mm));
+                }
+                float norm = 1.f;
+                if (ri < nr) {
+                    const int tok = ri / a.G, head = hk * a.G + ri - tok * a.G;
+                    if (flags & (F_LEAD | F_TRAIL)) {
+                        const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
+                        part[e] = w.part + slot * DVP + CV * g;
+                        if (slice == 0 && g == 0) w.ml[slot] = make_float2(mm, ll);
+                    } else {
+                        float lf = ll, mf = mm;
+                        if (a.sink) {
+                            const float sk = __ldg(a.sink + head) * kLog2e;
+                            mf = fmaxf(mm, sk);
+                            norm = mm == -INFINITY ? 1.f : ex2(mm - mf);
+                            lf = ll * norm + ex2(sk - mf);
                         }
-                    continue;
+                        if (a.m && slice == 0 && g == 0) {
+                            a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = mf == -INFINITY ? mf : mf * kLn2;
+                            a.l[static_cast<int64_t>(head) * a.T + row0 + tok] = lf;
+                        }
+                        norm = lf == 0.f ? 0.f : norm / lf;
+                        out[e] = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] +
+                                 static_cast<int64_t>(head) * a.os[1] + CV * g;
+                    }
                 }
-                const int tok = ri / a.G, head = hk * a.G + ri - tok * a.G;
-                if (a.sink) {
-                    const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(mm, sk);
-                    ll = (mm == -INFINITY ? ll : ll * ex2(mm - nm)) + ex2(sk - nm);
-                    mm = nm;
-                }
-                if (a.m && g == 0) {
-                    a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = mm == -INFINITY ? mm : mm * kLn2;
-                    a.l[static_cast<int64_t>(head) * a.T + row0 + tok] = ll;
-                }
-                const float x = ll == 0.f || MM == -INFINITY ? (ll != ll ? ll : 0.f) : ex2(MM - kOff - mm) / ll;
-                E* o = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] + static_cast<int64_t>(head) * a.os[1];
 #pragma unroll
-                for (int hv = 0; hv < C::HV; ++hv) {
-                    const int c0 = hv * 128 + CV * g;
-                    if constexpr (!SPLIT) {
-                        if (w.vec_o && c0 + CV <= a.dv) {
+                for (int k = 0; k < kNW; ++k)
+                    x[e][k] = (MS[k] == -INFINITY ? (norm != norm ? norm : 0.f)
+                                                  : ex2(MS[k] - kOff - (mm == -INFINITY ? 0.f : mm)) * norm);
+            }
+            auto put = [&](int i, float4 v) {              // fragment i: channels 2 (i % (CV / 2)) and the next of a half
+                const int c = (i / (CV / 2)) * 128 + (i % (CV / 2)) * 2;
 #pragma unroll
-                            for (int c = 0; c < CV; c += 8) {
-                                uint32_t p[4];
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int i = hv * (CV / 2) + c / 2 + q;
-                                    p[q] = pack_bf16(acc[i][nt][e] * x, acc[i][nt][2 + e] * x);
-                                }
-                                *reinterpret_cast<uint4*>(o + c0 + c) = make_uint4(p[0], p[1], p[2], p[3]);
-                            }
-                            continue;
+                for (int e = 0; e < 2; ++e) {
+                    const float y0 = e ? v.y : v.x, y1 = e ? v.w : v.z;
+                    if (part[e]) *reinterpret_cast<float2*>(part[e] + c) = make_float2(y0, y1);
+                    if (out[e] && CV * g + c < a.dv) {
+                        if (!SPLIT && w.vec_o) {
+                            *reinterpret_cast<uint32_t*>(out[e] + c) = pack_bf16(y0, y1);
+                        } else {
+                            out[e][c] = static_cast<E>(y0);
+                            out[e][c + 1] = static_cast<E>(y1);
                         }
                     }
+                }
+            };
+            if (slices == 1) {
 #pragma unroll
-                    for (int c = 0; c < CV; ++c)
-                        if (c0 + c < a.dv) o[c0 + c] = static_cast<E>(acc[hv * (CV / 2) + c / 2][nt][(c & 1) * 2 + e] * x);
+                for (int i = 0; i < F; ++i)
+                    put(i, make_float4(acc[i][nt][0] * x[0][0], acc[i][nt][1] * x[1][0], acc[i][nt][2] * x[0][0],
+                                       acc[i][nt][3] * x[1][0]));
+            } else {
+                const int each = F / slices;
+                for (int i = slice * each; i < (slice + 1) * each; ++i) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < kNW; ++k)
+                        if (k < slices) {
+                            const float4 b = *reinterpret_cast<const float4*>(state + k * RT * C::STATE + ((i * NT + nt) * 32 + lane) * 4);
+                            v.x = fmaf(b.x, x[0][k], v.x);
+                            v.y = fmaf(b.y, x[1][k], v.y);
+                            v.z = fmaf(b.z, x[0][k], v.z);
+                            v.w = fmaf(b.w, x[1][k], v.w);
+                        }
+                    put(i, v);
                 }
             }
+        }
+        if (slices > 1 && !consumers_meet()) return;       // the states may be written again
     }
 }
 
@@ -755,6 +822,7 @@ template <int DVP, typename E>
 __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint32_t* out_status) {
     constexpr int V = DVP / 32;
     __shared__ float s_acc[8][DVP];
+    __shared__ float2 s_ml[8];
     __shared__ uint32_t s_flags, s_where;
     const CacheAttnArgs& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
@@ -774,71 +842,68 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
         }
     }
     const Rec rec = w.recs[c];
-    const int row = blockIdx.y * rpb + warp % rpb, part = warp / rpb, parts = 8 / rpb;
-    if (!rec.trail || static_cast<int>(blockIdx.y) * rpb >= rec.nrows) return;
-    int n = 1;                                     // pieces
-    for (;;) {
-        const int i = c + n + lane;
-        const unsigned b = __ballot_sync(0xffffffffu, i >= w.ctas || !w.recs[i].lead || w.recs[i].lead_ends);
-        if (b) {
-            n += __ffs(b);
-            break;
-        }
-        n += 32;
-    }
-    n = min(n, w.ctas - c);
+    const int row = blockIdx.y * rpb + warp % rpb, part = warp / rpb, parts = 8 / rpb, n = rec.trail;
+    if (!n || static_cast<int>(blockIdx.y) * rpb >= rec.nrows) return;
     const bool there = row < rec.nrows;
-    auto slot = [&](int k) { return (k ? 2 * (static_cast<int64_t>(c) + k) : 2 * static_cast<int64_t>(c) + 1) * w.rows_per + row; };
     float m = -INFINITY, l = 0.f, acc[V];
-    if (there)
-        for (int k = lane; k < n; k += 32) m = fmaxf(m, w.ml[slot(k)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    if (there)
-        for (int k = lane; k < n; k += 32) {
-            const float2 x = w.ml[slot(k)];
-            l += x.y == 0.f ? 0.f : x.y * ex2(x.x - ref);
-        }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     if (there) {
-#pragma unroll 4
-        for (int k = part; k < n; k += parts) {
-            const int64_t s = slot(k);
-            const float2 x = w.ml[s];
-            const float f = x.y == 0.f ? 0.f : ex2(x.x - ref);
-            const float* p = w.part + s * DVP + lane * V;
-            float v[V];
-            if constexpr (V == 2) {
-                const float2 t = *reinterpret_cast<const float2*>(p);
-                v[0] = t.x;
-                v[1] = t.y;
-            } else {
+        // one pass with the running maximum; four pieces' loads at a time
+        for (int k0 = part; k0 < n; k0 += 4 * parts) {
+            float2 x[4];
+            float v[4][V];
 #pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(p + i);
-                    v[i] = t.x;
-                    v[i + 1] = t.y;
-                    v[i + 2] = t.z;
-                    v[i + 3] = t.w;
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + q * parts;
+                x[q] = make_float2(-INFINITY, 0.f);
+                if (k >= n) continue;
+                const int64_t s = (2 * (static_cast<int64_t>(c) + k) + (k == 0)) * w.rows_per + row;
+                x[q] = w.ml[s];
+                const float* p = w.part + s * DVP + lane * V;
+                if constexpr (V == 2) {
+                    const float2 t = *reinterpret_cast<const float2*>(p);
+                    v[q][0] = t.x;
+                    v[q][1] = t.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; i += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(p + i);
+                        v[q][i] = t.x;
+                        v[q][i + 1] = t.y;
+                        v[q][i + 2] = t.z;
+                        v[q][i + 3] = t.w;
+                    }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(f, v[i], acc[i]);
+            for (int q = 0; q < 4; ++q) {
+                if (k0 + q * parts >= n || x[q].y == 0.f) continue;      // no keys in the piece
+                const float nm = fmaxf(m, x[q].x), ref = nm == -INFINITY ? 0.f : nm;
+                const float f0 = m == -INFINITY ? (l != l ? l : 0.f) : ex2(m - ref), f1 = ex2(x[q].x - ref);
+                l = l * f0 + x[q].y * f1;
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + v[q][i] * f1;
+                m = nm;
+            }
         }
     }
-    if (parts > 1) {
-        if (part)
+    if (parts > 1) {                               // the groups of pieces, in order
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
 #pragma unroll
-            for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
+        for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
         __syncthreads();
         if (part) return;
-        for (int q = 1; q < parts; ++q)
+        for (int q = 1; q < parts; ++q) {
+            const float2 x = s_ml[q * rpb + warp];
+            if (x.y == 0.f) continue;
+            const float nm = fmaxf(m, x.x), ref = nm == -INFINITY ? 0.f : nm;
+            const float f0 = m == -INFINITY ? (l != l ? l : 0.f) : ex2(m - ref), f1 = ex2(x.x - ref);
+            l = l * f0 + x.y * f1;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += s_acc[q * rpb + warp][lane * V + i];
+            for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + s_acc[q * rpb + warp][lane * V + i] * f1;
+            m = nm;
+        }
     }
     if (!there) return;
     const int ri = rec.i0 + row, tok = ri / a.G, head = rec.hk * a.G + ri - tok * a.G;
@@ -951,7 +1016,6 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     if (!plan_of(a, p)) return cudaErrorInvalidValue;
     Work w;
     w.a = a;
-    w.RT = p.RT;
     w.rows_per = p.rows_per;
     // no more CTAs than the longest table rows have tiles
     const int64_t groups = (static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G + p.rows_per - 1) / p.rows_per;
@@ -961,7 +1025,9 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     w.recs = reinterpret_cast<Rec*>(ws + p.recs);
     w.ml = reinterpret_cast<float2*>(ws + p.ml);
     w.part = reinterpret_cast<float*>(ws + p.part);
-    w.vec_o = a.dtype == BPA_BF16 && (reinterpret_cast<uintptr_t>(a.o) & 15) == 0 && a.os[0] % 8 == 0 && a.os[1] % 8 == 0;
+    const uintptr_t qa = a.dtype == BPA_BF16 ? 7 : 15;
+    w.vec_q = (reinterpret_cast<uintptr_t>(a.q) & qa) == 0 && a.qs[0] % 4 == 0 && a.qs[1] % 4 == 0;
+    w.vec_o = a.dtype == BPA_BF16 && (reinterpret_cast<uintptr_t>(a.o) & 3) == 0 && a.os[0] % 2 == 0 && a.os[1] % 2 == 0;
     // rows of a join block: few when an item is cut into many pieces
     const int64_t pieces = w.ctas / (static_cast<int64_t>(a.R) * a.Hkv);
     const int rpb = pieces <= 4 ? 8 : pieces <= 16 ? 4 : pieces <= 64 ? 2 : 1;
