@@ -47,6 +47,29 @@ struct CacheAttnArgs {
 };
 
 #ifdef __CUDACC__
+// Programmatic dependent launch: a kernel launched by launch_early may start while the one before it
+// on the stream still runs; it sets itself up and calls wait_for_previous() before it touches
+// anything in global memory (with plain loads, which the compiler does not move across it, until an
+// address depends on one), so the stream's order holds for everything that a caller can see.
+// launch_dependents() lets the next such kernel start as soon as every CTA of this one has.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(dim3 grid, dim3 block, size_t smem, cudaStream_t s, void (*kernel)(P...), A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Rows and keys of request r, made safe to address: rows clamped to [0, T], the length to the table.
 struct Req {
     int row0, n, len;                // first packed row, rows, keys
@@ -54,10 +77,10 @@ struct Req {
 };
 __device__ __forceinline__ Req request_of(const CacheAttnArgs& a, int r) {
     Req q;
-    q.row0 = min(max(__ldg(a.cu_q + r), 0), a.T);
-    q.n = max(min(__ldg(a.cu_q + r + 1), a.T) - q.row0, 0);
+    q.row0 = min(max(*(a.cu_q + r), 0), a.T);
+    q.n = max(min(*(a.cu_q + r + 1), a.T) - q.row0, 0);
     const int64_t cap = static_cast<int64_t>(a.max_pages) * a.P;
-    const int len = __ldg(a.kv_lens + r);
+    const int len = *(a.kv_lens + r);
     q.len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), cap));
     q.bad = len != q.len;
     return q;

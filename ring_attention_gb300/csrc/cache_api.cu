@@ -235,10 +235,7 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
     a.slots = slot_map;
     a.max_new = max_new;
     a.status = static_cast<uint32_t*>(workspace);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
-    if (st != BPA_OK || T == 0) return st;
-    return cuda_status(launch_cache_append(a, s), "append launch");
+    return cuda_status(launch_cache_append(a, static_cast<cudaStream_t>(stream)), "append launch");
 }
 
 size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cache_batch* batch) {

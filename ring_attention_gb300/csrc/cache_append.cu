@@ -14,12 +14,37 @@
 namespace bpa {
 namespace {
 
-BPA_DEV float load_f32(const float* p) { return __ldg(p); }
-BPA_DEV float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+// VE consecutive channels of a row as float32 bit patterns (16 bytes at a time, or one element)
+template <int VE>
+BPA_DEV void load_row(const float* p, uint32_t (&v)[VE]) {
+    if constexpr (VE == 1) {
+        v[0] = __float_as_uint(__ldg(p));
+    } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+        v[0] = x.x;
+        v[1] = x.y;
+        v[2] = x.z;
+        v[3] = x.w;
+    }
+}
+template <int VE>
+BPA_DEV void load_row(const __nv_bfloat16* p, uint32_t (&v)[VE]) {
+    if constexpr (VE == 1) {
+        v[0] = static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16;
+    } else {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = w[i] << 16;
+            v[2 * i + 1] = w[i] & 0xffff0000u;
+        }
+    }
+}
 
-// round to nearest even; infinities (and what lies past 448, which the scale rules out) become NaN
-BPA_DEV uint8_t to_e4m3(float x) {
-    return fabsf(x) < INFINITY ? static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3)) : 0x7f;
+// round to nearest even; |x| <= 448 here, NaN gives NaN, infinities 448
+BPA_DEV uint32_t e4m3_pair(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 BPA_DEV float from_e4m3(uint8_t c) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
@@ -34,70 +59,161 @@ BPA_DEV float scale_for(float amax) {
     return __uint_as_float(static_cast<uint32_t>(max(e, 27)) << 23);   // 27 - 127 = -100
 }
 
-// One warp per (row, head, tensor): the warp of a run's first row takes the run.
-template <typename E>
+// One warp per (ROWS rows, head, tensor): it takes the runs that begin in its rows, one after the
+// other, reading a run twice (largest magnitude, then codes; the second time from L2).  ROWS = 1
+// when requests bring few rows (every row is then a run of its own, or nearly); ROWS = 16 for prompts,
+// whose runs are whole pages: sixteen times fewer warps that find no beginning.  The last block looks
+// the slots over for the status word, so that nothing has to clear it before.
+template <typename E, int VE, int ROWS>
 __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int t0 = static_cast<int>(item / (2 * a.Hkv));
-    if (t0 >= a.T) return;
-    const int hw = static_cast<int>(item % (2 * a.Hkv)), h = hw >> 1;
-    const bool is_v = hw & 1;
-    const int slot = __ldg(a.slots + t0);
-    if (slot < 0) return;
-    const int cap = a.P * a.num_pages;
-    if (slot >= cap) {
-        if (lane == 0) report(a.status, ST_CHECK, 0xCB0);
+    launch_dependents();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, cap = a.P * a.num_pages;
+    if (blockIdx.x == gridDim.x - 1) {
+        __shared__ int s_bad;
+        if (threadIdx.x == 0) s_bad = 0;
+        __syncthreads();
+        for (int t = threadIdx.x; t < a.T; t += 128)
+            if (a.slots[t] >= cap) s_bad = 1;
+        __syncthreads();
+        if (threadIdx.x < 2) a.status[threadIdx.x] = !s_bad ? 0u : threadIdx.x ? 0xCB0u : static_cast<uint32_t>(ST_CHECK);
         return;
     }
-    const int page = slot / a.P, off = slot - page * a.P;
-    if (off && t0 && __ldg(a.slots + t0 - 1) == slot - 1) return;   // not the run's first row
-    int n = 1;                                                      // rows of the run
-    for (;;) {
-        const int i = n + lane, t = t0 + i;
-        const bool in = t < a.T && off + i < a.P && __ldg(a.slots + t) == slot + i;
-        const unsigned b = __ballot_sync(0xffffffffu, in);
-        if (b != 0xffffffffu) {
-            n += __ffs(~b) - 1;
-            break;
-        }
-        n += 32;
-    }
+    const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int first = static_cast<int>(item / (2 * a.Hkv)) * ROWS;
+    if (first >= a.T) return;
+    const int hw = static_cast<int>(item % (2 * a.Hkv)), h = hw >> 1;
+    const bool is_v = hw & 1;
     const int c = is_v ? a.dv : a.d;
-    const E* x = static_cast<const E*>(is_v ? a.v : a.k) + t0 * (is_v ? a.vs[0] : a.ks[0]) + h * (is_v ? a.vs[1] : a.ks[1]);
-    const int64_t xs = is_v ? a.vs[0] : a.ks[0];
-    const int64_t ts = is_v ? a.vcs[2] : a.kcs[2];
-    uint8_t* out = is_v ? a.vc + page * a.vcs[0] + h * a.vcs[1] : a.kc + page * a.kcs[0] + h * a.kcs[1];
-    float* scale = (is_v ? a.vscale : a.kscale) + static_cast<int64_t>(page) * a.Hkv + h;
-    float amax = 0.f;
-    for (int i = 0; i < n; ++i)
-        for (int j = lane; j < c; j += 32) {
-            const float y = fabsf(load_f32(x + i * xs + j));
-            if (y < INFINITY) amax = fmaxf(amax, y);
+    const int64_t xs = is_v ? a.vs[0] : a.ks[0], ts = is_v ? a.vcs[2] : a.kcs[2];
+    const E* rows = static_cast<const E*>(is_v ? a.v : a.k) + h * (is_v ? a.vs[1] : a.ks[1]);
+    const int units = c / VE, across = min(units, 32);             // lanes of a row
+    const int down = 32 / across, li = lane / across, lu = lane % across;
+    const bool active = li < down;
+
+    // lane i: slot of row first + i and of the one before
+    const int mine = lane < ROWS && first + lane < a.T ? a.slots[first + lane] : -1;
+    const int before = lane < ROWS && first + lane > 0 && first + lane < a.T ? a.slots[first + lane - 1] : -1;
+    unsigned begins = __ballot_sync(0xffffffffu, mine >= 0 && mine < cap && (mine % a.P == 0 || before != mine - 1));
+    while (begins) {
+        const int b = __ffs(begins) - 1;
+        begins &= begins - 1;
+        const int t0 = first + b, slot = __shfl_sync(0xffffffffu, mine, b);
+        const int page = slot / a.P, off = slot - page * a.P;
+        float* scale = (is_v ? a.vscale : a.kscale) + static_cast<int64_t>(page) * a.Hkv + h;
+        const float old = off ? *scale : 0.f;
+        int n = 1;                                                 // rows of the run
+        while (off + n < a.P) {
+            const int i = n + lane, t = t0 + i;
+            const unsigned more = __ballot_sync(0xffffffffu, t < a.T && off + i < a.P && a.slots[min(t, a.T - 1)] == slot + i);
+            n += more == 0xffffffffu ? 32 : __ffs(~more) - 1;
+            if (more != 0xffffffffu) break;
         }
+        const E* x = rows + t0 * xs;
+        // the largest magnitude as bits: at and above 0x7f800000 infinities and NaN are among the rows
+        uint32_t top = 0;
+        if (active) {
+#pragma unroll 4
+            for (int i = li; i < n; i += down)
+                for (int u = lu; u < units; u += across) {
+                    uint32_t v[VE];
+                    load_row<VE>(x + i * xs + u * VE, v);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float old = off ? *scale : 0.f;
-    const float s = fmaxf(old, scale_for(amax));
-    if (s > old && off) {
-        const float ratio = old / s;
-        for (int i = 0; i < off; ++i)
-            for (int j = lane; j < c; j += 32) out[i * ts + j] = to_e4m3(from_e4m3(out[i * ts + j]) * ratio);
+                    for (int e = 0; e < VE; ++e) top = max(top, v[e] & 0x7fffffffu);
+                }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool plain = top < 0x7f800000u;
+        if (!plain) {
+            top = 0;
+            if (active)
+                for (int i = li; i < n; i += down)
+                    for (int u = lu; u < units; u += across) {
+                        uint32_t v[VE];
+                        load_row<VE>(x + i * xs + u * VE, v);
+#pragma unroll
+                        for (int e = 0; e < VE; ++e)
+                            if ((v[e] & 0x7fffffffu) < 0x7f800000u) top = max(top, v[e] & 0x7fffffffu);
+                    }
+            top = __reduce_max_sync(0xffffffffu, top);
+        }
+        const float s = fmaxf(old, scale_for(__uint_as_float(top)));
+        uint8_t* out = is_v ? a.vc + page * a.vcs[0] + h * a.vcs[1] : a.kc + page * a.kcs[0] + h * a.kcs[1];
+        if (off && s > old) {
+            const float ratio = old / s;
+            if (active)
+#pragma unroll 2
+                for (int i = li; i < off; i += down)
+                    for (int u = lu; u < units; u += across) {
+                        uint8_t* p = out + i * ts + u * VE;
+                        if constexpr (VE == 1) {
+                            *p = static_cast<uint8_t>(e4m3_pair(from_e4m3(*p) * ratio, 0.f));
+                        } else {
+                            uint32_t* q = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+                            for (int k = 0; k < VE / 4; ++k) {
+                                const uint32_t y = q[k];
+                                q[k] = e4m3_pair(from_e4m3(y & 0xff) * ratio, from_e4m3((y >> 8) & 0xff) * ratio) |
+                                       e4m3_pair(from_e4m3((y >> 16) & 0xff) * ratio, from_e4m3(y >> 24) * ratio) << 16;
+                            }
+                        }
+                    }
+        }
+        const float inv = s > 0.f ? 1.f / s : 1.f;
+        out += off * ts;
+        if (active) {
+#pragma unroll 4
+            for (int i = li; i < n; i += down)
+                for (int u = lu; u < units; u += across) {
+                    uint32_t v[VE];
+                    load_row<VE>(x + i * xs + u * VE, v);
+                    if (!plain)
+#pragma unroll
+                        for (int e = 0; e < VE; ++e)               // an infinity is stored as NaN
+                            if ((v[e] & 0x7fffffffu) == 0x7f800000u) v[e] = 0x7fc00000u;
+                    uint8_t* p = out + i * ts + u * VE;
+                    if constexpr (VE == 1) {
+                        *p = static_cast<uint8_t>(e4m3_pair(__uint_as_float(v[0]) * inv, 0.f));
+                    } else {
+                        uint32_t w[VE / 4];
+#pragma unroll
+                        for (int k = 0; k < VE / 4; ++k)
+                            w[k] = e4m3_pair(__uint_as_float(v[4 * k]) * inv, __uint_as_float(v[4 * k + 1]) * inv) |
+                                   e4m3_pair(__uint_as_float(v[4 * k + 2]) * inv, __uint_as_float(v[4 * k + 3]) * inv) << 16;
+                        if constexpr (VE == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+                        else *reinterpret_cast<uint32_t*>(p) = w[0];
+                    }
+                }
+        }
+        __syncwarp();
+        if (lane == 0) *scale = s;
+        __syncwarp();
     }
-    const float inv = s > 0.f ? 1.f / s : 1.f;
-    for (int i = 0; i < n; ++i)
-        for (int j = lane; j < c; j += 32) out[(off + i) * ts + j] = to_e4m3(load_f32(x + i * xs + j) * inv);
-    __syncwarp();
-    if (lane == 0) *scale = s;
+}
+
+template <typename E, int VE>
+cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
+    const bool few = a.max_new > 0 ? a.max_new <= 8 : a.T <= 512;
+    const int rows = few ? 1 : 16;
+    const int64_t items = static_cast<int64_t>((a.T + rows - 1) / rows) * 2 * a.Hkv;
+    const dim3 grid(static_cast<unsigned>((items + 3) / 4 + 1));
+    return few ? launch_early(grid, dim3(128), 0, s, k_cache_append<E, VE, 1>, a)
+               : launch_early(grid, dim3(128), 0, s, k_cache_append<E, VE, 16>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s) {
-    const int64_t blocks = (static_cast<int64_t>(a.T) * 2 * a.Hkv + 3) / 4;
-    if (a.dtype == BPA_BF16) k_cache_append<__nv_bfloat16><<<static_cast<unsigned>(blocks), 128, 0, s>>>(a);
-    else k_cache_append<float><<<static_cast<unsigned>(blocks), 128, 0, s>>>(a);
-    return cudaGetLastError();
+    // 16-byte loads and 8- or 4-byte stores where everything is aligned to them
+    const int ve = a.dtype == BPA_BF16 ? 8 : 4;
+    const uintptr_t in = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+    uintptr_t out = reinterpret_cast<uintptr_t>(a.kc) | reinterpret_cast<uintptr_t>(a.vc) | a.d | a.dv;
+    int64_t strides = 0;
+    for (int i = 0; i < 2; ++i) strides |= a.ks[i] | a.vs[i];
+    for (int i = 0; i < 3; ++i) out |= static_cast<uintptr_t>(a.kcs[i]) | static_cast<uintptr_t>(a.vcs[i]);
+    const bool wide = in % 16 == 0 && strides % ve == 0 && out % ve == 0;
+    if (a.dtype == BPA_BF16) return wide ? launch<__nv_bfloat16, 8>(a, s) : launch<__nv_bfloat16, 1>(a, s);
+    return wide ? launch<float, 4>(a, s) : launch<float, 1>(a, s);
 }
 
 }  // namespace bpa

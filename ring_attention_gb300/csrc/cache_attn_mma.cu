@@ -68,18 +68,24 @@ struct Meta {
 };
 enum { F_FIRST = 1, F_LAST = 2, F_LEAD = 4, F_TRAIL = 8, F_END = 16 };
 
+// CTAs of an SM: what the sums (DVP / 4 registers of a thread) and q (DP / 8) leave, both times NT
+constexpr int occupancy(int DP, int DVP, int NT) {
+    const int regs = NT * (DVP / 4 + DP / 8);
+    return regs <= 32 ? 4 : regs <= 64 ? 3 : regs <= 96 ? 2 : 1;
+}
+
 // DP, DVP: head dims of k and v padded to 64, 128 or 256; NT: query rows of a warp / 8; SPLIT: float32
 template <int DP, int DVP, int NT, bool SPLIT>
 struct Cfg {
     static constexpr int RBK = DP < 128 ? DP : 128, RBV = DVP < 128 ? DVP : 128;   // bytes of a swizzled row
     static constexpr int HK = DP / RBK, HV = DVP / RBV;                            // 128-byte halves
     static constexpr int K_BYTES = kTile * DP, V_BYTES = kTile * DVP, STAGE = K_BYTES + V_BYTES;
-    static constexpr bool Q_REGS = !SPLIT && DP * NT <= 256;
+    static constexpr bool Q_REGS = !SPLIT && NT == 1;                              // else in shared memory
     static constexpr int QF = DP / 16 * NT * 256 * (SPLIT ? 2 : 1);                // fragments of a row tile
     static constexpr int QS = Q_REGS ? 0 : QF * (NT == 1 ? 1 : 4);                 // ... of all row tiles
     static constexpr int STATE = 8 * NT * DVP + 8 * NT * 4;                        // floats of a warp's state
     static constexpr int MERGE = kNW * STATE * 4;
-    static constexpr int OCC = DP <= 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 2 : 1);
+    static constexpr int OCC = occupancy(DP, DVP, NT);
     static constexpr int FIXED = 1024 + MERGE + 256 + QS;
     static constexpr int FIT = (233472 / OCC - 1024 - 128 - FIXED) / (STAGE + (int)sizeof(Meta));
     static constexpr int NS = FIT > 8 ? 8 : FIT;
@@ -163,6 +169,12 @@ BPA_DEV long long cost_of_request(const CacheAttnArgs& a, const Req& q, int rows
     return n * a.Hkv;
 }
 
+// total * c / parts, in 32 bits where they hold the product
+BPA_DEV long long share(long long total, int c, int parts) {
+    const unsigned long long x = static_cast<unsigned long long>(total) * c;
+    return x >> 32 ? x / parts : static_cast<uint32_t>(x) / static_cast<uint32_t>(parts);
+}
+
 template <int DP, int DVP, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     k_cache_attn_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Work w) {
@@ -198,14 +210,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         fence_mbar_init();
         s_abort = 0;
         s_r = -1;
-        rec->flags = rec->where = 0;
-        __threadfence();
     }
     if (threadIdx.x == 32 * kNW) {
         tma_prefetch(&tmK);
         tma_prefetch(&tmV);
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    launch_dependents();
+    wait_for_previous();               // nothing of the caller's is read or written before
+    if (threadIdx.x == 0) rec->flags = rec->where = 0;
 
     // ---- this CTA's share: [begin, end) of the running sum of tiles and kExtra over the items
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min(a.R, static_cast<int>(threadIdx.x) * per),
@@ -228,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     before += x - mine;
     // a share is never empty among the CTAs that take part, so the pieces of an item lie side by side
     const int parts = static_cast<int>(min(total, static_cast<long long>(w.ctas)));
-    const long long begin = cta < parts ? total * cta / parts : total, end = cta < parts ? total * (cta + 1) / parts : total;
+    const long long begin = cta < parts ? share(total, cta, parts) : total, end = cta < parts ? share(total, cta + 1, parts) : total;
     if (begin < end && begin >= before && begin < before + mine) {
         long long at = before;
         for (int r = r0; r < r1; ++r) {
@@ -826,7 +838,8 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
     __shared__ uint32_t s_flags, s_where;
     const CacheAttnArgs& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    launch_dependents();
+    wait_for_previous();
     if (c == 0 && blockIdx.y == 0) {               // the call's status word
         if (threadIdx.x == 0) s_flags = s_where = 0;
         __syncthreads();
@@ -953,7 +966,7 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     p.NT = rows <= 8 ? 1 : 2;
     p.RT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.rows_per = 8 * p.NT * p.RT;
-    p.occ = p.DP <= 128 ? (p.NT == 1 ? 3 : 2) : (p.NT == 1 ? 2 : 1);
+    p.occ = occupancy(p.DP, p.DVP, p.NT);
     p.max_ctas = kMaxSms * p.occ;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     const size_t slots = 2 * static_cast<size_t>(p.max_ctas) * p.rows_per;
@@ -978,19 +991,9 @@ cudaError_t launch(const Work& w, const CUtensorMap* maps, int rpb, cudaStream_t
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    kernel<<<w.ctas, kThreads, C::SMEM, s>>>(maps[0], maps[1], w);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, w.rows_per / rpb);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    if ((e = launch_early(dim3(w.ctas), dim3(kThreads), C::SMEM, s, kernel, maps[0], maps[1], w)) != cudaSuccess) return e;
     using E = typename std::conditional<SPLIT, float, __nv_bfloat16>::type;
-    return cudaLaunchKernelEx(&cfg, k_cache_join<DVP, E>, w, rpb, w.a.status);
+    return launch_early(dim3(w.ctas, w.rows_per / rpb), dim3(256), 0, s, k_cache_join<DVP, E>, w, rpb, w.a.status);
 }
 
 }  // namespace

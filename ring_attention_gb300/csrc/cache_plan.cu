@@ -82,12 +82,14 @@ __global__ void __launch_bounds__(kThreads) k_cache_plan(const PlanArgs a) {
         s_taken = 0;
         s_bad = 0;
     }
-    const int raw = __ldg(a.free_count), count = min(max(raw, 0), a.num_pages);
+    launch_dependents();
+    wait_for_previous();
+    const int raw = *(a.free_count), count = min(max(raw, 0), a.num_pages);
     __syncthreads();
     if (raw != count) s_bad = 1;
     for (int base = 0; base < a.R; base += kThreads) {
         const int r = base + threadIdx.x;
-        const int ctx = r < a.R ? __ldg(a.ctx + r) : 0, add = r < a.R ? __ldg(a.add + r) : 0;
+        const int ctx = r < a.R ? *(a.ctx + r) : 0, add = r < a.R ? *(a.add + r) : 0;
         const int n = max(add, 0);
         const long long row = block_scan(rows, n), last = static_cast<long long>(ctx) + n;
         const bool bad = ctx < 0 || add < 0 || last > static_cast<long long>(a.max_pages) * a.P || row + n > a.T;
@@ -124,11 +126,11 @@ __global__ void __launch_bounds__(kThreads) k_cache_plan(const PlanArgs a) {
         const int sum = (c & INT_MAX) + (s_cu[r + 1] - s_cu[r]);
         a.kv_lens[r] = c < 0 ? 0 : sum;
         if (c >= 0) a.ctx_out[r] = sum;
-        else if (a.ctx_out != a.ctx) a.ctx_out[r] = __ldg(a.ctx + r);
+        else if (a.ctx_out != a.ctx) a.ctx_out[r] = *(a.ctx + r);
     }
     for (int n = g; n < taken; n += step) {
         const int r = last_not_above(s_off, a.R, n);
-        int id = __ldg(a.free_pages + count - 1 - n);
+        int id = *(a.free_pages + count - 1 - n);
         if (id < 0 || id >= a.num_pages) {
             report(a.status, ST_CHECK, 0xCA1);
             id = -1;
@@ -144,8 +146,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_plan(const PlanArgs a) {
             if (ctx >= 0) {
                 pos = ctx + (t - s_cu[r]);
                 const int j = pos / a.P, have = ctx / a.P + (ctx % a.P != 0);
-                const int id = j < have ? __ldg(a.table + static_cast<int64_t>(r) * a.max_pages + j)
-                                        : __ldg(a.free_pages + count - 1 - (s_off[r] + j - have));
+                const int id = j < have ? *(a.table + static_cast<int64_t>(r) * a.max_pages + j)
+                                        : *(a.free_pages + count - 1 - (s_off[r] + j - have));
                 if (id >= 0 && id < a.num_pages) {
                     slot = id * a.P + (pos - j * a.P);
                 } else {
@@ -170,17 +172,19 @@ cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s) {
                                                    static_cast<int>(sizeof(int) * (3 * kPlanMaxR + 1)));
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_cache_plan, a);
 }
 
