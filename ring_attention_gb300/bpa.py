@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -77,6 +78,9 @@ class bpa_cache_batch(ctypes.Structure):
     ]
 
 
+_CACHE_SIZE, _BATCH_SIZE = ctypes.sizeof(bpa_cache_desc), ctypes.sizeof(bpa_cache_batch)
+_TWO_PACK = struct.Struct("@2q").pack
+
 _lib = None
 
 
@@ -114,13 +118,13 @@ def lib() -> ctypes.CDLL:
         L.bpa_select_blocks_noalloc.restype = ctypes.c_int
         L.bpa_set_phase_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i32]
         L.bpa_set_phase_events.restype = None
-        cp, bp, i64p = ctypes.POINTER(bpa_cache_desc), ctypes.POINTER(bpa_cache_batch), ctypes.POINTER(ctypes.c_int64)
+        # descriptors and strides of the cache calls: a pointer, byref(...) or packed bytes
         L.bpa_cache_plan.argtypes = [i32] * 5 + [P] * 12 + [sz, P]
         L.bpa_cache_plan.restype = ctypes.c_int
-        L.bpa_cache_append.argtypes = [cp, P, P, i64p, i64p, P, i32, i32, P, sz, P]
+        L.bpa_cache_append.argtypes = [P, P, P, P, P, P, i32, i32, P, sz, P]
         L.bpa_cache_append.restype = ctypes.c_int
-        L.bpa_cache_attn_workspace_size.argtypes, L.bpa_cache_attn_workspace_size.restype = [cp, bp], sz
-        L.bpa_cache_attn.argtypes = [cp, bp, P, P, P, P, sz, P]
+        L.bpa_cache_attn_workspace_size.argtypes, L.bpa_cache_attn_workspace_size.restype = [P, P], sz
+        L.bpa_cache_attn.argtypes = [P, P, P, P, P, P, sz, P]
         L.bpa_cache_attn.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -337,83 +341,88 @@ def bpa_debug_wait_timeout(workspace_buf: torch.Tensor, limit_ns: int, stream=No
 
 
 # ---- paged 8-bit key / value cache --------------------------------------------------------------
+# A generation step is a few microseconds of device time, so these calls marshal leanly: descriptors
+# are packed in one go (the layouts of bpa_cache_desc and bpa_cache_batch) and each tensor is looked
+# at once.
+_CACHE_PACK = struct.Struct("@I7iPP6qPP").pack
+_BATCH_PACK = struct.Struct("@I5iP4qPPPf3iP").pack
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_CODES = {torch.bfloat16: BPA_BF16, torch.float32: BPA_FP32}
+
+
 def _i32_buffer(t, name, shape, device=None):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor, got {t.dtype} {list(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t.data_ptr()
 
 
-class _Launch:
-    """The device of a call made current, and its stream: ``stream``, or torch's current one there.
-    Buffers that the call makes for itself on another stream than torch's are marked for it."""
+def _enter(device, stream):
+    """(guard, stream pointer, other): the device to leave again (None: it is current), the stream of
+    the call (``stream``, or torch's current one) and, where that is not torch's current one, itself."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    guard = None
+    if device.index != torch.cuda.current_device():
+        guard = torch.cuda.device(device)
+        guard.__enter__()
+    here = torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
+        return guard, here, None
+    return guard, stream.cuda_stream, stream if stream.cuda_stream != here else None
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"the tensors must be on a CUDA device, got {device}")
-        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-        self.device, self.stream = device, stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        here = torch.cuda.current_stream(self.device)
-        self.other = self.stream if self.stream is not None and self.stream.cuda_stream != here.cuda_stream else None
-        self.ptr = here.cuda_stream if self.stream is None else self.stream.cuda_stream
-        return self
+def _empty(shape, dtype, device, other):
+    """A buffer that the call makes for itself, marked for the stream it is used on."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if other is not None:
+        t.record_stream(other)
+    return t
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
 
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
+def _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype):
+    """(packed bpa_cache_desc, pages, Hkv, page_size, d, dv) of the cache's tensors."""
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"tensors must be bfloat16 or float32, got {dtype}")
+    ks, vs, kst, vst = k_cache.shape, v_cache.shape, k_cache.stride(), v_cache.stride()
+    for name, c, sh, st in (("k_cache", k_cache, ks, kst), ("v_cache", v_cache, vs, vst)):
+        if c.dtype not in _E4M3 or len(sh) != 4 or (st[3] != 1 and sh[3] != 1):
+            raise ValueError(f"{name} must be a 4-D [pages, Hkv, page_size, channels] tensor of uint8 or "
+                             "float8_e4m3fn with contiguous channels")
+    pages, Hkv, P, d = ks
+    if vs[:3] != ks[:3]:
+        raise ValueError("k_cache and v_cache must share pages, heads and page size")
+    dev = k_cache.device
+    for name, c in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if c.dtype is not torch.float32 or c.shape != ks[:2] or not c.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 [{pages}, {Hkv}] tensor")
+        if c.device != dev:
+            raise ValueError("the cache's tensors must be on one device")
+    if v_cache.device != dev:
+        raise ValueError("the cache's tensors must be on one device")
+    dv = vs[3]
+    return _CACHE_PACK(_CACHE_SIZE, code, Hkv, d, dv, P, pages, 0, k_cache.data_ptr(), v_cache.data_ptr(), kst[0],
+                       kst[1], kst[2], vst[0], vst[1], vst[2], k_scale.data_ptr(), v_scale.data_ptr()), pages, Hkv, P, d, dv
 
 
 def make_cache_desc(k_cache, v_cache, k_scale, v_scale, dtype) -> bpa_cache_desc:
-    """Fill a bpa_cache_desc from the cache's tensors (no data is touched): k_cache [pages, Hkv,
-    page_size, d], v_cache [pages, Hkv, page_size, dv] (uint8 or float8_e4m3fn, last dim
-    contiguous; a [pages, page_size, Hkv, d] cache is passed as its transpose(1, 2)), scales
-    float32 [pages, Hkv].  dtype: of the tensors beside the cache."""
-    D = bpa_cache_desc()
-    D.struct_size = ctypes.sizeof(bpa_cache_desc)
-    if dtype == torch.bfloat16:
-        D.dtype = BPA_BF16
-    elif dtype == torch.float32:
-        D.dtype = BPA_FP32
-    else:
-        raise TypeError(f"tensors must be bfloat16 or float32, got {dtype}")
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dim() != 4 or c.dtype not in (torch.uint8, torch.float8_e4m3fn) or (c.stride(3) != 1 and c.shape[3] != 1):
-            raise ValueError(f"{name} must be a 4-D [pages, Hkv, page_size, channels] tensor of uint8 or "
-                             "float8_e4m3fn with contiguous channels")
-    pages, Hkv, P, d = k_cache.shape
-    if v_cache.shape[:3] != k_cache.shape[:3]:
-        raise ValueError("k_cache and v_cache must share pages, heads and page size")
-    for name, c in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if c.dtype != torch.float32 or c.shape != (pages, Hkv) or not c.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 [{pages}, {Hkv}] tensor")
-    if not (k_cache.device == v_cache.device == k_scale.device == v_scale.device):
-        raise ValueError("the cache's tensors must be on one device")
-    D.Hkv, D.d, D.dv, D.page_size, D.num_pages = Hkv, d, v_cache.shape[3], P, pages
-    D.k_cache, D.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-    D.k_cache_strides[:] = k_cache.stride()[:3]
-    D.v_cache_strides[:] = v_cache.stride()[:3]
-    D.k_scale, D.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-    return D
+    """A bpa_cache_desc of the cache's tensors (no data is touched): k_cache [pages, Hkv, page_size,
+    d], v_cache [pages, Hkv, page_size, dv] (uint8 or float8_e4m3fn, last dim contiguous; a [pages,
+    page_size, Hkv, d] cache is passed as its transpose(1, 2)), scales float32 [pages, Hkv].
+    dtype: of the tensors beside the cache."""
+    return bpa_cache_desc.from_buffer_copy(_pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)[0])
 
 
 def _rows_strides(t, name, shape, dtype, device):
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on {device}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
-    if t.stride(2) != 1 and shape[2] != 1:
+    st = t.stride()
+    if st[2] != 1 and shape[2] != 1:
         raise ValueError(f"{name}: the head dimension must be contiguous")
-    return t.stride()[:2]
+    return st
 
 
 def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, page_size, T, ctx_lens_out=None,
@@ -432,18 +441,26 @@ def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, pa
     ins = [_i32_buffer(t, name, shape, dev) for t, name, shape in (
         (ctx_lens, "ctx_lens", (R,)), (new_lens, "new_lens", (R,)), (free_pages, "free_pages", (num_pages,)),
         (free_count, "free_count", (1,)), (page_table, "page_table", (R, max_pages)))]
-    given = [(kv_lens, "kv_lens", (R,)), (cu_q, "cu_q", (R + 1,)), (slot_map, "slot_map", (T,)),
+    given = ((kv_lens, "kv_lens", (R,)), (cu_q, "cu_q", (R + 1,)), (slot_map, "slot_map", (T,)),
              (positions, "positions", (T,)), (ctx_lens_out, "ctx_lens_out", (R,)),
-             (free_count_out, "free_count_out", (1,))]
+             (free_count_out, "free_count_out", (1,)))
     for t, name, shape in given:
         if t is not None:
             _i32_buffer(t, name, shape, dev)
-    with _Launch(dev, stream) as at:
-        outs = [at.empty(shape, torch.int32) if t is None else t for t, name, shape in given]
-        ws = at.empty(256, torch.uint8) if workspace_buf is None else workspace_buf
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        # the buffers made here are parts of one (the status word first, on 256 bytes)
+        sizes = [0 if t is not None else shape[0] for t, _, shape in given]
+        made = _empty(sum(sizes) + 64, torch.int32, dev, other).split([64] + sizes)
+        outs = [new if t is None else t for (t, _, _), new in zip(given, made[1:])]
+        ws = made[0] if workspace_buf is None else workspace_buf
         st = lib().bpa_cache_plan(R, T, int(page_size), num_pages, max_pages, *ins, *[t.data_ptr() for t in outs],
-                                  ws.data_ptr(), ws.numel(), at.ptr)
-    _raise_if(st, "bpa_cache_plan")
+                                  ws.data_ptr(), ws.numel() * ws.element_size(), ptr)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _raise_if(st, "bpa_cache_plan")
     return tuple(outs)
 
 
@@ -451,41 +468,44 @@ def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_
                      stream=None):
     """Write rows k [T, Hkv, d], v [T, Hkv, dv] into the cache's slots slot_map [T] (-1: skipped),
     updating k_cache, v_cache, k_scale, v_scale in place."""
-    D = make_cache_desc(k_cache, v_cache, k_scale, v_scale, k.dtype)
+    cache, _, Hkv, _, d, dv = _pack_cache(k_cache, v_cache, k_scale, v_scale, k.dtype)
     dev, T = k_cache.device, k.shape[0]
-    ks = (ctypes.c_int64 * 2)(*_rows_strides(k, "k", (T, D.Hkv, D.d), k.dtype, dev))
-    vs = (ctypes.c_int64 * 2)(*_rows_strides(v, "v", (T, D.Hkv, D.dv), k.dtype, dev))
+    ks = _rows_strides(k, "k", (T, Hkv, d), k.dtype, dev)
+    vs = _rows_strides(v, "v", (T, Hkv, dv), k.dtype, dev)
     slots = _i32_buffer(slot_map, "slot_map", (T,), dev)
-    with _Launch(dev, stream) as at:
-        ws = at.empty(256, torch.uint8) if workspace_buf is None else workspace_buf
-        st = lib().bpa_cache_append(ctypes.byref(D), k.data_ptr(), v.data_ptr(), ks, vs, slots, T, int(max_new),
-                                    ws.data_ptr(), ws.numel(), at.ptr)
-    _raise_if(st, "bpa_cache_append")
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        ws = _empty(256, torch.uint8, dev, other) if workspace_buf is None else workspace_buf
+        st = lib().bpa_cache_append(cache, k.data_ptr(), v.data_ptr(), _TWO_PACK(ks[0], ks[1]), _TWO_PACK(vs[0], vs[1]),
+                                    slots, T, int(max_new), ws.data_ptr(), ws.numel(), ptr)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _raise_if(st, "bpa_cache_append")
 
 
-def make_cache_batch(q, page_table, kv_lens, cu_q, *, max_q=0, causal=True, window=(-1, -1), scale=None,
-                     sink=None) -> bpa_cache_batch:
-    """Fill a bpa_cache_batch (all but o_strides) from the step's tensors (no data is touched)."""
+def _pack_batch(q, o, page_table, kv_lens, cu_q, max_q=0, causal=True, window=(-1, -1), scale=None, sink=None):
+    """Packed bpa_cache_batch; o: the output's (row, head) strides."""
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("q must be [T, Hq, d], page_table [R, max_pages]")
-    B = bpa_cache_batch()
-    B.struct_size = ctypes.sizeof(bpa_cache_batch)
-    T, Hq, d = q.shape
-    R, dev = page_table.shape[0], q.device
-    B.R, B.T, B.Hq, B.max_pages, B.max_q = R, T, Hq, page_table.shape[1], int(max_q)
-    B.q = q.data_ptr()
-    B.q_strides[:] = _rows_strides(q, "q", (T, Hq, d), q.dtype, dev)
-    B.page_table = _i32_buffer(page_table, "page_table", (R, page_table.shape[1]), dev)
-    B.kv_lens = _i32_buffer(kv_lens, "kv_lens", (R,), dev)
-    B.cu_q = _i32_buffer(cu_q, "cu_q", (R + 1,), dev)
-    B.scale = 0.0 if scale is None else float(scale)
-    B.causal = int(bool(causal))
-    B.window_left, B.window_right = (-1, -1) if window is None else (int(window[0]), int(window[1]))
-    if sink is not None:
-        if sink.dtype != torch.float32 or sink.shape != (Hq,) or not sink.is_contiguous() or sink.device != dev:
-            raise ValueError("sink must be a contiguous float32 [Hq] tensor on q's device")
-        B.sink = sink.data_ptr()
-    return B
+    T, Hq, _ = q.shape
+    dev, (R, max_pages) = q.device, page_table.shape
+    st = _rows_strides(q, "q", q.shape, q.dtype, dev)
+    if sink is not None and (sink.dtype is not torch.float32 or sink.shape != (Hq,) or not sink.is_contiguous() or
+                             sink.device != dev):
+        raise ValueError("sink must be a contiguous float32 [Hq] tensor on q's device")
+    wl, wr = (-1, -1) if window is None else window
+    return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, int(max_q), q.data_ptr(), st[0], st[1], o[0], o[1],
+                       _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
+                       _i32_buffer(cu_q, "cu_q", (R + 1,), dev), 0.0 if scale is None else float(scale),
+                       1 if causal else 0, int(wl), int(wr), 0 if sink is None else sink.data_ptr())
+
+
+def make_cache_batch(q, page_table, kv_lens, cu_q, **kw) -> bpa_cache_batch:
+    """A bpa_cache_batch (all but o_strides) of the step's tensors (no data is touched); keywords as
+    bpa_cache_attn's."""
+    return bpa_cache_batch.from_buffer_copy(_pack_batch(q, (0, 0), page_table, kv_lens, cu_q, **kw))
 
 
 def bpa_cache_attn_workspace_size(cache: bpa_cache_desc, batch: bpa_cache_batch) -> int:
@@ -497,28 +517,37 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
     """Attention of packed rows q [T, Hq, d] over the cache.  Returns (o, m, l): o [T, Hq, dv]; m and
     l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  Keywords: max_q (the most rows
     of a request, guides the choice of kernel), causal, window, scale, sink."""
-    D = make_cache_desc(k_cache, v_cache, k_scale, v_scale, q.dtype)
-    B = make_cache_batch(q, page_table, kv_lens, cu_q, **kw)
-    T, Hq, dev = B.T, B.Hq, k_cache.device
-    if q.shape[2] != D.d or q.device != dev:
-        raise ValueError("q must have k_cache's head dim and device")
+    cache, _, _, _, d, dv = _pack_cache(k_cache, v_cache, k_scale, v_scale, q.dtype)
+    dev = k_cache.device
+    if q.dim() != 3 or q.shape[2] != d or q.device != dev:
+        raise ValueError("q must be [T, Hq, d] with k_cache's head dim and device")
+    T, Hq, _ = q.shape
     for t, name in ((m, "m"), (l, "l")):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (Hq, T) or not t.is_contiguous() or
+        if t is not None and (t.dtype is not torch.float32 or t.shape != (Hq, T) or not t.is_contiguous() or
                               t.device != dev):
             raise ValueError(f"{name} must be a contiguous float32 [Hq, T] tensor on q's device")
-    if o is not None:
-        B.o_strides[:] = _rows_strides(o, "o", (T, Hq, D.dv), q.dtype, dev)
-    with _Launch(dev, stream) as at:
+    os = (Hq * dv, dv) if o is None else _rows_strides(o, "o", (T, Hq, dv), q.dtype, dev)
+    batch = _pack_batch(q, os, page_table, kv_lens, cu_q, **kw)
+    guard, ptr, other = _enter(dev, stream)
+    try:
         if o is None:
-            o = at.empty((T, Hq, D.dv), q.dtype)
-            B.o_strides[:] = o.stride()[:2]
-        m = at.empty((Hq, T), torch.float32) if m is None else m
-        l = at.empty((Hq, T), torch.float32) if l is None else l
-        need = bpa_cache_attn_workspace_size(D, B)
-        if need == 0:
-            _raise_if(BPA_ERR_INVALID_ARG, "bpa_cache_attn_workspace_size")
-        ws = at.empty(need, torch.uint8) if workspace_buf is None else workspace_buf
-        st = lib().bpa_cache_attn(ctypes.byref(D), ctypes.byref(B), o.data_ptr(), m.data_ptr(), l.data_ptr(),
-                                  ws.data_ptr(), ws.numel(), at.ptr)
-    _raise_if(st, "bpa_cache_attn")
+            o = _empty((T, Hq, dv), q.dtype, dev, other)
+        if m is None:
+            m = _empty((Hq, T), torch.float32, dev, other)
+        if l is None:
+            l = _empty((Hq, T), torch.float32, dev, other)
+        L = lib()
+        if workspace_buf is None:
+            need = L.bpa_cache_attn_workspace_size(cache, batch)
+            if need == 0:
+                _raise_if(BPA_ERR_INVALID_ARG, "bpa_cache_attn_workspace_size")
+            ws = _empty(need, torch.uint8, dev, other)
+        else:
+            ws = workspace_buf
+        st = L.bpa_cache_attn(cache, batch, o.data_ptr(), m.data_ptr(), l.data_ptr(), ws.data_ptr(), ws.numel(), ptr)
+    finally:
+        if guard is not None:
+            guard.__exit__(None, None, None)
+    if st:
+        _raise_if(st, "bpa_cache_attn")
     return o, m, l

@@ -47,13 +47,14 @@ struct CacheAttnArgs {
 };
 
 #ifdef __CUDACC__
-// Programmatic dependent launch: a kernel launched by launch_early may start while the one before it
-// on the stream still runs; it sets itself up and calls wait_for_previous() before it touches
-// anything in global memory (with plain loads, which the compiler does not move across it, until an
-// address depends on one), so the stream's order holds for everything that a caller can see.
-// launch_dependents() lets the next such kernel start as soon as every CTA of this one has.
+// Programmatic dependent launch: a kernel launched by launch_early is set up while the one before it
+// on the stream ends; it calls wait_for_previous() before it touches anything in global memory (with
+// plain loads, which the compiler does not move across it, until an address depends on one), so the
+// stream's order holds for everything that a caller can see.  No kernel here lets the next one start
+// before its own end: measured, CTAs of the next kernel then take room on some SMs while the join
+// still runs there, and a persistent kernel that is not spread evenly cost 64 requests x up to 8192
+// tokens 135 us instead of 100.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... P, typename... A>
 cudaError_t launch_early(dim3 grid, dim3 block, size_t smem, cudaStream_t s, void (*kernel)(P...), A... args) {

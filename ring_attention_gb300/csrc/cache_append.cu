@@ -66,7 +66,6 @@ BPA_DEV float scale_for(float amax) {
 // the slots over for the status word, so that nothing has to clear it before.
 template <typename E, int VE, int ROWS>
 __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
-    launch_dependents();
     wait_for_previous();
     const int lane = threadIdx.x & 31, cap = a.P * a.num_pages;
     if (blockIdx.x == gridDim.x - 1) {

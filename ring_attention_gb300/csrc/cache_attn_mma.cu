@@ -15,8 +15,8 @@
 // Bounded by the bytes of K and V.  So the CTAs are persistent and each takes an equal share of all
 // tiles of all items, whatever the lengths (an item counts kExtra tiles more, about what its start
 // and end cost); a share may begin and end inside an item.  Pieces of items go to the workspace as
-// (m, l, O) and a second, small launch joins them in ascending order (its launch overlaps the first
-// kernel: programmatic dependent launch), so nothing is added in an order that changes.  Per CTA one
+// (m, l, O) and a second, small launch joins them in ascending order, so nothing is added in an order
+// that changes.  Per CTA one
 // warp copies tiles by TMA (a page's rows at a time, swizzled) into a ring of stages and passes the
 // page's scales beside them; four warps take 16 keys of a tile each, or more of the keys for a part
 // of the rows.
@@ -40,8 +40,8 @@ namespace {
 constexpr int kTile = 64;             // keys per stage
 constexpr int kNW = 4;                // consumer warps
 constexpr int kThreads = 32 * (kNW + 1);
-constexpr int kExtra = 1;             // tiles that an item's start and end count for in a share
-constexpr int kBatch = 8;             // tiles whose page ids and scales are fetched together
+constexpr int kExtra = 6;             // tiles that an item's start and end count for in a share
+constexpr int kBatch = 8;             // tiles whose page ids and scales are fetched together (four lanes each)
 constexpr float kOff = 9.f;           // log2 of the largest fp16 weight right after M moved
 constexpr float kLazy = 6.f;          // M moves when it grows by more
 
@@ -83,8 +83,8 @@ struct Cfg {
     static constexpr bool Q_REGS = !SPLIT && NT == 1;                              // else in shared memory
     static constexpr int QF = DP / 16 * NT * 256 * (SPLIT ? 2 : 1);                // fragments of a row tile
     static constexpr int QS = Q_REGS ? 0 : QF * (NT == 1 ? 1 : 4);                 // ... of all row tiles
-    static constexpr int STATE = 8 * NT * DVP + 8 * NT * 4;                        // floats of a warp's state
-    static constexpr int MERGE = kNW * STATE * 4;
+    static constexpr int STATE = 8 * NT * DVP, STATS = 8 * NT;                     // of a warp: floats, float4
+    static constexpr int MERGE = kNW * (STATE * 4 + STATS * 16);
     static constexpr int OCC = occupancy(DP, DVP, NT);
     static constexpr int FIXED = 1024 + MERGE + 256 + QS;
     static constexpr int FIT = (233472 / OCC - 1024 - 128 - FIXED) / (STAGE + (int)sizeof(Meta));
@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         tma_prefetch(&tmK);
         tma_prefetch(&tmV);
     }
-    launch_dependents();
     wait_for_previous();               // nothing of the caller's is read or written before
     if (threadIdx.x == 0) rec->flags = rec->where = 0;
 
@@ -256,128 +255,40 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     __syncthreads();
 
     if (warp == kNW) {
-        // ---- producer: tiles of the share, item by item
-        int r = s_r, stage = 0;
+        // ---- producer: the share's segments (its part of an item) in batches of up to kBatch tiles.  A
+        // batch's page ids are asked for one batch ahead and its scales half a batch ahead.
+        struct Batch {
+            int cnt, key0, len, n, row0, hk, i0, flags;   // flags: kind; F_FIRST / F_LAST of its first / last tile
+            int id;                                       // lane 4 t + c: page of chunk c of tile t (-1: none)
+            float ks, vs;                                 // ... and its scales
+        };
+        int r = s_r, stage = 0, hk = 0, rg = 0, groups = 0, t = 0, te = 0, kind = 0;
         uint32_t phase = 1;            // the ring starts empty
-        long long left = end - begin;
+        long long left = r >= 0 ? end - begin : 0, off = s_off, at = begin;   // of the cost; `at`: the running sum at `off`
+        bool first = false, started = false, ok = true;
+        Req rq = {};
+        Tiles tl = {};
         Rec out = {};
-        bool ok = true;
         if (r >= 0) {
-            bool fresh = true;
-            const int BR = min(a.P, kTile);
-            const uint32_t copy = static_cast<uint32_t>(BR) * (DP + DVP);
-            Req rq = request_of(a, r);
+            rq = request_of(a, r);
             if (rq.bad && lane == 0) report(status, ST_CHECK, 0xCD1);
-            int groups = (rq.n * a.G + rows_per - 1) / rows_per;
-            long long off = s_off;
+            groups = (rq.n * a.G + rows_per - 1) / rows_per;
             const long long per_head = cost_of_request(a, rq, rows_per) / a.Hkv;
-            int hk = static_cast<int>(off / per_head), rg = 0;
+            hk = static_cast<int>(off / per_head);
             off -= hk * per_head;
-            Tiles tl = tiles_of(a, rq, 0, rows_per);
+            tl = tiles_of(a, rq, 0, rows_per);
             while (off >= tl.n + kExtra) {
                 off -= tl.n + kExtra;
                 tl = tiles_of(a, rq, ++rg, rows_per);
             }
-            long long at = begin;                          // the running sum at `off`
-            while (left > 0 && ok) {
-                // [off, to) of the item's cost; its first kExtra are no tiles
-                const long long to = min(static_cast<long long>(tl.n + kExtra), off + left);
-                const int t = max(static_cast<int>(off) - kExtra, 0), te = max(static_cast<int>(to) - kExtra, 0);
-                const bool lead = t > 0, trail = te < tl.n;
-                const int i0 = rg * rows_per;
-                const int kind = lead ? F_LEAD : trail ? F_TRAIL : 0;
-                if (t < te && trail && !lead) {
-                    // its pieces: up to the last CTA c with total c / parts < the end of the item's cost
-                    const long long at_end = at + (tl.n + kExtra - off);
-                    out.trail = static_cast<int>((at_end * parts + total - 1) / total) - cta;
-                    out.row0 = rq.row0;
-                    out.hk = hk;
-                    out.i0 = i0;
-                    out.nrows = min(rq.n * a.G - i0, rows_per);
-                }
-                const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
-                if (t < te) {                              // q of the item on its way to L2
-                    const int rows = min(rq.n * a.G - i0, rows_per), lines = (a.d * static_cast<int>(sizeof(E)) + 127) / 128;
-                    for (int i = lane; i < rows * lines; i += 32) {
-                        const int ri = i0 + i / lines, tok = ri / a.G;
-                        const E* q = static_cast<const E*>(a.q) + static_cast<int64_t>(rq.row0 + tok) * a.qs[0] +
-                                     static_cast<int64_t>(hk * a.G + ri - tok * a.G) * a.qs[1];
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(q) + 128 * (i % lines)));
-                    }
-                }
-                for (int b = t; b < te && ok; b += kBatch) {
-                    // lane = tile of the batch * 4 + chunk of 16 keys
-                    const int tile = b + (lane >> 2), chunk = lane & 3;
-                    const int key = (tl.first + tile) * kTile + 16 * chunk;
-                    int id = -1;
-                    if (tile < te && key < rq.len) {
-                        id = __ldg(table + key / a.P);
-                        if (id < 0 || id >= a.num_pages) {
-                            report(status, ST_CHECK, 0xCD0);
-                            id = -1;
-                        }
-                    }
-                    float ks = 0.f, vs = 0.f;
-                    if (id >= 0) {
-                        ks = __ldg(a.kscale + static_cast<int64_t>(id) * a.Hkv + hk);
-                        vs = __ldg(a.vscale + static_cast<int64_t>(id) * a.Hkv + hk);
-                    }
-                    const int cnt = min(kBatch, te - b);
-                    // tile jj of the batch into stage st
-                    auto copy_tile = [&](int jj, int st) {
-                        const bool copies = (lane >> 2) == jj && id >= 0 && (16 * chunk) % BR == 0;
-                        const uint32_t n = __popc(__ballot_sync(0xffffffffu, copies));
-                        if (lane == 0) mbar_expect_tx_only(FULL(st), n * copy);
-                        __syncwarp();
-                        if (copies) {
-                            const uint32_t to_k = sb + st * C::STAGE + 16 * chunk * C::RBK;
-                            const uint32_t to_v = sb + st * C::STAGE + C::K_BYTES + 16 * chunk * C::RBV;
-                            const int tok = key % a.P;
-                            for (int h = 0; h < C::HK; ++h)
-                                tma_load_4d(to_k + h * kTile * C::RBK, &tmK, FULL(st), 128 * h, tok, hk, id);
-                            for (int h = 0; h < C::HV; ++h)
-                                tma_load_4d(to_v + h * kTile * C::RBV, &tmV, FULL(st), 128 * h, tok, hk, id);
-                        }
-                    };
-                    // the first tiles of the share are on their way before their pages' scales are here
-                    int ahead = 0;
-                    if (fresh) {
-                        for (; ahead < min(cnt, C::NS); ++ahead) copy_tile(ahead, ahead);
-                        fresh = false;
-                    }
-                    for (int jj = 0; jj < cnt; ++jj) {
-                        if (jj >= ahead) {
-                            ok = mbar_wait(EMPTY(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD2);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            copy_tile(jj, stage);
-                        }
-                        Meta* m = meta + stage;
-                        if (lane == 0) {
-                            m->key0 = (tl.first + b + jj) * kTile;
-                            m->len = rq.len;
-                            m->n = rq.n;
-                            m->row0 = rq.row0;
-                            m->hk = hk;
-                            m->i0 = i0;
-                            m->flags = kind | (b + jj == t ? F_FIRST : 0) | (b + jj == te - 1 ? F_LAST : 0);
-                        }
-                        if ((lane >> 2) == jj) {
-                            m->ks[chunk] = ks;
-                            m->vs[chunk] = vs;
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(FULL(stage));
-                        if (++stage == C::NS) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
-                    }
-                }
-                left -= to - off;
-                at += to - off;
-                off = 0;
-                if (left > 0) {        // the next item: row group, head, request
+        }
+        const int chunk = lane & 3;
+        auto next_batch = [&](Batch& b) {
+            b.cnt = 0;
+            b.id = -1;
+            while (t >= te) {
+                if (left <= 0) return;
+                if (started) {         // the next item: row group, head, request
                     if (++rg == groups) {
                         rg = 0;
                         if (++hk == a.Hkv) {
@@ -389,14 +300,132 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                             } while (rq.n == 0);
                             if (r >= a.R) {
                                 if (lane == 0) report(status, ST_CHECK, 0xCD5);
-                                break;
+                                left = 0;
+                                return;
                             }
                             groups = (rq.n * a.G + rows_per - 1) / rows_per;
                         }
                     }
                     tl = tiles_of(a, rq, rg, rows_per);
                 }
+                started = true;
+                // [off, to) of the item's cost; its first kExtra are no tiles
+                const long long to = min(static_cast<long long>(tl.n + kExtra), off + left);
+                t = max(static_cast<int>(off) - kExtra, 0);
+                te = max(static_cast<int>(to) - kExtra, 0);
+                const bool lead = t > 0, trail = te < tl.n;
+                kind = lead ? F_LEAD : trail ? F_TRAIL : 0;
+                first = true;
+                const int i0 = rg * rows_per, rows = min(rq.n * a.G - i0, rows_per);
+                if (t < te) {
+                    if (trail && !lead) {
+                        // its pieces: up to the last CTA c with total c / parts < the end of the item's cost
+                        const long long at_end = at + (tl.n + kExtra - off);
+                        out.trail = static_cast<int>((at_end * parts + total - 1) / total) - cta;
+                        out.row0 = rq.row0;
+                        out.hk = hk;
+                        out.i0 = i0;
+                        out.nrows = rows;
+                    }
+                    const int lines = (a.d * static_cast<int>(sizeof(E)) + 127) / 128;   // q on its way to L2
+                    for (int i = lane; i < rows * lines; i += 32) {
+                        const int ri = i0 + i / lines, tok = ri / a.G;
+                        const E* q = static_cast<const E*>(a.q) + static_cast<int64_t>(rq.row0 + tok) * a.qs[0] +
+                                     static_cast<int64_t>(hk * a.G + ri - tok * a.G) * a.qs[1];
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(q) + 128 * (i % lines)));
+                    }
+                }
+                left -= to - off;
+                at += to - off;
+                off = 0;
             }
+            b.cnt = min(kBatch, te - t);
+            b.key0 = (tl.first + t) * kTile;
+            b.len = rq.len;
+            b.n = rq.n;
+            b.row0 = rq.row0;
+            b.hk = hk;
+            b.i0 = rg * rows_per;
+            t += b.cnt;
+            b.flags = kind | (first ? F_FIRST : 0) | (t == te ? F_LAST : 0);
+            first = false;
+            const int key = b.key0 + 16 * lane;
+            if ((lane >> 2) < b.cnt && key < b.len) {
+                b.id = a.table[static_cast<int64_t>(r) * a.max_pages + key / a.P];
+                if (b.id < 0) b.id = -2;
+            }
+        };
+        auto checked = [&](Batch& b) {             // ids outside the cache: reported, not copied
+            if (b.id == -2 || b.id >= a.num_pages) {
+                report(status, ST_CHECK, 0xCD0);
+                b.id = -1;
+            }
+        };
+        auto fetch_scales = [&](Batch& b) {
+            checked(b);
+            b.ks = b.vs = 0.f;
+            if (b.id >= 0) {
+                b.ks = a.kscale[static_cast<int64_t>(b.id) * a.Hkv + b.hk];
+                b.vs = a.vscale[static_cast<int64_t>(b.id) * a.Hkv + b.hk];
+            }
+        };
+        const int BR = min(a.P, kTile);
+        const uint32_t copy = static_cast<uint32_t>(BR) * (DP + DVP);
+        auto copy_tile = [&](const Batch& b, int jj, int st) {   // tile jj of the batch into stage st
+            const bool copies = (lane >> 2) == jj && b.id >= 0 && (16 * chunk) % BR == 0;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, copies));
+            if (lane == 0) mbar_expect_tx_only(FULL(st), n * copy);
+            __syncwarp();
+            if (copies) {
+                const uint32_t to_k = sb + st * C::STAGE + 16 * chunk * C::RBK;
+                const uint32_t to_v = sb + st * C::STAGE + C::K_BYTES + 16 * chunk * C::RBV;
+                const int tok = (b.key0 + 16 * lane) % a.P;
+                for (int h = 0; h < C::HK; ++h) tma_load_4d(to_k + h * kTile * C::RBK, &tmK, FULL(st), 128 * h, tok, b.hk, b.id);
+                for (int h = 0; h < C::HV; ++h) tma_load_4d(to_v + h * kTile * C::RBV, &tmV, FULL(st), 128 * h, tok, b.hk, b.id);
+            }
+        };
+        Batch cur, nxt;
+        next_batch(cur);
+        checked(cur);
+        // the first tiles are on their way before their pages' scales are here
+        int ahead = 0;
+        for (; ahead < min(cur.cnt, C::NS); ++ahead) copy_tile(cur, ahead, ahead);
+        fetch_scales(cur);
+        next_batch(nxt);
+        while (cur.cnt && ok) {
+            for (int jj = 0; jj < cur.cnt; ++jj) {
+                if (jj == cur.cnt / 2) fetch_scales(nxt);
+                if (jj >= ahead) {
+                    ok = mbar_wait(EMPTY(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD2);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    copy_tile(cur, jj, stage);
+                }
+                Meta* m = meta + stage;
+                if (lane == 0) {
+                    m->key0 = cur.key0 + jj * kTile;
+                    m->len = cur.len;
+                    m->n = cur.n;
+                    m->row0 = cur.row0;
+                    m->hk = cur.hk;
+                    m->i0 = cur.i0;
+                    m->flags = (cur.flags & (F_LEAD | F_TRAIL)) | (jj == 0 ? cur.flags & F_FIRST : 0) |
+                               (jj == cur.cnt - 1 ? cur.flags & F_LAST : 0);
+                }
+                if ((lane >> 2) == jj) {
+                    m->ks[chunk] = cur.ks;
+                    m->vs[chunk] = cur.vs;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(FULL(stage));
+                if (++stage == C::NS) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            ahead = 0;
+            cur = nxt;
+            next_batch(nxt);
         }
         if (ok) {                          // one more stage, without a tile: the end
             ok = __all_sync(0xffffffffu, mbar_wait(EMPTY(stage), phase, const_cast<volatile int*>(&s_abort), status, 0xCD2));
@@ -710,121 +739,85 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                     l[nt][e] = __fadd_rn(__fmul_rn(l[nt][e], ex2(m[nt][e] - ref)), __fmul_rn(y, ex2(x - ref)));
                     m[nt][e] = n;
                 }
+        // Each warp's (m, l, M) and sums go to shared memory; a thread per row turns them into the
+        // slices' factors, then all threads add the slices up.  Rolled loops: this code runs seldom, and
+        // its instructions come from far.
         constexpr int CV = (DVP < 128 ? DVP : 128) / 8, F = DVP / 16;
-        float* state = merge + rt * C::STATE;              // slice k of the row tile: k * RT states further
-        const int RT = kNW / slices;
-        if (slices > 1) {
-            float* buf = state + slice * RT * C::STATE;
+        const int RT = kNW / slices, rows = min(nr - i0, RT * C::STATS);
+        float4* stats = reinterpret_cast<float4*>(merge + kNW * C::STATE);   // [slice][row of the item]
+        if (g == 0)
 #pragma unroll
-            for (int i = 0; i < F; ++i)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    *reinterpret_cast<float4*>(buf + ((i * NT + nt) * 32 + lane) * 4) =
-                        make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
-            if (g == 0)
+                for (int e = 0; e < 2; ++e)
+                    stats[warp * C::STATS + 8 * nt + 2 * j + e] = make_float4(m[nt][e], l[nt][e], M[nt][e], 0.f);
+        float4* buf = reinterpret_cast<float4*>(merge + warp * C::STATE) + lane;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < F; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float4*>(buf + 8 * NT * DVP + (8 * nt + 2 * j + e) * 4) =
-                            make_float4(m[nt][e], l[nt][e], M[nt][e], 0.f);
-            if (!consumers_meet()) return;
-        }
-        // every warp of a row tile writes its share of the channels
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x[2][kNW];                               // factors of the slices' sums, per row
-            float* part[2];
-            E* out[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = rt * 8 * NT + 8 * nt + 2 * j + e, ri = i0 + row;
-                part[e] = nullptr;
-                out[e] = nullptr;
-                float mm = m[nt][e], ll = l[nt][e], MS[kNW] = {M[nt][e], -INFINITY, -INFINITY, -INFINITY};
-                if (slices > 1) {
-                    float4 b[kNW];
-                    mm = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < kNW; ++k) {
-                        b[k] = k < slices ? *reinterpret_cast<const float4*>(state + k * RT * C::STATE + 8 * NT * DVP +
-                                                                             (8 * nt + 2 * j + e) * 4)
-                                          : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                        mm = fmaxf(mm, b[k].x);
-                        MS[k] = b[k].z;
-                    }
-                    ll = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kNW; ++k) ll += b[k].y * ex2(b[k].x - (mm == -INFINITY ? 0.f : mm));
-                }
-                float norm = 1.f;
-                if (ri < nr) {
-                    const int tok = ri / a.G, head = hk * a.G + ri - tok * a.G;
-                    if (flags & (F_LEAD | F_TRAIL)) {
-                        const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
-                        part[e] = w.part + slot * DVP + CV * g;
-                        if (slice == 0 && g == 0) w.ml[slot] = make_float2(mm, ll);
-                    } else {
-                        float lf = ll, mf = mm;
-                        if (a.sink) {
-                            const float sk = __ldg(a.sink + head) * kLog2e;
-                            mf = fmaxf(mm, sk);
-                            norm = mm == -INFINITY ? 1.f : ex2(mm - mf);
-                            lf = ll * norm + ex2(sk - mf);
-                        }
-                        if (a.m && slice == 0 && g == 0) {
-                            a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = mf == -INFINITY ? mf : mf * kLn2;
-                            a.l[static_cast<int64_t>(head) * a.T + row0 + tok] = lf;
-                        }
-                        norm = lf == 0.f ? 0.f : norm / lf;
-                        out[e] = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] +
-                                 static_cast<int64_t>(head) * a.os[1] + CV * g;
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kNW; ++k)
-                    x[e][k] = (MS[k] == -INFINITY ? (norm != norm ? norm : 0.f)
-                                                  : ex2(MS[k] - kOff - (mm == -INFINITY ? 0.f : mm)) * norm);
+            for (int nt = 0; nt < NT; ++nt)
+                buf[(i * NT + nt) * 32] = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+        if (!consumers_meet()) return;
+        for (int row = threadIdx.x; row < rows; row += 32 * kNW) {
+            const int tok = (i0 + row) / a.G, head = hk * a.G + (i0 + row) - tok * a.G;
+            float mm = -INFINITY, ll = 0.f;
+            for (int k = 0; k < slices; ++k) mm = fmaxf(mm, stats[k * RT * C::STATS + row].x);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            for (int k = 0; k < slices; ++k) {
+                const float4 b = stats[k * RT * C::STATS + row];
+                ll += b.y * ex2(b.x - ref);
             }
-            auto put = [&](int i, float4 v) {              // fragment i: channels 2 (i % (CV / 2)) and the next of a half
-                const int c = (i / (CV / 2)) * 128 + (i % (CV / 2)) * 2;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float y0 = e ? v.y : v.x, y1 = e ? v.w : v.z;
-                    if (part[e]) *reinterpret_cast<float2*>(part[e] + c) = make_float2(y0, y1);
-                    if (out[e] && CV * g + c < a.dv) {
-                        if (!SPLIT && w.vec_o) {
-                            *reinterpret_cast<uint32_t*>(out[e] + c) = pack_bf16(y0, y1);
-                        } else {
-                            out[e][c] = static_cast<E>(y0);
-                            out[e][c + 1] = static_cast<E>(y1);
-                        }
-                    }
-                }
-            };
-            if (slices == 1) {
-#pragma unroll
-                for (int i = 0; i < F; ++i)
-                    put(i, make_float4(acc[i][nt][0] * x[0][0], acc[i][nt][1] * x[1][0], acc[i][nt][2] * x[0][0],
-                                       acc[i][nt][3] * x[1][0]));
+            float norm = 1.f;
+            if (flags & (F_LEAD | F_TRAIL)) {
+                w.ml[(2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row] = make_float2(mm, ll);
             } else {
-                const int each = F / slices;
-                for (int i = slice * each; i < (slice + 1) * each; ++i) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < kNW; ++k)
-                        if (k < slices) {
-                            const float4 b = *reinterpret_cast<const float4*>(state + k * RT * C::STATE + ((i * NT + nt) * 32 + lane) * 4);
-                            v.x = fmaf(b.x, x[0][k], v.x);
-                            v.y = fmaf(b.y, x[1][k], v.y);
-                            v.z = fmaf(b.z, x[0][k], v.z);
-                            v.w = fmaf(b.w, x[1][k], v.w);
-                        }
-                    put(i, v);
+                float lf = ll, mf = mm;
+                if (a.sink) {
+                    const float sk = __ldg(a.sink + head) * kLog2e;
+                    mf = fmaxf(mm, sk);
+                    norm = mm == -INFINITY ? 1.f : ex2(mm - mf);
+                    lf = ll * norm + ex2(sk - mf);
+                }
+                if (a.m) {
+                    a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = mf == -INFINITY ? mf : mf * kLn2;
+                    a.l[static_cast<int64_t>(head) * a.T + row0 + tok] = lf;
+                }
+                norm = lf == 0.f ? 0.f : norm / lf;
+            }
+            for (int k = 0; k < slices; ++k) {
+                float4& b = stats[k * RT * C::STATS + row];
+                b.w = b.z == -INFINITY ? (norm != norm ? norm : 0.f) : ex2(b.z - kOff - ref) * norm;
+            }
+        }
+        if (!consumers_meet()) return;
+        // two channels of a row at a time
+        for (int x = threadIdx.x; x < rows * (8 * F); x += 32 * kNW) {
+            const int row = x / (8 * F), y = x - row * (8 * F), gg = y / F, i = y - gg * F;
+            const int c = (i / (CV / 2)) * 128 + CV * gg + (i % (CV / 2)) * 2;
+            const int tile = row / C::STATS, r = row - tile * C::STATS;
+            const float* at = merge + tile * C::STATE + ((i * NT + (r >> 3)) * 32 + gg * 4 + ((r & 7) >> 1)) * 4 + (r & 1);
+            float y0 = 0.f, y1 = 0.f;
+            for (int k = 0; k < slices; ++k) {
+                const float f0 = stats[k * RT * C::STATS + row].w;
+                y0 = fmaf(at[k * RT * C::STATE], f0, y0);
+                y1 = fmaf(at[k * RT * C::STATE + 2], f0, y1);
+            }
+            if (flags & (F_LEAD | F_TRAIL)) {
+                const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
+                *reinterpret_cast<float2*>(w.part + slot * DVP + c) = make_float2(y0, y1);
+            } else if (c < a.dv) {
+                const int tok = (i0 + row) / a.G, head = hk * a.G + (i0 + row) - tok * a.G;
+                E* o = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] +
+                       static_cast<int64_t>(head) * a.os[1] + c;
+                if (!SPLIT && w.vec_o) {
+                    *reinterpret_cast<uint32_t*>(o) = pack_bf16(y0, y1);
+                } else {
+                    o[0] = static_cast<E>(y0);
+                    o[1] = static_cast<E>(y1);
                 }
             }
         }
-        if (slices > 1 && !consumers_meet()) return;       // the states may be written again
+        if (!consumers_meet()) return;                     // the buffers may be written again
     }
 }
 
@@ -838,7 +831,6 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
     __shared__ uint32_t s_flags, s_where;
     const CacheAttnArgs& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
-    launch_dependents();
     wait_for_previous();
     if (c == 0 && blockIdx.y == 0) {               // the call's status word
         if (threadIdx.x == 0) s_flags = s_where = 0;

@@ -82,7 +82,6 @@ __global__ void __launch_bounds__(kThreads) k_cache_plan(const PlanArgs a) {
         s_taken = 0;
         s_bad = 0;
     }
-    launch_dependents();
     wait_for_previous();
     const int raw = *(a.free_count), count = min(max(raw, 0), a.num_pages);
     __syncthreads();
