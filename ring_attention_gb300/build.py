@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libbpa.so")
 
 SOURCES = ["fwd_tc.cu", "fwd_tc_drop.cu", "fwd_band.cu", "api.cu", "simt.cu", "aux.cu", "bwd_tc.cu", "select.cu", "gather.cu",
            "noalloc.cu", "cache_api.cu", "cache_plan.cu", "cache_append.cu", "cache_attn.cu",
-           "cache_attn_mma.cu"]
+           "cache_attn_mma.cu", "cache_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

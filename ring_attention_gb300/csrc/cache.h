@@ -9,6 +9,7 @@
 
 namespace bpa {
 
+constexpr int kFewRows = 64;         // query rows of a kv head up to which a request is one of few rows
 constexpr int kPlanMaxR = 8192;      // requests of one plan: their lengths and offsets sit in shared memory
 
 struct PlanArgs {
@@ -110,6 +111,13 @@ struct CacheBox {
 bool cache_attn_mma_supported(const CacheAttnArgs& a);
 size_t cache_attn_mma_workspace(const CacheAttnArgs& a);
 CacheBox cache_attn_mma_box(const CacheAttnArgs& a);
-cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, cudaStream_t s);
+// few_only: requests of more than kFewRows rows are left to launch_cache_attn_tc, which has run before
+// on the same status word.
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, bool few_only, cudaStream_t s);
+
+// Tensor-core kernel for requests of more than kFewRows rows (bf16, head dims in steps of 16 up to 128,
+// pages in steps of 16 tokens); the others are left alone.  counter: zero before the launch.
+bool cache_attn_tc_supported(const CacheAttnArgs& a);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, uint32_t* counter, cudaStream_t s);
 
 }  // namespace bpa

@@ -263,9 +263,18 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
         const CacheBox box = cache_attn_mma_box(a);
         CUtensorMap maps[2];
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows) &&
-            make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows))
-            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), s),
+            make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows)) {
+            // requests of many rows first (none where no request may have so many)
+            const bool many = static_cast<int64_t>(a.max_q) * a.G > kFewRows && cache_attn_tc_supported(a);
+            if (many) {
+                st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
+                if (st != BPA_OK) return st;
+                st = cuda_status(launch_cache_attn_tc(a, a.status + 2, s), "cache attention launch");
+                if (st != BPA_OK) return st;
+            }
+            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), many, s),
                                "cache attention launch");
+        }
     }
     st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
     if (st != BPA_OK || a.T == 0) return st;

@@ -56,6 +56,7 @@ static_assert(sizeof(Rec) == 32, "record");
 struct Work {
     CacheAttnArgs a;
     int rows_per, ctas;               // rows of an item, CTAs
+    int few_only;                     // requests of more than kFewRows rows are another kernel's
     int vec_q, vec_o;                 // four elements of q, two of o at a time
     Rec* recs;                        // [ctas]
     float2* ml;                       // [2 ctas][rows_per] (m in log2 units, l)
@@ -148,6 +149,13 @@ BPA_DEV void ld_q4(const __nv_bfloat16* p, float (&v)[4]) {
     v[3] = __uint_as_float(x.y & 0xffff0000u);
 }
 
+// Request r, without rows where another kernel takes it.
+BPA_DEV Req own_request(const Work& w, int r) {
+    Req q = request_of(w.a, r);
+    if (w.few_only && q.n * w.a.G > kFewRows) q.n = 0;
+    return q;
+}
+
 // Key tiles of row group rg: first tile and count (at least one, so that rows without keys are
 // written too; such a tile holds no allowed key).
 struct Tiles {
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min(a.R, static_cast<int>(threadIdx.x) * per),
               r1 = min(a.R, r0 + per);
     long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += cost_of_request(a, request_of(a, r), rows_per);
+    for (int r = r0; r < r1; ++r) mine += cost_of_request(a, own_request(w, r), rows_per);
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     if (begin < end && begin >= before && begin < before + mine) {
         long long at = before;
         for (int r = r0; r < r1; ++r) {
-            const long long n = cost_of_request(a, request_of(a, r), rows_per);
+            const long long n = cost_of_request(a, own_request(w, r), rows_per);
             if (begin < at + n) {
                 s_r = r;
                 s_off = begin - at;
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         Tiles tl = {};
         Rec out = {};
         if (r >= 0) {
-            rq = request_of(a, r);
+            rq = own_request(w, r);
             if (rq.bad && lane == 0) report(status, ST_CHECK, 0xCD1);
             groups = (rq.n * a.G + rows_per - 1) / rows_per;
             const long long per_head = cost_of_request(a, rq, rows_per) / a.Hkv;
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                             hk = 0;
                             do {
                                 if (++r >= a.R) break;      // only if the lengths changed during the call
-                                rq = request_of(a, r);
+                                rq = own_request(w, r);
                                 if (rq.bad && rq.n && lane == 0) report(status, ST_CHECK, 0xCD1);
                             } while (rq.n == 0);
                             if (r >= a.R) {
@@ -842,8 +850,12 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
             }
         __syncthreads();
         if (threadIdx.x == 0) {
-            out_status[0] = s_flags;
-            out_status[1] = s_where;
+            if (!w.few_only) {
+                out_status[0] = s_flags;
+                out_status[1] = s_where;
+            } else if (s_flags) {                  // beside what the other kernel has reported
+                report(out_status, s_flags, s_where);
+            }
         }
     }
     const Rec rec = w.recs[c];
@@ -1006,12 +1018,13 @@ CacheBox cache_attn_mma_box(const CacheAttnArgs& a) {
     return {p.DP < 128 ? p.DP : 128, p.DVP < 128 ? p.DVP : 128, a.P < kTile ? a.P : kTile};
 }
 
-cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, cudaStream_t s) {
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, bool few_only, cudaStream_t s) {
     Plan p;
     if (!plan_of(a, p)) return cudaErrorInvalidValue;
     Work w;
     w.a = a;
     w.rows_per = p.rows_per;
+    w.few_only = few_only;
     // no more CTAs than the longest table rows have tiles
     const int64_t groups = (static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G + p.rows_per - 1) / p.rows_per;
     const int64_t most = ((static_cast<int64_t>(a.max_pages) * a.P + kTile - 1) / kTile + kExtra) * a.Hkv * a.R * groups;
