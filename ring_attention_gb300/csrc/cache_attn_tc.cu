@@ -41,8 +41,8 @@ constexpr float kTau = 8.f, kOff = 7.f;
 constexpr float kFar = 100.f;         // log2 of the largest ratio of the v scales below the item's first
 
 struct TileMeta {
-    int id[8];                        // page of each 16 keys, -1: none
-    int key0, len, hk, end;
+    int64_t k[8], v[8];               // where each 16 keys begin in k_cache, v_cache (-1: no page)
+    int key0, len, end, pad;
     float a[8], lv[8], e[8];          // k scale * softmax scale * log2(e); log2 v scale; 2^(lv0 - lv)
 };
 struct Item {
@@ -90,8 +90,8 @@ BPA_DEV uint32_t cvt_hi(uint32_t four) {
 }
 
 // One pass over the row's 128 scores: weights (fp16 pairs), the row's sum of W e, and the maxima of u
-// and x.  EDGE: keys outside [kmin, kmax] are masked.  WEIGHTS false: the maxima only.
-template <bool EDGE, bool WEIGHTS>
+// and x.  EDGE: keys outside [kmin, kmax] are masked.
+template <bool EDGE>
 BPA_DEV void pass(uint32_t tS, const TileMeta* mt, float f_row, float mref, int k0, int kmin, int kmax, uint32_t (&pk)[64],
                   float& sum, float& umax, float& xmax) {
     sum = 0.f;
@@ -120,22 +120,18 @@ BPA_DEV void pass(uint32_t tS, const TileMeta* mt, float f_row, float mref, int 
                     y1 += b;
                 } else {
                     mx = fmax3(mx, s0, s1);
-                    if (WEIGHTS) f2_unpack(ffma2(f2_pack(s0, s1), a2, b2), y0, y1);
+                    f2_unpack(ffma2(f2_pack(s0, s1), a2, b2), y0, y1);
                 }
-                if (WEIGHTS) {
-                    const float w0 = ex2(y0), w1 = ex2(y1);
-                    r2 = fadd2(r2, f2_pack(w0, w1));
-                    pk[8 * ch + i] = h2(w0, w1);
-                }
+                const float w0 = ex2(y0), w1 = ex2(y1);
+                r2 = fadd2(r2, f2_pack(w0, w1));
+                pk[8 * ch + i] = h2(w0, w1);
             }
             const float x = EDGE ? mx : mx * a;                   // a >= 0
             umax = fmaxf(umax, x + lv);
             xmax = fmaxf(xmax, x);
-            if (WEIGHTS) {
-                float p, q;
-                f2_unpack(r2, p, q);
-                sum = fmaf(p + q, mt->e[ch], sum);
-            }
+            float p, q;
+            f2_unpack(r2, p, q);
+            sum = fmaf(p + q, mt->e[ch], sum);
         }
     }
 }
@@ -194,14 +190,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         const int wq = warp - 12, c = lane & 7, r4 = lane >> 3;        // 16-byte piece of a row; row of four
         uint4 kr[8], vr[8];
-        // this thread's pieces of a tile: rows 32 wq + 4 i + r4
-        auto load = [&](const TileMeta* mt, const uint8_t* base, const int64_t* st, int ch, int width, uint4 (&x)[8]) {
+        // this thread's pieces of a tile: rows 32 wq + 4 i + r4, so two stretches of 16 keys
+        auto load = [&](const TileMeta* mt, const int64_t* starts, const uint8_t* base, int64_t step, int ch, uint4 (&x)[8]) {
+            const int left = mt->len - mt->key0 - 32 * wq - r4;        // rows of this thread that are keys: 4 i < left
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 32 * wq + 4 * i + r4, key = mt->key0 + row, id = mt->id[row >> 4];
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (id >= 0 && key < mt->len && 16 * c < ch && 16 * c < width)
-                    x[i] = *reinterpret_cast<const uint4*>(base + id * st[0] + mt->hk * st[1] + (key % a.P) * st[2] + 16 * c);
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = starts[2 * wq + h];
+                const uint8_t* p = base + at + r4 * step + 16 * c;
+                const bool some = at >= 0 && 16 * c < ch;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[4 * h + i] = make_uint4(0, 0, 0, 0);
+                    if (some && 16 * h + 4 * i < left) x[4 * h + i] = *reinterpret_cast<const uint4*>(p + 4 * i * step);
+                }
             }
         };
         auto store = [&](uint8_t* tile, int width, const uint4 (&x)[8]) {
@@ -221,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
         bool ok = wait(C::B_MF, 0, 0xE0);
         bool more = ok && !metas[0].end;
         if (more) {
-            load(&metas[0], a.kc, a.kcs, a.d, D, kr);
-            load(&metas[0], a.vc, a.vcs, a.dv, DV, vr);
+            load(&metas[0], metas[0].k, a.kc, a.kcs[2], a.d, kr);
+            load(&metas[0], metas[0].v, a.vc, a.vcs[2], a.dv, vr);
         }
         for (; ok && more; ++t) {
             const int st = t % C::NS, use = t / C::NS;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
             if (lane == 0) mbar_arrive(BAR(C::B_KF + st));
             if (!(ok = wait(C::B_MF + next, (t + 1) / kMetas, 0xE2))) break;
             more = !metas[next].end;
-            if (more) load(&metas[next], a.kc, a.kcs, a.d, D, kr);
+            if (more) load(&metas[next], metas[next].k, a.kc, a.kcs[2], a.d, kr);
             if (use > 0 && !(ok = wait(C::B_VE + st, use - 1, 0xE3))) break;
             store(smem + C::OFF_V + st * C::V_BYTES, DV, vr);
             fence_proxy_async_smem();
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 mbar_arrive(BAR(C::B_VF + st));
                 mbar_arrive(BAR(C::B_ME + t % kMetas));                // its codes have been loaded
             }
-            if (more) load(&metas[next], a.vc, a.vcs, a.dv, DV, vr);
+            if (more) load(&metas[next], metas[next].v, a.vc, a.vcs[2], a.dv, vr);
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -305,26 +306,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 row_keys(a, rq, i0 / a.G, lo, y);
                 row_keys(a, rq, last / a.G, y, hi);
                 const int first = lo <= hi ? lo / BN : 0, tiles = lo <= hi ? hi / BN - first + 1 : 0;
-                // lanes 0..7: the page of 16 keys of a tile, one tile ahead
+                // lanes 0..7: 16 keys each; a tile's page ids are asked for two tiles ahead, its scales one
                 const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
-                auto fetch = [&](int j, int& id, float& ks, float& vs) {
+                auto page_of = [&](int j) {
                     const int key = (first + j) * BN + 16 * lane;
-                    id = -1;
+                    return lane < 8 && j < tiles && key < rq.len ? table[key / a.P] : INT_MIN;
+                };
+                auto scales_of = [&](int& id, float& ks, float& vs) {
                     ks = vs = 0.f;
-                    if (lane < 8 && j < tiles && key < rq.len) {
-                        id = table[key / a.P];
-                        if (id < 0 || id >= a.num_pages) {
-                            report(a.status, ST_CHECK, 0xCE0);
-                            id = -1;
-                        } else {
-                            ks = a.kscale[static_cast<int64_t>(id) * a.Hkv + hk];
-                            vs = a.vscale[static_cast<int64_t>(id) * a.Hkv + hk];
-                        }
+                    if (id >= 0 && id < a.num_pages) {
+                        ks = a.kscale[static_cast<int64_t>(id) * a.Hkv + hk];
+                        vs = a.vscale[static_cast<int64_t>(id) * a.Hkv + hk];
+                    } else {
+                        if (id != INT_MIN) report(a.status, ST_CHECK, 0xCE0);
+                        id = -1;
                     }
                 };
-                int id;
+                int id = page_of(0), id1 = page_of(1);
                 float ks, vs;
-                fetch(0, id, ks, vs);
+                scales_of(id, ks, vs);
                 const unsigned some = __ballot_sync(0xffffffffu, vs > 0.f);
                 const float lv0 = some ? __log2f(__shfl_sync(0xffffffffu, vs, __ffs(some) - 1)) : 0.f;
                 if (lane == 0) {
@@ -333,15 +333,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 }
                 bool ok = true;
                 for (int j = 0; j < tiles; ++j, ++t) {
-                    const int sl = t % kMetas;
-                    int id2;
-                    float ks2, vs2;
-                    fetch(j + 1, id2, ks2, vs2);
+                    const int sl = t % kMetas, id2 = page_of(j + 2);
+                    float ks1, vs1;
+                    scales_of(id1, ks1, vs1);
                     if (t >= kMetas && !(ok = wait(C::B_ME + sl, t / kMetas - 1, 0xE6))) break;
                     TileMeta* m = metas + sl;
                     if (lane < 8) {
+                        const int tok = ((first + j) * BN + 16 * lane) % a.P;
                         const float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : lv0 - kFar;
-                        m->id[lane] = id;
+                        m->k[lane] = id < 0 ? -1 : id * a.kcs[0] + hk * a.kcs[1] + tok * a.kcs[2];
+                        m->v[lane] = id < 0 ? -1 : id * a.vcs[0] + hk * a.vcs[1] + tok * a.vcs[2];
                         m->a[lane] = ks * a.scale * kLog2e;
                         m->lv[lane] = lv;
                         m->e[lane] = ex2(lv0 - lv);
@@ -349,14 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                     if (lane == 0) {
                         m->key0 = (first + j) * BN;
                         m->len = rq.len;
-                        m->hk = hk;
                         m->end = 0;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_MF + sl));
-                    id = id2;
-                    ks = ks2;
-                    vs = vs2;
+                    id = id1;
+                    ks = ks1;
+                    vs = vs1;
+                    id1 = id2;
                 }
                 if (!ok) break;
             }
@@ -503,39 +504,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 const bool edge = __any_sync(0xffffffffu, k0 < kmin || k0 + BN - 1 > kmax);
                 uint32_t pk[64];
                 float sum, um, x;
-                bool redo = j == 0;
-                if (!redo) {
+                // a second round where a row of the warp moves its M (always for the first tile)
+#pragma unroll 1
+                for (;;) {
                     const float mref = M == -INFINITY ? 0.f : M - kOff;
-                    if (edge) pass<true, true>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, um, x);
-                    else pass<false, true>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, um, x);
-                    redo = __any_sync(0xffffffffu, um > M + kTau);
-                }
-                if (redo) {                    // the first tile, or a row of the warp moves its M
-                    if (j == 0) {
-                        if (edge) pass<true, false>(tS, mt, f_row, 0.f, k0, kmin, kmax, pk, sum, um, x);
-                        else pass<false, false>(tS, mt, f_row, 0.f, k0, kmin, kmax, pk, sum, um, x);
-                    }
+                    if (edge) pass<true>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, um, x);
+                    else pass<false>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, um, x);
+                    if (!__any_sync(0xffffffffu, um > M + kTau)) break;
                     float fac = 1.f;
                     if (um > M + kTau) {
                         fac = M == -INFINITY ? 0.f : ex2(M - um);
                         M = um;
                         L *= fac;
                     }
-                    if (j > 0 && __any_sync(0xffffffffu, fac != 1.f)) {
-                        // S(j) is complete, so every earlier W V has been added to O
+                    if (j == 0) continue;
+                    // S(j) is complete, so every earlier W V has been added to O
 #pragma unroll 1
-                        for (int cc = 0; cc < DV / 32; ++cc) {
-                            uint32_t r[32];
-                            tmem_ld32(tO + cc * 32, r);
+                    for (int cc = 0; cc < DV / 32; ++cc) {
+                        uint32_t r[32];
+                        tmem_ld32(tO + cc * 32, r);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fac);
-                            tmem_st32(tO + cc * 32, r);
-                        }
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fac);
+                        tmem_st32(tO + cc * 32, r);
                     }
-                    const float mref = M == -INFINITY ? 0.f : M - kOff;
-                    float u2, x2;
-                    if (edge) pass<true, true>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, u2, x2);
-                    else pass<false, true>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, u2, x2);
                 }
                 L += sum;
                 xm = fmaxf(xm, x);
