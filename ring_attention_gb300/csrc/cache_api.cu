@@ -89,7 +89,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 bool make_cache_map(CUtensorMap* map, const uint8_t* base, const CacheAttnArgs& a, int channels, const int64_t st[3],
-                    int box_cols, int box_rows) {
+                    int box_cols, int box_rows, bool swizzled) {
     static const EncodeTiledFn enc = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -111,7 +111,8 @@ bool make_cache_map(CUtensorMap* map, const uint8_t* base, const CacheAttnArgs& 
     cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1, 1};
     cuuint32_t one[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -262,14 +263,19 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
     if (a.T > 0 && cache_attn_mma_supported(a)) {
         const CacheBox box = cache_attn_mma_box(a);
         CUtensorMap maps[2];
-        if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows) &&
-            make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows)) {
+        if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&
+            make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows, true)) {
             // requests of many rows first (none where no request may have so many)
             const bool many = static_cast<int64_t>(a.max_q) * a.G > kFewRows && cache_attn_tc_supported(a);
             if (many) {
                 st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
                 if (st != BPA_OK) return st;
-                st = cuda_status(launch_cache_attn_tc(a, a.status + 2, s), "cache attention launch");
+                const CacheBox plain = cache_attn_tc_box(a);
+                CUtensorMap raw[2];
+                if (!make_cache_map(&raw[0], a.kc, a, a.d, a.kcs, plain.cols_k, plain.rows, false) ||
+                    !make_cache_map(&raw[1], a.vc, a, a.dv, a.vcs, plain.cols_v, plain.rows, false))
+                    return fail(BPA_ERR_CUDA, "cache attention: no tensor map");
+                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, s), "cache attention launch");
                 if (st != BPA_OK) return st;
             }
             return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), many, s),

@@ -13,19 +13,23 @@
 // scale that the item meets; a page below 2^-100 of that one, or of zeros (scale 0), counts as 2^-100 of it.
 //
 // Bounded by the softmax's instructions and the exponentials beside the products (compute, not
-// bytes): per 128 x 128 scores of one row tile a thread owns a row and spends about three instructions
-// and one exponential a score.
-// Roles (512 threads; registers moved to the softmax by setmaxnreg):
-//   warps 0-3, 4-7   softmax of tile 0, 1; they also bring their rows of Q into shared memory
-//   warp 8           MMA issuer, TMEM owner
-//   warp 9           items, and for each key tile its pages' ids and scales (a ring of records)
-//   warps 12-15      K and V: global memory -> registers (one tile ahead) -> fp16 -> swizzled tiles
-// TMEM: S0 [0,128), S1 [128,256), O0 [256,256+DV), O1 [384,384+DV); W over the first half of S.
+// bytes): about three instructions and one exponential a score.  Two threads share a row (64 columns
+// each), so sixteen warps work on the softmax and cover each other's latencies.
+// Roles (768 threads; registers moved to the softmax by setmaxnreg):
+//   warps 0-7, 8-15  softmax of row tile 0, 1; of eight warps the second four take columns 64-127.  They
+//                    also bring their rows of Q into shared memory
+//   warp 16          MMA issuer, TMEM owner
+//   warp 17          items, a record of each key tile (page scales), and its codes by TMA (a ring of
+//                    two half tiles: K, V, K, ...)
+//   warps 20-23      codes -> fp16 -> swizzled K and V tiles
+// TMEM: S0 [0,128), S1 [128,256), O0 [256,256+DV), O1 [384,384+DV); W over the first half of each 64
+// columns of S.
 // Every wait is bounded; on a timeout the roles leave their loops and the CTA frees its TMEM.
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cache.h"
 #include "common.cuh"
@@ -33,15 +37,15 @@
 namespace bpa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int BN = 128;               // keys of a tile
 constexpr int kRows = 256;            // rows of an item
 constexpr int kMetas = 4;             // records of key tiles in flight
+constexpr int kMma = 16, kAux = 17, kConv = 20;   // first warps of the roles
 constexpr float kTau = 8.f, kOff = 7.f;
 constexpr float kFar = 100.f;         // log2 of the largest ratio of the v scales below the item's first
 
 struct TileMeta {
-    int64_t k[8], v[8];               // where each 16 keys begin in k_cache, v_cache (-1: no page)
     int key0, len, end, pad;
     float a[8], lv[8], e[8];          // k scale * softmax scale * log2(e); log2 v scale; 2^(lv0 - lv)
 };
@@ -56,11 +60,16 @@ struct Cfg {
     static constexpr int SUB = 128 * 128;                        // a slab of 64 fp16 columns x 128 rows
     static constexpr int Q_BYTES = D / 64 * SUB, K_BYTES = D / 64 * SUB, V_BYTES = DV / 64 * SUB;
     static constexpr int NS = 2;
-    static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NS * K_BYTES, OFF_META = OFF_V + NS * V_BYTES;
-    static constexpr int OFF_ITEM = OFF_META + kMetas * (int)sizeof(TileMeta), OFF_BAR = OFF_ITEM + 2 * (int)sizeof(Item);
+    static constexpr int RBK = D < 128 ? D : 128, RBV = DV;      // bytes of a row of codes
+    static constexpr int RAW = BN * (RBK > RBV ? RBK : RBV);     // half a tile of codes
+    static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NS * K_BYTES, OFF_RAW = OFF_V + NS * V_BYTES;
+    static constexpr int OFF_META = OFF_RAW + 2 * RAW, OFF_ITEM = OFF_META + kMetas * (int)sizeof(TileMeta);
+    static constexpr int OFF_PAIR = OFF_ITEM + 2 * (int)sizeof(Item);           // flags of the softmax warps
+    static constexpr int OFF_BAR = OFF_PAIR + 128;
     static constexpr int B_Q = 0, B_KF = 2, B_KE = B_KF + NS, B_VF = B_KE + NS, B_VE = B_VF + NS, B_S = B_VE + NS,
                          B_P = B_S + 2, B_O = B_P + 2, B_OE = B_O + 2, B_MF = B_OE + 2, B_ME = B_MF + kMetas,
-                         B_IF = B_ME + kMetas, B_IE = B_IF + 2, B_FIN = B_IE + 2, NBAR = B_FIN + 1;
+                         B_IF = B_ME + kMetas, B_IE = B_IF + 2, B_RF = B_IE + 2, B_RE = B_RF + 2, B_PAIR = B_RE + 2,
+                         B_FIN = B_PAIR + 8, NBAR = B_FIN + 1;
     static constexpr int SMEM = 1024 + OFF_BAR + 8 * NBAR + 16;
     static_assert(SMEM <= 232448, "shared memory");
     static constexpr uint32_t F16 = 1u << 4;                     // float32 sums, both operands fp16
@@ -89,55 +98,79 @@ BPA_DEV uint32_t cvt_hi(uint32_t four) {
     return h;
 }
 
-// One pass over the row's 128 scores: weights (fp16 pairs), the row's sum of W e, and the maxima of u
-// and x.  EDGE: keys outside [kmin, kmax] are masked.
+// This thread's 64 scores of its row (columns c0 ..).  Rolled loops over 32 columns: the roles' code
+// together has to stay in the instruction caches (unrolled, the warps spent two fifths of their time
+// waiting for instructions).  EDGE: keys outside [kmin, kmax] are masked.
+
+// The maxima of u and x.
 template <bool EDGE>
-BPA_DEV void pass(uint32_t tS, const TileMeta* mt, float f_row, float mref, int k0, int kmin, int kmax, uint32_t (&pk)[64],
-                  float& sum, float& umax, float& xmax) {
-    sum = 0.f;
+BPA_DEV void maxima(uint32_t tS, const TileMeta* mt, int c0, float f_row, int k0, int kmin, int kmax, float& umax, float& xmax) {
     umax = xmax = -INFINITY;
-#pragma unroll
-    for (int cc = 0; cc < 4; ++cc) {
+#pragma unroll 1
+    for (int c = c0; c < c0 + 64; c += 32) {
         uint32_t s[32];
-        tmem_ld32(tS + cc * 32, s);
+        tmem_ld32(tS + c, s);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int ch = 2 * cc + h;
-            const float a = f_row * mt->a[ch], lv = mt->lv[ch], b = lv - mref;
-            const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
-            uint64_t r2 = 0;
+            const float a = f_row * mt->a[c / 16 + h];
             float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s0 = __uint_as_float(s[16 * h + 2 * i]), s1 = __uint_as_float(s[16 * h + 2 * i + 1]);
-                float y0, y1;
+            for (int i = 0; i < 16; i += 2) {
+                float s0 = __uint_as_float(s[16 * h + i]), s1 = __uint_as_float(s[16 * h + i + 1]);
                 if (EDGE) {
-                    const int k = k0 + 16 * ch + 2 * i;
-                    y0 = k < kmin || k > kmax ? -INFINITY : s0 * a;
-                    y1 = k + 1 < kmin || k + 1 > kmax ? -INFINITY : s1 * a;
-                    mx = fmax3(mx, y0, y1);
-                    y0 += b;
-                    y1 += b;
-                } else {
-                    mx = fmax3(mx, s0, s1);
-                    f2_unpack(ffma2(f2_pack(s0, s1), a2, b2), y0, y1);
+                    const int k = k0 + c + 16 * h + i;
+                    s0 = k < kmin || k > kmax ? -INFINITY : s0 * a;
+                    s1 = k + 1 < kmin || k + 1 > kmax ? -INFINITY : s1 * a;
                 }
-                const float w0 = ex2(y0), w1 = ex2(y1);
-                r2 = fadd2(r2, f2_pack(w0, w1));
-                pk[8 * ch + i] = h2(w0, w1);
+                mx = fmax3(mx, s0, s1);
             }
             const float x = EDGE ? mx : mx * a;                   // a >= 0
-            umax = fmaxf(umax, x + lv);
+            umax = fmaxf(umax, x + mt->lv[c / 16 + h]);
             xmax = fmaxf(xmax, x);
-            float p, q;
-            f2_unpack(r2, p, q);
-            sum = fmaf(p + q, mt->e[ch], sum);
         }
     }
 }
 
+// The weights as fp16 pairs over the scores (columns c0 .. c0 + 31); returns their sum of W e.
+template <bool EDGE>
+BPA_DEV float weights(uint32_t tS, const TileMeta* mt, int c0, float f_row, float mref, int k0, int kmin, int kmax) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int cc = 0; cc < 2; ++cc) {
+        const int c = c0 + 32 * cc;
+        uint32_t s[32], pk[16];
+        tmem_ld32(tS + c, s);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float a = f_row * mt->a[c / 16 + h], b = mt->lv[c / 16 + h] - mref;
+            const uint64_t a2 = f2_pack(a, a), b2 = f2_pack(b, b);
+            uint64_t r2 = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float y0, y1;
+                f2_unpack(ffma2(f2_pack(__uint_as_float(s[16 * h + 2 * i]), __uint_as_float(s[16 * h + 2 * i + 1])), a2, b2), y0, y1);
+                if (EDGE) {
+                    const int k = k0 + c + 16 * h + 2 * i;
+                    y0 = k < kmin || k > kmax ? -INFINITY : y0;
+                    y1 = k + 1 < kmin || k + 1 > kmax ? -INFINITY : y1;
+                }
+                const float w0 = ex2(y0), w1 = ex2(y1);
+                r2 = fadd2(r2, f2_pack(w0, w1));
+                pk[8 * h + i] = h2(w0, w1);
+            }
+            float p, q;
+            f2_unpack(r2, p, q);
+            sum = fmaf(p + q, mt->e[c / 16 + h], sum);
+        }
+        tmem_st16_nowait(tS + c0 + 16 * cc, pk);
+    }
+    tmem_st_wait();
+    return sum;
+}
+
 template <int D, int DV>
-__global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnArgs a, uint32_t* counter, int vec_q, int vec_o) {
+__global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_constant__ CUtensorMap tmK,
+    const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a, uint32_t* counter, int vec_q, int vec_o) {
     using C = Cfg<D, DV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -151,13 +184,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(BAR(C::B_Q + i), 128);
+            mbar_init(BAR(C::B_Q + i), 256);
             mbar_init(BAR(C::B_S + i), 1);
-            mbar_init(BAR(C::B_P + i), 128);
+            mbar_init(BAR(C::B_P + i), 256);
             mbar_init(BAR(C::B_O + i), 1);
-            mbar_init(BAR(C::B_OE + i), 128);
+            mbar_init(BAR(C::B_OE + i), 256);
+            mbar_init(BAR(C::B_RF + i), 1);
+            mbar_init(BAR(C::B_RE + i), 4);
             mbar_init(BAR(C::B_IF + i), 1);
-            mbar_init(BAR(C::B_IE + i), 9);        // MMA warp, eight softmax warps
+            mbar_init(BAR(C::B_IE + i), 17);       // MMA warp, sixteen softmax warps
         }
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(BAR(C::B_KF + i), 4);
@@ -167,13 +202,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
         }
         for (int i = 0; i < kMetas; ++i) {
             mbar_init(BAR(C::B_MF + i), 1);
-            mbar_init(BAR(C::B_ME + i), 12);       // four converting and eight softmax warps
+            mbar_init(BAR(C::B_ME + i), 20);       // four converting and sixteen softmax warps
         }
+        for (int i = 0; i < 8; ++i) mbar_init(BAR(C::B_PAIR + i), 2);
         mbar_init(BAR(C::B_FIN), 1);
         *abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == kMma) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -185,70 +221,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
         return __all_sync(0xffffffffu, mbar_wait(BAR(b), parity & 1, abort, a.status, where)) != 0;
     };
 
-    if (warp >= 12) {
-        // ------------------------------------------------------------ K, V: codes -> fp16 tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        const int wq = warp - 12, c = lane & 7, r4 = lane >> 3;        // 16-byte piece of a row; row of four
-        uint4 kr[8], vr[8];
-        // this thread's pieces of a tile: rows 32 wq + 4 i + r4, so two stretches of 16 keys
-        auto load = [&](const TileMeta* mt, const int64_t* starts, const uint8_t* base, int64_t step, int ch, uint4 (&x)[8]) {
-            const int left = mt->len - mt->key0 - 32 * wq - r4;        // rows of this thread that are keys: 4 i < left
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = starts[2 * wq + h];
-                const uint8_t* p = base + at + r4 * step + 16 * c;
-                const bool some = at >= 0 && 16 * c < ch;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[4 * h + i] = make_uint4(0, 0, 0, 0);
-                    if (some && 16 * h + 4 * i < left) x[4 * h + i] = *reinterpret_cast<const uint4*>(p + 4 * i * step);
-                }
-            }
-        };
-        auto store = [&](uint8_t* tile, int width, const uint4 (&x)[8]) {
-            if (16 * c >= width) return;
+    if (warp >= kConv) {
+        // ------------------------------------------------------------ codes -> fp16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const int wq = warp - kConv;
+        // half a tile from the ring to a K or V tile: rows of RB bytes, 16 bytes of a row at a time
+        auto convert = [&](const uint8_t* raw, auto rb, uint8_t* tile, int left) {
+            constexpr int RB = decltype(rb)::value, PER = RB / 16, ROWS = 32 / PER;   // lanes of a row, rows of a warp's read
+            const int c = lane % PER, r = lane / PER, flip = c >> 2;                  // flip: the halves of a row on other banks
             uint8_t* slab = tile + (c >> 2) * C::SUB;
-            const int flip = c >> 2;                                   // the halves of a row on other banks
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 32 * wq + 4 * i + r4;
-                const uint4 lo = make_uint4(cvt_lo(x[i].x), cvt_hi(x[i].x), cvt_lo(x[i].y), cvt_hi(x[i].y));
-                const uint4 hi = make_uint4(cvt_lo(x[i].z), cvt_hi(x[i].z), cvt_lo(x[i].w), cvt_hi(x[i].w));
+#pragma unroll 2
+            for (int i = 0; i < 32 / ROWS; ++i) {
+                const int row = 32 * wq + ROWS * i + r;
+                uint4 x = *reinterpret_cast<const uint4*>(raw + row * RB + 16 * c);
+                if (row >= left) x = make_uint4(0, 0, 0, 0);       // slots past the last token may hold anything
+                const uint4 lo = make_uint4(cvt_lo(x.x), cvt_hi(x.x), cvt_lo(x.y), cvt_hi(x.y));
+                const uint4 hi = make_uint4(cvt_lo(x.z), cvt_hi(x.z), cvt_lo(x.w), cvt_hi(x.w));
                 *reinterpret_cast<uint4*>(slab + sw128_offset(row, (c & 3) * 2 + flip)) = flip ? hi : lo;
                 *reinterpret_cast<uint4*>(slab + sw128_offset(row, (c & 3) * 2 + 1 - flip)) = flip ? lo : hi;
             }
+            fence_proxy_async_smem();
+            __syncwarp();
         };
-        int t = 0;
-        bool ok = wait(C::B_MF, 0, 0xE0);
-        bool more = ok && !metas[0].end;
-        if (more) {
-            load(&metas[0], metas[0].k, a.kc, a.kcs[2], a.d, kr);
-            load(&metas[0], metas[0].v, a.vc, a.vcs[2], a.dv, vr);
-        }
-        for (; ok && more; ++t) {
-            const int st = t % C::NS, use = t / C::NS;
-            const int next = (t + 1) % kMetas;
-            if (use > 0 && !(ok = wait(C::B_KE + st, use - 1, 0xE1))) break;
-            store(smem + C::OFF_K + st * C::K_BYTES, D, kr);
-            fence_proxy_async_smem();
+        for (int t = 0;; ++t) {
+            const int st = t % C::NS, use = t / C::NS, sl = t % kMetas;
+            if (!wait(C::B_MF + sl, t / kMetas, 0xE0) || metas[sl].end) break;
+            const int left = metas[sl].len - metas[sl].key0;
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(C::B_KF + st));
-            if (!(ok = wait(C::B_MF + next, (t + 1) / kMetas, 0xE2))) break;
-            more = !metas[next].end;
-            if (more) load(&metas[next], metas[next].k, a.kc, a.kcs[2], a.d, kr);
-            if (use > 0 && !(ok = wait(C::B_VE + st, use - 1, 0xE3))) break;
-            store(smem + C::OFF_V + st * C::V_BYTES, DV, vr);
-            fence_proxy_async_smem();
-            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
+            if (!wait(C::B_RF, t, 0xE1) || (use > 0 && !wait(C::B_KE + st, use - 1, 0xE2))) break;
+            convert(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
+            if (lane == 0) {
+                mbar_arrive(BAR(C::B_KF + st));
+                mbar_arrive(BAR(C::B_RE));
+            }
+            if (!wait(C::B_RF + 1, t, 0xE3) || (use > 0 && !wait(C::B_VE + st, use - 1, 0xE4))) break;
+            convert(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
             if (lane == 0) {
                 mbar_arrive(BAR(C::B_VF + st));
-                mbar_arrive(BAR(C::B_ME + t % kMetas));                // its codes have been loaded
+                mbar_arrive(BAR(C::B_RE + 1));
             }
-            if (more) load(&metas[next], metas[next].v, a.vc, a.vcs[2], a.dv, vr);
         }
-    } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == 9) {
+    } else if (warp >= kMma) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kAux) {
             // -------------------------------------------------------- items and their key tiles' records
             int t = 0;                 // records written
             auto publish_end = [&]() {
@@ -339,10 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                     if (t >= kMetas && !(ok = wait(C::B_ME + sl, t / kMetas - 1, 0xE6))) break;
                     TileMeta* m = metas + sl;
                     if (lane < 8) {
-                        const int tok = ((first + j) * BN + 16 * lane) % a.P;
                         const float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : lv0 - kFar;
-                        m->k[lane] = id < 0 ? -1 : id * a.kcs[0] + hk * a.kcs[1] + tok * a.kcs[2];
-                        m->v[lane] = id < 0 ? -1 : id * a.vcs[0] + hk * a.vcs[1] + tok * a.vcs[2];
                         m->a[lane] = ks * a.scale * kLog2e;
                         m->lv[lane] = lv;
                         m->e[lane] = ex2(lv0 - lv);
@@ -354,6 +367,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_MF + sl));
+                    // the tile's codes: K, then V, 16 keys a copy
+                    const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                    const int tok = ((first + j) * BN + 16 * lane) % a.P;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int rb = kv ? C::RBV : C::RBK;
+                        if (t > 0 && !(ok = wait(C::B_RE + kv, t - 1, 0xEF))) break;
+                        if (lane == 0) mbar_expect_tx(BAR(C::B_RF + kv), n * 16 * rb);
+                        __syncwarp();
+                        if (id >= 0)
+                            tma_load_4d(sb + C::OFF_RAW + kv * C::RAW + 16 * lane * rb, kv ? &tmV : &tmK, BAR(C::B_RF + kv), 0, tok, hk, id);
+                    }
+                    if (!ok) break;
                     id = id1;
                     ks = ks1;
                     vs = vs1;
@@ -361,8 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 }
                 if (!ok) break;
             }
+            if (t > 0 && *abort) {     // after a timeout: the copies in flight end before the CTA does
+                int never = 0;
+                for (int kv = 0; kv < 2; ++kv)
+                    for (int p = t - 1; p <= t; ++p) mbar_wait(BAR(C::B_RF + kv), p & 1, &never, a.status, 0xEF);
+            }
             publish_end();
-        } else if (warp == 8) {
+        } else if (warp == kMma) {
             // -------------------------------------------------------- MMA issuer
             int t = 0, np[2] = {0, 0}, seen[2] = {0, 0};   // key tiles; W tiles used, items with work, per row tile
             bool ok = true;
@@ -377,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 auto issue_s = [&](int i, int pos) {
                     const uint64_t qd = sdesc_sw128(sb + i * C::Q_BYTES, 16, 1024);
                     const uint64_t kd = sdesc_sw128(sb + C::OFF_K + pos % C::NS * C::K_BYTES, 16, 1024);
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::SUB + (kk & 3) * 32;
                         tc_mma_ss_w(tmem + i * BN, sdesc_advance(qd, off), sdesc_advance(kd, off), C::IDESC_S, kk > 0);
@@ -386,9 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 };
                 auto issue_pv = [&](int i, int pos, bool first) {
                     const uint64_t vd = sdesc_sw128(sb + C::OFF_V + pos % C::NS * C::V_BYTES, C::SUB, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        tc_mma_ts_w(tmem + 256 + i * 128, tmem + i * BN + kk * 8, sdesc_advance(vd, kk * 2048), C::IDESC_PV,
+#pragma unroll 2
+                    for (int kk = 0; kk < BN / 16; ++kk)       // the weights of 64 keys lie over the first half of their scores
+                        tc_mma_ts_w(tmem + 256 + i * 128, tmem + i * BN + kk * 8 + (kk >> 2) * 32, sdesc_advance(vd, kk * 2048), C::IDESC_PV,
                                     (!first || kk > 0) ? 1u : 0u);
                 };
                 for (int i = 0; ok && i < two; ++i) ok = wait(C::B_Q + i, seen[i], 0xE8);
@@ -426,11 +457,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
             mbar_wait(BAR(C::B_FIN), 0, &never, a.status, 0xEE);
         }
     } else {
-        // ------------------------------------------------------------ softmax: thread t owns row t of its tile
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        const int qt = warp >> 2, row = threadIdx.x & 127;
+        // ------------------------------------------------------------ softmax: two threads own a row, 64 columns each
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+        const int qt = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane, c0 = 64 * half;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + qt * BN + lanes, tO = tmem + 256 + qt * 128 + lanes;
+        // the two warps of 32 rows meet at a barrier of their own and tell each other whether a row moves its M
+        const int pair = qt * 4 + (warp & 3);
+        volatile int* flags = reinterpret_cast<volatile int*>(smem + C::OFF_PAIR) + 4 * pair;
+        int meets = 0;
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_PAIR + pair));
+            return wait(C::B_PAIR + pair, meets++, 0xF4);
+        };
         int t = 0, cs = 0, seen = 0;   // key tiles, S tiles and items with work of this row tile
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -442,22 +482,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
             const int rows = it.n * a.G, ri = it.i0 + qt * 128 + row;
             const bool there = ri < rows, busy = it.i0 + qt * 128 < rows;     // busy: the tile has rows
             const int tok = there ? ri / a.G : 0, head = it.hk * a.G + (there ? ri - tok * a.G : 0);
-            const Req rq = {it.row0, it.n, it.len, false};
             int kmin = 0, kmax = INT_MAX;      // a row that is not there masks nothing (q = 0)
-            if (there) row_keys(a, rq, tok, kmin, kmax);
+            if (there) row_keys(a, Req{it.row0, it.n, it.len, false}, tok, kmin, kmax);
             float f_row = 1.f;
             if (busy && it.tiles) {
-                // ---- the row of q as fp16, its largest value scaled into [2^7, 2^8)
+                // ---- the row of q as fp16, its largest value scaled into [2^7, 2^8): all of it for the
+                // largest, this thread's half to store
                 const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(it.row0 + tok) * a.qs[0] +
                                          static_cast<int64_t>(head) * a.qs[1];
-                uint4 x[D / 8];
-                uint32_t top = 0;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    x[c] = make_uint4(0, 0, 0, 0);
+                auto piece = [&](int c) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
                     if (there && 8 * c < a.d) {
                         if (vec_q) {
-                            x[c] = *reinterpret_cast<const uint4*>(q + 8 * c);
+                            x = *reinterpret_cast<const uint4*>(q + 8 * c);
                         } else {
                             uint32_t w[4];
 #pragma unroll
@@ -465,21 +502,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                                 const unsigned short* p = reinterpret_cast<const unsigned short*>(q + 8 * c + 2 * e);
                                 w[e] = p[0] | static_cast<uint32_t>(p[1]) << 16;
                             }
-                            x[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                            x = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
-                    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                    return x;
+                };
+                uint32_t top = 0;
+                auto largest = [&](const uint4& x) {
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
-                }
+                };
+                uint4 x[D / 16];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) x[c] = piece(half * (D / 16) + c);
+#pragma unroll 4
+                for (int c = 0; c < D / 16; ++c) largest(piece((1 - half) * (D / 16) + c));
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) largest(x[c]);
                 int ex = top && top < 0x7f800000u ? static_cast<int>(top >> 23) - 127 - 7 : 0;
                 ex = min(max(ex, -126), 126);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
                 f_row = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
                 uint8_t* tile = smem + qt * C::Q_BYTES;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                for (int i = 0; i < D / 16; ++i) {
+                    const int c = half * (D / 16) + i;
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                     uint32_t y[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -489,48 +538,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 fence_proxy_async_smem();
                 mbar_arrive(BAR(C::B_Q + qt));
             }
-            float M = -INFINITY, xm = -INFINITY, L = 0.f;
+            float M = -INFINITY, xm = -INFINITY, L = 0.f;      // M of the row; x and L of this thread's columns
             for (int j = 0; j < it.tiles; ++j, ++t) {
                 const int sl = t % kMetas, k0 = (it.first + j) * BN;
+                if (!(ok = wait(C::B_MF + sl, t / kMetas, 0xF1))) break;
                 if (!busy) {                   // no rows: only the record's turn
-                    if (!(ok = wait(C::B_MF + sl, t / kMetas, 0xF1))) break;
                     if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
                     continue;
                 }
-                if (!(ok = wait(C::B_MF + sl, t / kMetas, 0xF1) && wait(C::B_S + qt, cs, 0xF2))) break;
+                if (!(ok = wait(C::B_S + qt, cs, 0xF2))) break;
                 ++cs;
                 tc_fence_after();
                 const TileMeta* mt = metas + sl;
                 const bool edge = __any_sync(0xffffffffu, k0 < kmin || k0 + BN - 1 > kmax);
-                uint32_t pk[64];
-                float sum, um, x;
-                // a second round where a row of the warp moves its M (always for the first tile)
-#pragma unroll 1
-                for (;;) {
-                    const float mref = M == -INFINITY ? 0.f : M - kOff;
-                    if (edge) pass<true>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, um, x);
-                    else pass<false>(tS, mt, f_row, mref, k0, kmin, kmax, pk, sum, um, x);
-                    if (!__any_sync(0xffffffffu, um > M + kTau)) break;
+                float um, x;
+                if (edge) maxima<true>(tS, mt, c0, f_row, k0, kmin, kmax, um, x);
+                else maxima<false>(tS, mt, c0, f_row, k0, kmin, kmax, um, x);
+                xm = fmaxf(xm, x);
+                bool move = j == 0;
+                if (!move) {                   // does a row of the two warps move its M?
+                    volatile int* f = flags + 2 * (t & 1);
+                    const int mine = __any_sync(0xffffffffu, um > M + kTau);
+                    if (lane == 0) f[half] = mine;
+                    if (!(ok = meet())) break;
+                    move = f[0] | f[1];
+                }
+                if (move) {                    // both threads of a row take the maximum of u over all of its columns
+                    float u2, x2;
+                    if (edge) maxima<true>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, u2, x2);
+                    else maxima<false>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, u2, x2);
+                    um = fmaxf(um, u2);
                     float fac = 1.f;
                     if (um > M + kTau) {
                         fac = M == -INFINITY ? 0.f : ex2(M - um);
                         M = um;
                         L *= fac;
                     }
-                    if (j == 0) continue;
-                    // S(j) is complete, so every earlier W V has been added to O
+                    if (j > 0) {               // S(j) is complete, so every earlier W V has been added to O
 #pragma unroll 1
-                    for (int cc = 0; cc < DV / 32; ++cc) {
-                        uint32_t r[32];
-                        tmem_ld32(tO + cc * 32, r);
+                        for (int cc = half * (DV / 64); cc < (half + 1) * (DV / 64); ++cc) {
+                            uint32_t r[32];
+                            tmem_ld32(tO + cc * 32, r);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fac);
-                        tmem_st32(tO + cc * 32, r);
+                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fac);
+                            tmem_st32(tO + cc * 32, r);
+                        }
                     }
+                    if (!(ok = meet())) break; // the other thread has read this one's scores
                 }
-                L += sum;
-                xm = fmaxf(xm, x);
-                tmem_st64(tS, pk);
+                const float mref = M == -INFINITY ? 0.f : M - kOff;
+                L += edge ? weights<true>(tS, mt, c0, f_row, mref, k0, kmin, kmax) : weights<false>(tS, mt, c0, f_row, mref, k0, kmin, kmax);
                 tc_fence_before();
                 mbar_arrive(BAR(C::B_P + qt));
                 __syncwarp();
@@ -542,25 +599,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
                 if (!(ok = wait(C::B_O + qt, seen, 0xF3))) break;
                 tc_fence_after();
                 ++seen;
+                // the other half of the row, by way of the tile of Q, which every product has read
+                float2* rows2 = reinterpret_cast<float2*>(smem + qt * C::Q_BYTES);
+                rows2[128 * half + row] = make_float2(L, xm);
+                if (!(ok = meet())) break;
+                const float2 other = rows2[128 * (1 - half) + row];
+                // the same sum on both threads
+                L = L + other.x;
+                xm = fmaxf(xm, other.y);
+                if (!(ok = meet())) break;
             }
             // ---- epilogue: o = O 2^lv0 / L; l relative to the row's maximum of x
-            float l = M == -INFINITY ? (L != L ? L : 0.f) : L * ex2(M - kOff - it.lv0 - xm), mm = xm, share = 1.f;
+            float l = M == -INFINITY ? (L != L ? L : 0.f) : L * ex2(M - kOff - it.lv0 - xm), mm = xm, part = 1.f;
             if (a.sink) {
                 const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(xm, sk);
                 const float old = l;
                 l = (xm == -INFINITY ? l : l * ex2(xm - nm)) + ex2(sk - nm);
-                share = xm == -INFINITY || old == 0.f ? (old != old ? old : 0.f) : old * ex2(xm - nm) / l;   // what the keys have of the row
+                part = xm == -INFINITY || old == 0.f ? (old != old ? old : 0.f) : old * ex2(xm - nm) / l;   // what the keys have of the row
                 mm = nm;
             }
-            const float inv = (L == 0.f || M == -INFINITY ? (L != L ? L : 0.f) : ex2(it.lv0) / L) * share;
+            const float inv = (L == 0.f || M == -INFINITY ? (L != L ? L : 0.f) : ex2(it.lv0) / L) * part;
             const int64_t out_row = it.row0 + tok;
-            if (there && a.m) {
+            if (there && a.m && half == 0) {
                 a.m[static_cast<int64_t>(head) * a.T + out_row] = mm == -INFINITY ? mm : mm * kLn2;
                 a.l[static_cast<int64_t>(head) * a.T + out_row] = l;
             }
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + out_row * a.os[0] + static_cast<int64_t>(head) * a.os[1];
 #pragma unroll 1
-            for (int cc = 0; cc < DV / 32; ++cc) {
+            for (int cc = half * (DV / 64); cc < (half + 1) * (DV / 64); ++cc) {
                 uint32_t r[32];
                 if (it.tiles) {
                     tmem_ld32(tO + cc * 32, r);
@@ -595,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kMma) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -603,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const CacheAttnAr
 }
 
 template <int D, int DV>
-cudaError_t launch(const CacheAttnArgs& a, uint32_t* counter, cudaStream_t s) {
+cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, cudaStream_t s) {
     using C = Cfg<D, DV>;
     static std::atomic<int> sms[64];
     int dev = 0;
@@ -620,22 +686,23 @@ cudaError_t launch(const CacheAttnArgs& a, uint32_t* counter, cudaStream_t s) {
     const bool vec_o = (reinterpret_cast<uintptr_t>(a.o) & 15) == 0 && a.os[0] % 8 == 0 && a.os[1] % 8 == 0;
     // at most the packed rows' groups and a ragged one per request
     const int64_t most = (static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
-    k_cache_attn_tc<D, DV><<<static_cast<unsigned>(std::min<int64_t>(n, most)), kThreads, C::SMEM, s>>>(a, counter, vec_q, vec_o);
+    k_cache_attn_tc<D, DV><<<static_cast<unsigned>(std::min<int64_t>(n, most)), kThreads, C::SMEM, s>>>(maps[0], maps[1], a, counter,
+                                                                                                       vec_q, vec_o);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 bool cache_attn_tc_supported(const CacheAttnArgs& a) {
-    if (a.dtype != BPA_BF16 || a.d % 16 || a.dv % 16 || a.d > 128 || a.dv > 128 || (a.d <= 64 && a.dv > 64) || a.P % 16) return false;
-    uintptr_t all = reinterpret_cast<uintptr_t>(a.kc) | reinterpret_cast<uintptr_t>(a.vc);
-    for (int i = 0; i < 3; ++i) all |= static_cast<uintptr_t>(a.kcs[i]) | static_cast<uintptr_t>(a.vcs[i]);
-    return all % 16 == 0;
+    return a.dtype == BPA_BF16 && a.d % 16 == 0 && a.dv % 16 == 0 && a.d <= 128 && a.dv <= 128 && (a.d > 64 || a.dv <= 64) &&
+           a.P % 16 == 0;
 }
 
-cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, uint32_t* counter, cudaStream_t s) {
-    if (a.d <= 64) return launch<64, 64>(a, counter, s);
-    return a.dv <= 64 ? launch<128, 64>(a, counter, s) : launch<128, 128>(a, counter, s);
+CacheBox cache_attn_tc_box(const CacheAttnArgs& a) { return {a.d <= 64 ? 64 : 128, a.dv <= 64 ? 64 : 128, 16}; }
+
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, cudaStream_t s) {
+    if (a.d <= 64) return launch<64, 64>(a, maps, counter, s);
+    return a.dv <= 64 ? launch<128, 64>(a, maps, counter, s) : launch<128, 128>(a, maps, counter, s);
 }
 
 }  // namespace bpa
