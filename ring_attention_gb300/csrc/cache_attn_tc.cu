@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 auto issue_s = [&](int i, int pos) {
                     const uint64_t qd = sdesc_sw128(sb + i * C::Q_BYTES, 16, 1024);
                     const uint64_t kd = sdesc_sw128(sb + C::OFF_K + pos % C::NS * C::K_BYTES, 16, 1024);
-#pragma unroll 2
+#pragma unroll 4
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::SUB + (kk & 3) * 32;
                         tc_mma_ss_w(tmem + i * BN, sdesc_advance(qd, off), sdesc_advance(kd, off), C::IDESC_S, kk > 0);
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 };
                 auto issue_pv = [&](int i, int pos, bool first) {
                     const uint64_t vd = sdesc_sw128(sb + C::OFF_V + pos % C::NS * C::V_BYTES, C::SUB, 1024);
-#pragma unroll 2
+#pragma unroll 4
                     for (int kk = 0; kk < BN / 16; ++kk)       // the weights of 64 keys lie over the first half of their scores
                         tc_mma_ts_w(tmem + 256 + i * 128, tmem + i * BN + kk * 8 + (kk >> 2) * 32, sdesc_advance(vd, kk * 2048), C::IDESC_PV,
                                     (!first || kk > 0) ? 1u : 0u);
