@@ -348,41 +348,46 @@ _CACHE_PACK = struct.Struct("@I7iPP6qPP").pack
 _BATCH_PACK = struct.Struct("@I5iP4qPPPf3iP").pack
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _CODES = {torch.bfloat16: BPA_BF16, torch.float32: BPA_FP32}
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+_empty, _current_device = torch.empty, torch.cuda.current_device
 
 
-def _i32_buffer(t, name, shape, device=None):
-    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+def _i32_buffer(t, name, shape, dev):
+    """The address of a contiguous int32 tensor of this shape on device number dev (-1: the CPU)."""
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor, got {t.dtype} {list(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors, got {t.device}")
     return t.data_ptr()
 
 
-def _enter(device, stream):
-    """(guard, stream pointer, other): the device to leave again (None: it is current), the stream of
-    the call (``stream``, or torch's current one) and, where that is not torch's current one, itself."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+def _enter(dev, stream):
+    """(guard, stream pointer, other) for device number dev: the device to leave again (None: it is
+    current), the stream of the call (``stream``, or torch's current one) and, where that is not
+    torch's current one, itself."""
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
     guard = None
-    if device.index != torch.cuda.current_device():
-        guard = torch.cuda.device(device)
+    if dev != _current_device():
+        guard = torch.cuda.device(dev)
         guard.__enter__()
-    here = torch._C._cuda_getCurrentRawStream(device.index)
+    here = torch._C._cuda_getCurrentRawStream(dev)
     if stream is None:
         return guard, here, None
     return guard, stream.cuda_stream, stream if stream.cuda_stream != here else None
 
 
-def _empty(shape, dtype, device, other):
-    """A buffer that the call makes for itself, marked for the stream it is used on."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+def _leave(guard, other, made):
+    """Undoes _enter; what the call made for itself on another stream than torch's is marked for it."""
+    if guard is not None:
+        guard.__exit__(None, None, None)
     if other is not None:
-        t.record_stream(other)
-    return t
+        for t in made:
+            t.record_stream(other)
 
 
 def _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype):
-    """(packed bpa_cache_desc, pages, Hkv, page_size, d, dv) of the cache's tensors."""
+    """(packed bpa_cache_desc, Hkv, d, dv, device number) of the cache's tensors."""
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"tensors must be bfloat16 or float32, got {dtype}")
@@ -392,19 +397,17 @@ def _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype):
             raise ValueError(f"{name} must be a 4-D [pages, Hkv, page_size, channels] tensor of uint8 or "
                              "float8_e4m3fn with contiguous channels")
     pages, Hkv, P, d = ks
-    if vs[:3] != ks[:3]:
+    pages_v, Hkv_v, P_v, dv = vs
+    if pages_v != pages or Hkv_v != Hkv or P_v != P:
         raise ValueError("k_cache and v_cache must share pages, heads and page size")
-    dev = k_cache.device
+    dev, per_page = k_cache.get_device(), (pages, Hkv)
     for name, c in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if c.dtype is not torch.float32 or c.shape != ks[:2] or not c.is_contiguous():
+        if c.dtype is not _F32 or c.shape != per_page or not c.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 [{pages}, {Hkv}] tensor")
-        if c.device != dev:
-            raise ValueError("the cache's tensors must be on one device")
-    if v_cache.device != dev:
+    if v_cache.get_device() != dev or k_scale.get_device() != dev or v_scale.get_device() != dev:
         raise ValueError("the cache's tensors must be on one device")
-    dv = vs[3]
     return _CACHE_PACK(_CACHE_SIZE, code, Hkv, d, dv, P, pages, 0, k_cache.data_ptr(), v_cache.data_ptr(), kst[0],
-                       kst[1], kst[2], vst[0], vst[1], vst[2], k_scale.data_ptr(), v_scale.data_ptr()), pages, Hkv, P, d, dv
+                       kst[1], kst[2], vst[0], vst[1], vst[2], k_scale.data_ptr(), v_scale.data_ptr()), Hkv, d, dv, dev
 
 
 def make_cache_desc(k_cache, v_cache, k_scale, v_scale, dtype) -> bpa_cache_desc:
@@ -415,9 +418,9 @@ def make_cache_desc(k_cache, v_cache, k_scale, v_scale, dtype) -> bpa_cache_desc
     return bpa_cache_desc.from_buffer_copy(_pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)[0])
 
 
-def _rows_strides(t, name, shape, dtype, device):
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on {device}, got {t.dtype} "
+def _rows_strides(t, name, shape, dtype, dev):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on the device of the cache, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
     st = t.stride()
     if st[2] != 1 and shape[2] != 1:
@@ -434,31 +437,34 @@ def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, pa
     all int32.  ctx_lens_out=ctx_lens and free_count_out=free_count update in place."""
     if ctx_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("ctx_lens must be [R], page_table [R, max_pages], free_pages [num_pages]")
-    dev, R, T = ctx_lens.device, ctx_lens.shape[0], int(T)
-    if page_table.shape[0] != R:
-        raise ValueError(f"page_table has {page_table.shape[0]} rows for {R} requests")
-    max_pages, num_pages = page_table.shape[1], free_pages.shape[0]
-    ins = [_i32_buffer(t, name, shape, dev) for t, name, shape in (
-        (ctx_lens, "ctx_lens", (R,)), (new_lens, "new_lens", (R,)), (free_pages, "free_pages", (num_pages,)),
-        (free_count, "free_count", (1,)), (page_table, "page_table", (R, max_pages)))]
-    given = ((kv_lens, "kv_lens", (R,)), (cu_q, "cu_q", (R + 1,)), (slot_map, "slot_map", (T,)),
-             (positions, "positions", (T,)), (ctx_lens_out, "ctx_lens_out", (R,)),
-             (free_count_out, "free_count_out", (1,)))
-    for t, name, shape in given:
+    dev, R, T = ctx_lens.get_device(), ctx_lens.shape[0], int(T)
+    rows, max_pages = page_table.shape
+    if rows != R:
+        raise ValueError(f"page_table has {rows} rows for {R} requests")
+    num_pages, each, one = free_pages.shape[0], (R,), (1,)
+    ins = (_i32_buffer(ctx_lens, "ctx_lens", each, dev), _i32_buffer(new_lens, "new_lens", each, dev),
+           _i32_buffer(free_pages, "free_pages", (num_pages,), dev), _i32_buffer(free_count, "free_count", one, dev),
+           _i32_buffer(page_table, "page_table", (R, max_pages), dev))
+    outs = [kv_lens, cu_q, slot_map, positions, ctx_lens_out, free_count_out]
+    shapes = (each, (R + 1,), (T,), (T,), each, one)
+    for t, name, shape in zip(outs, ("kv_lens", "cu_q", "slot_map", "positions", "ctx_lens_out", "free_count_out"), shapes):
         if t is not None:
             _i32_buffer(t, name, shape, dev)
     guard, ptr, other = _enter(dev, stream)
+    made = []
     try:
-        # the buffers made here are parts of one (the status word first, on 256 bytes)
-        sizes = [0 if t is not None else shape[0] for t, _, shape in given]
-        made = _empty(sum(sizes) + 64, torch.int32, dev, other).split([64] + sizes)
-        outs = [new if t is None else t for (t, _, _), new in zip(given, made[1:])]
-        ws = made[0] if workspace_buf is None else workspace_buf
+        where = ctx_lens.device
+        for i in range(6):
+            if outs[i] is None:
+                outs[i] = _empty(shapes[i], dtype=_I32, device=where)
+                made.append(outs[i])
+        if workspace_buf is None:
+            workspace_buf = _empty(256, dtype=_U8, device=where)
+            made.append(workspace_buf)
         st = lib().bpa_cache_plan(R, T, int(page_size), num_pages, max_pages, *ins, *[t.data_ptr() for t in outs],
-                                  ws.data_ptr(), ws.numel() * ws.element_size(), ptr)
+                                  workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
-        if guard is not None:
-            guard.__exit__(None, None, None)
+        _leave(guard, other, made)
     if st:
         _raise_if(st, "bpa_cache_plan")
     return tuple(outs)
@@ -468,86 +474,94 @@ def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_
                      stream=None):
     """Write rows k [T, Hkv, d], v [T, Hkv, dv] into the cache's slots slot_map [T] (-1: skipped),
     updating k_cache, v_cache, k_scale, v_scale in place."""
-    cache, _, Hkv, _, d, dv = _pack_cache(k_cache, v_cache, k_scale, v_scale, k.dtype)
-    dev, T = k_cache.device, k.shape[0]
-    ks = _rows_strides(k, "k", (T, Hkv, d), k.dtype, dev)
-    vs = _rows_strides(v, "v", (T, Hkv, dv), k.dtype, dev)
+    dtype = k.dtype
+    cache, Hkv, d, dv, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)
+    T = k.shape[0]
+    ks = _rows_strides(k, "k", (T, Hkv, d), dtype, dev)
+    vs = _rows_strides(v, "v", (T, Hkv, dv), dtype, dev)
     slots = _i32_buffer(slot_map, "slot_map", (T,), dev)
     guard, ptr, other = _enter(dev, stream)
+    made = ()
     try:
-        ws = _empty(256, torch.uint8, dev, other) if workspace_buf is None else workspace_buf
+        if workspace_buf is None:
+            workspace_buf = _empty(256, dtype=_U8, device=k.device)
+            made = (workspace_buf,)
         st = lib().bpa_cache_append(cache, k.data_ptr(), v.data_ptr(), _TWO_PACK(ks[0], ks[1]), _TWO_PACK(vs[0], vs[1]),
-                                    slots, T, int(max_new), ws.data_ptr(), ws.numel(), ptr)
+                                    slots, T, int(max_new), workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
-        if guard is not None:
-            guard.__exit__(None, None, None)
+        _leave(guard, other, made)
     if st:
         _raise_if(st, "bpa_cache_append")
 
 
-def _pack_batch(q, o, page_table, kv_lens, cu_q, max_q=0, causal=True, window=(-1, -1), scale=None, sink=None):
-    """Packed bpa_cache_batch; o: the output's (row, head) strides."""
+def _pack_batch(q, o_row, o_head, page_table, kv_lens, cu_q, max_q, causal, window, scale, sink):
+    """Packed bpa_cache_batch; o_row, o_head: the output's strides."""
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("q must be [T, Hq, d], page_table [R, max_pages]")
-    T, Hq, _ = q.shape
-    dev, (R, max_pages) = q.device, page_table.shape
-    st = _rows_strides(q, "q", q.shape, q.dtype, dev)
-    if sink is not None and (sink.dtype is not torch.float32 or sink.shape != (Hq,) or not sink.is_contiguous() or
-                             sink.device != dev):
+    shape, dev, (R, max_pages) = q.shape, q.get_device(), page_table.shape
+    T, Hq, _ = shape
+    st = _rows_strides(q, "q", shape, q.dtype, dev)
+    if sink is not None and (sink.dtype is not _F32 or sink.shape != (Hq,) or not sink.is_contiguous() or
+                             sink.get_device() != dev):
         raise ValueError("sink must be a contiguous float32 [Hq] tensor on q's device")
     wl, wr = (-1, -1) if window is None else window
-    return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, int(max_q), q.data_ptr(), st[0], st[1], o[0], o[1],
+    return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, int(max_q), q.data_ptr(), st[0], st[1], o_row, o_head,
                        _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
                        _i32_buffer(cu_q, "cu_q", (R + 1,), dev), 0.0 if scale is None else float(scale),
                        1 if causal else 0, int(wl), int(wr), 0 if sink is None else sink.data_ptr())
 
 
-def make_cache_batch(q, page_table, kv_lens, cu_q, **kw) -> bpa_cache_batch:
+def make_cache_batch(q, page_table, kv_lens, cu_q, *, max_q=0, causal=True, window=(-1, -1), scale=None,
+                     sink=None) -> bpa_cache_batch:
     """A bpa_cache_batch (all but o_strides) of the step's tensors (no data is touched); keywords as
     bpa_cache_attn's."""
-    return bpa_cache_batch.from_buffer_copy(_pack_batch(q, (0, 0), page_table, kv_lens, cu_q, **kw))
+    return bpa_cache_batch.from_buffer_copy(_pack_batch(q, 0, 0, page_table, kv_lens, cu_q, max_q, causal, window, scale,
+                                                        sink))
 
 
 def bpa_cache_attn_workspace_size(cache: bpa_cache_desc, batch: bpa_cache_batch) -> int:
     return int(lib().bpa_cache_attn_workspace_size(ctypes.byref(cache), ctypes.byref(batch)))
 
 
-def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, cu_q, *, o=None, m=None, l=None,
-                   workspace_buf=None, stream=None, **kw):
+def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, cu_q, *, max_q=0, causal=True,
+                   window=(-1, -1), scale=None, sink=None, o=None, m=None, l=None, workspace_buf=None, stream=None):
     """Attention of packed rows q [T, Hq, d] over the cache.  Returns (o, m, l): o [T, Hq, dv]; m and
-    l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  Keywords: max_q (the most rows
-    of a request, guides the choice of kernel), causal, window, scale, sink."""
-    cache, _, _, _, d, dv = _pack_cache(k_cache, v_cache, k_scale, v_scale, q.dtype)
-    dev = k_cache.device
-    if q.dim() != 3 or q.shape[2] != d or q.device != dev:
+    l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  max_q: the most rows of a
+    request (0: unknown), guides the choice of kernel."""
+    dtype = q.dtype
+    cache, _, d, dv, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)
+    if q.dim() != 3 or q.shape[2] != d or q.get_device() != dev:
         raise ValueError("q must be [T, Hq, d] with k_cache's head dim and device")
     T, Hq, _ = q.shape
+    stats = (Hq, T)
     for t, name in ((m, "m"), (l, "l")):
-        if t is not None and (t.dtype is not torch.float32 or t.shape != (Hq, T) or not t.is_contiguous() or
-                              t.device != dev):
+        if t is not None and (t.dtype is not _F32 or t.shape != stats or not t.is_contiguous() or t.get_device() != dev):
             raise ValueError(f"{name} must be a contiguous float32 [Hq, T] tensor on q's device")
-    os = (Hq * dv, dv) if o is None else _rows_strides(o, "o", (T, Hq, dv), q.dtype, dev)
-    batch = _pack_batch(q, os, page_table, kv_lens, cu_q, **kw)
+    st = (Hq * dv, dv) if o is None else _rows_strides(o, "o", (T, Hq, dv), dtype, dev)
+    batch = _pack_batch(q, st[0], st[1], page_table, kv_lens, cu_q, max_q, causal, window, scale, sink)
     guard, ptr, other = _enter(dev, stream)
+    made = []
     try:
+        L, where = lib(), q.device
         if o is None:
-            o = _empty((T, Hq, dv), q.dtype, dev, other)
+            o = _empty((T, Hq, dv), dtype=dtype, device=where)
+            made.append(o)
         if m is None:
-            m = _empty((Hq, T), torch.float32, dev, other)
+            m = _empty(stats, dtype=_F32, device=where)
+            made.append(m)
         if l is None:
-            l = _empty((Hq, T), torch.float32, dev, other)
-        L = lib()
+            l = _empty(stats, dtype=_F32, device=where)
+            made.append(l)
         if workspace_buf is None:
             need = L.bpa_cache_attn_workspace_size(cache, batch)
             if need == 0:
                 _raise_if(BPA_ERR_INVALID_ARG, "bpa_cache_attn_workspace_size")
-            ws = _empty(need, torch.uint8, dev, other)
-        else:
-            ws = workspace_buf
-        st = L.bpa_cache_attn(cache, batch, o.data_ptr(), m.data_ptr(), l.data_ptr(), ws.data_ptr(), ws.numel(), ptr)
+            workspace_buf = _empty(need, dtype=_U8, device=where)
+            made.append(workspace_buf)
+        st = L.bpa_cache_attn(cache, batch, o.data_ptr(), m.data_ptr(), l.data_ptr(), workspace_buf.data_ptr(),
+                              workspace_buf.numel(), ptr)
     finally:
-        if guard is not None:
-            guard.__exit__(None, None, None)
+        _leave(guard, other, made)
     if st:
         _raise_if(st, "bpa_cache_attn")
     return o, m, l
