@@ -117,7 +117,7 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
 
 // Tensor-core kernel for requests of more than kFewRows rows (bf16, head dims in steps of 16 up to 128,
 // pages in steps of 16 tokens); the others are left alone.  counter: zero before the launch.
-bool cache_attn_tc_supported(const CacheAttnArgs& a);
+bool cache_attn_tc_takes(const CacheAttnArgs& a);       // supported, and there may be enough such requests
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a);      // plain (not swizzled) boxes
 cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, cudaStream_t s);
 

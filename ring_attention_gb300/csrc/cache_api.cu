@@ -207,6 +207,10 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
         return fail(BPA_ERR_INVALID_ARG, "k, v, their strides or slot_map is NULL");
     for (int i = 0; i < 2; ++i)
         if (k_strides[i] < 0 || v_strides[i] < 0) return fail(BPA_ERR_INVALID_ARG, "strides must be >= 0");
+    const int32_t extents[3] = {cache->num_pages, cache->Hkv, cache->page_size};
+    for (int i = 0; i < 3; ++i)
+        if (extents[i] > 1 && (cache->k_cache_strides[i] == 0 || cache->v_cache_strides[i] == 0))
+            return fail(BPA_ERR_INVALID_ARG, "a cache that is written needs strides above 0");
     if (static_cast<int64_t>(T) * cache->Hkv > kMost)
         return fail(BPA_ERR_UNSUPPORTED, "T * Hkv above 2^30");
     if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
@@ -265,8 +269,7 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
         CUtensorMap maps[2];
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&
             make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows, true)) {
-            // requests of many rows first (none where no request may have so many)
-            const bool many = static_cast<int64_t>(a.max_q) * a.G > kFewRows && cache_attn_tc_supported(a);
+            const bool many = cache_attn_tc_takes(a);   // requests of many rows first
             if (many) {
                 st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
                 if (st != BPA_OK) return st;

@@ -10,7 +10,9 @@
 //   W = exp2(u - M + 7) in fp16, M the row's running maximum of u (moved only when it grows by
 //       more than 8, so W <= 2^15);  O += W V;  L += sum W / (v scale);  o = O / L
 // One exponential serves the numerator and the denominator, with 1 / (v scale) relative to the first
-// scale that the item meets; a page below 2^-100 of that one, or of zeros (scale 0), counts as 2^-100 of it.
+// scale lv0 that the item meets (a page below 2^-90 of that one counts as 2^-90 of it).  Pages of zeros
+// (scale 0) have no scale of their own: they count 2^-20 below the largest met so far, so their keys stay
+// in L (far below, W would leave float32's range) and do not push the others' W out of fp16's.
 //
 // Bounded by the softmax's instructions and the exponentials beside the products (compute, not
 // bytes): about three instructions and one exponential a score.  Two threads share a row (64 columns
@@ -43,7 +45,8 @@ constexpr int kRows = 256;            // rows of an item
 constexpr int kMetas = 4;             // records of key tiles in flight
 constexpr int kMma = 16, kAux = 17, kConv = 20;   // first warps of the roles
 constexpr float kTau = 8.f, kOff = 7.f;
-constexpr float kFar = 100.f;         // log2 of the largest ratio of the v scales below the item's first
+constexpr float kFar = 90.f;          // log2: scales further below the item's first count as this far below
+constexpr float kZeros = 20.f, kAllZeros = -80.f;   // log2 scale of a page of zeros: below the largest so far; before any
 
 struct TileMeta {
     int key0, len, end, pad;
@@ -348,14 +351,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     mbar_arrive(BAR(C::B_IF + (k & 1)));
                 }
                 bool ok = true;
+                float lvmax = -INFINITY;
                 for (int j = 0; j < tiles; ++j, ++t) {
                     const int sl = t % kMetas, id2 = page_of(j + 2);
                     float ks1, vs1;
                     scales_of(id1, ks1, vs1);
                     if (t >= kMetas && !(ok = wait(C::B_ME + sl, t / kMetas - 1, 0xE6))) break;
                     TileMeta* m = metas + sl;
+                    float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : -INFINITY;
+                    lvmax = fmaxf(lvmax, lv);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) lvmax = fmaxf(lvmax, __shfl_xor_sync(0xffffffffu, lvmax, o));
+                    if (lv == -INFINITY) lv = lvmax == -INFINITY ? kAllZeros : lvmax - kZeros;
                     if (lane < 8) {
-                        const float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : lv0 - kFar;
                         m->a[lane] = ks * a.scale * kLog2e;
                         m->lv[lane] = lv;
                         m->e[lane] = ex2(lv0 - lv);
@@ -693,9 +701,16 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* co
 
 }  // namespace
 
-bool cache_attn_tc_supported(const CacheAttnArgs& a) {
-    return a.dtype == BPA_BF16 && a.d % 16 == 0 && a.dv % 16 == 0 && a.d <= 128 && a.dv <= 128 && (a.d > 64 || a.dv <= 64) &&
-           a.P % 16 == 0;
+bool cache_attn_tc_takes(const CacheAttnArgs& a) {
+    if (a.dtype != BPA_BF16 || a.d % 16 || a.dv % 16 || a.d > 128 || a.dv > 128 || (a.d <= 64 && a.dv > 64) || a.P % 16) return false;
+    const int64_t rows = static_cast<int64_t>(a.max_q) * a.G;
+    if (rows <= kFewRows) return false;
+    // An item's keys are not shared between CTAs here, as they are in the kernel for few rows: with few
+    // items (one token of 128 heads over a long context) that one fills the GPU and this one does not.
+    // With all CTAs busy this one is 4.7 times faster (pieces of prompts 1531 and 7225 us), so from about
+    // a fifth of them on it wins.
+    const int64_t items = std::min(a.R * ((rows + kRows - 1) / kRows), static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
+    return items >= 32;
 }
 
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a) { return {a.d <= 64 ? 64 : 128, a.dv <= 64 ? 64 : 128, 16}; }

@@ -102,6 +102,9 @@ def test_append_refuses(bpa):
         assert call(_cache(bpa), **bad) == 1, bad
     assert call(_cache(bpa), n=255) == 3 and call(_cache(bpa), ws=None) == 3
     assert call(_cache(bpa), T=1 << 30) == 2
+    flat = _cache(bpa)
+    flat.k_cache_strides[1] = 0                  # heads over one another: read at most, never written
+    assert call(flat) == 1
 
 
 def test_plan_refuses(bpa):

@@ -13,6 +13,8 @@ with A = sum p |v| / l (the same attention over |v|) and Z = the largest sum_c |
     whatever its own size, times |v| <= 448: n 2^-34 448 H;
   * the output is rounded once: 2^-8 |o| in bf16, 2^-24 |o| in float32.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -345,6 +347,19 @@ def test_attention_matches_the_definition(bpa, case, dtype):
     run_and_check(bpa, make_step(np.random.default_rng(sum(case[0]) + case[4]), *case), dtype)
 
 
+MANY = [     # ctx, new, Hq, Hkv, d, dv, P: enough requests of more than 64 rows for the kernel for many rows,
+             # beside others of few; row tiles half full, one row too many, of one token
+    ([0, 130, 37, 250], [70, 1, 33, 9], 32, 8, 128, 128, 64), ([300, 5, 64, 127, 1], [17, 20, 64, 1, 129], 32, 8, 128, 64, 32),
+    ([90, 0, 15], [130, 40, 257], 32, 16, 64, 64, 16), ([40, 200], [30, 2], 96, 16, 80, 112, 128), ([0, 60], [40, 41], 112, 16, 96, 48, 64),
+    ([600, 1], [5, 6], 256, 16, 64, 64, 16),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"H{c[2]}_{c[3]}_d{c[4]}_{c[5]}_P{c[6]}_q{max(c[1])}")
+def test_attention_many_rows_beside_few(bpa, case):
+    run_and_check(bpa, make_step(np.random.default_rng(sum(case[1]) + case[4]), *case, pad=3), torch.bfloat16)
+
+
 MASKS = {"window": dict(window=(20, -1)), "window_0": dict(window=(0, -1)), "not_causal": dict(causal=False),
          "band": dict(causal=False, window=(10, 5)), "right": dict(causal=False, window=(-1, 0)),
          "scale": dict(scale=0.3), "wide": dict(window=(2 ** 31 - 1, 2 ** 31 - 1), causal=False)}
@@ -356,6 +371,62 @@ MASKS = {"window": dict(window=(20, -1)), "window_0": dict(window=(0, -1)), "not
 def test_attention_masks(bpa, mask, new, dtype):
     c = make_step(np.random.default_rng(8), [200, 0, 63], new, 8, 2, 64, 64, 16, pad=2)
     run_and_check(bpa, c, dtype, **MASKS[mask])
+
+
+@pytest.mark.parametrize("mask", MASKS)
+def test_attention_masks_many_rows(bpa, mask):
+    c = make_step(np.random.default_rng(20), [200, 0, 63, 140], [40, 65, 3, 20], 64, 16, 64, 64, 16, pad=2)
+    run_and_check(bpa, c, torch.bfloat16, **MASKS[mask])
+
+
+def test_attention_many_rows_sinks_scales_and_ranges(bpa):
+    rng = np.random.default_rng(21)
+    sink = rng.standard_normal(64) * 3
+    for qmag in (1e-6, 1.0, 30.0, 1e4):
+        c = make_step(rng, [90, 0, 30, 1], [40, 20, 33, 50], 64, 16, 128, 128, 32, pad=3, qmag=qmag)
+        c["kv"] = c["kv"].copy()
+        c["kv"][1] = 0                            # a request that waits
+        run_and_check(bpa, c, torch.bfloat16, sink=sink)
+        c["kv"][0] = 5                            # fewer keys than rows
+        run_and_check(bpa, c, torch.bfloat16, sink=sink)
+        run_and_check(bpa, c, torch.bfloat16)
+    c = make_step(rng, [150, 70], [60, 40], 64, 16, 64, 64, 16)
+    c["vs"][:] = np.exp2(rng.integers(-30, 30, c["vs"].shape) - 7.0).astype(np.float32)
+    for page in (c["table"][0, 0], c["table"][0, 2], c["table"][1, 1]):
+        c["vs"][page] = 0
+        c["vc"][page] = 0
+    run_and_check(bpa, c, torch.bfloat16)
+    run_and_check(bpa, c, torch.bfloat16, window=(3, -1))
+
+
+def test_attention_without_statistics(bpa):
+    c = make_step(np.random.default_rng(22), [90, 700, 30], [40, 1, 33], 32, 16, 128, 128, 32)
+    for dtype in (torch.bfloat16, torch.float32):
+        t = on_gpu(c, dtype)
+        o, m, l = bpa.bpa_cache_attn(*t, max_q=40)
+        got = torch.zeros_like(o)
+        D, B = bpa.make_cache_desc(*t[1:5], dtype), bpa.make_cache_batch(t[0], *t[5:], max_q=40)
+        B.o_strides[:] = o.stride()[:2]
+        ws = torch.empty(bpa.bpa_cache_attn_workspace_size(D, B), dtype=torch.uint8, device="cuda")
+        st = bpa.lib().bpa_cache_attn(ctypes.byref(D), ctypes.byref(B), got.data_ptr(), None, None, ws.data_ptr(),
+                                      ws.numel(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0 and torch.equal(got, o)
+
+
+@pytest.mark.parametrize("max_q", [0, 1, 10 ** 6], ids=["unknown", "too_small", "too_large"])
+def test_attention_any_max_q(bpa, max_q):
+    c = make_step(np.random.default_rng(23), [90, 0, 30, 5], [40, 1, 70, 0], 32, 16, 64, 64, 32)
+    t = on_gpu(c, torch.bfloat16)
+    o, m, l = bpa.bpa_cache_attn(*t, max_q=max_q)
+    torch.cuda.synchronize()
+    check_attention(c, torch.bfloat16, o, m, l)
+
+
+def test_attention_one_token_of_many_heads(bpa):
+    # 128 rows of one token, one kv head: the keys are shared out between CTAs all the same
+    run_and_check(bpa, make_step(np.random.default_rng(24), [1500], [1], 128, 1, 128, 64, 64), torch.bfloat16)
+    run_and_check(bpa, make_step(np.random.default_rng(25), [700, 3], [2, 1], 130, 1, 64, 64, 16), torch.float32)
 
 
 @DTYPES
