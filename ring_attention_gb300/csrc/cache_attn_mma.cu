@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                     const float sk = __ldg(a.sink + head) * kLog2e;
                     mf = fmaxf(mm, sk);
                     norm = mm == -INFINITY ? 1.f : ex2(mm - mf);
-                    lf = ll * norm + ex2(sk - mf);
+                    lf = ll * norm + ex2(sk - (mf == -INFINITY ? 0.f : mf));
                 }
                 if (a.m) {
                     a.m[static_cast<int64_t>(head) * a.T + row0 + tok] = mf == -INFINITY ? mf : mf * kLn2;
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
     if (a.sink) {
         const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(m, sk);
         x = m == -INFINITY ? 1.f : ex2(m - nm);
-        l = l * x + ex2(sk - nm);
+        l = l * x + ex2(sk - (nm == -INFINITY ? 0.f : nm));
         m = nm;
     }
     if (a.m && lane == 0) {

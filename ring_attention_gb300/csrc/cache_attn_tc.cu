@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             if (a.sink) {
                 const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(xm, sk);
                 const float old = l;
-                l = (xm == -INFINITY ? l : l * ex2(xm - nm)) + ex2(sk - nm);
+                l = (xm == -INFINITY ? l : l * ex2(xm - nm)) + ex2(sk - (nm == -INFINITY ? 0.f : nm));
                 part = xm == -INFINITY || old == 0.f ? (old != old ? old : 0.f) : old * ex2(xm - nm) / l;   // what the keys have of the row
                 mm = nm;
             }

@@ -399,6 +399,31 @@ def test_attention_many_rows_sinks_scales_and_ranges(bpa):
     run_and_check(bpa, c, torch.bfloat16, window=(3, -1))
 
 
+@pytest.mark.parametrize("new", [[1, 1, 2], [40, 20, 33]], ids=["step", "prompt"])
+@DTYPES
+def test_attention_sink_of_minus_infinity_is_none(bpa, new, dtype):
+    c = make_step(np.random.default_rng(26), [90, 0, 30], new, 32, 16, 64, 64, 16)
+    c["kv"] = c["kv"].copy()
+    c["kv"][1] = 0
+    t = on_gpu(c, dtype)
+    sink = torch.full((32,), -np.inf, device="cuda")
+    for a, b in zip(bpa.bpa_cache_attn(*t, max_q=max(new), sink=sink), bpa.bpa_cache_attn(*t, max_q=max(new))):
+        assert torch.equal(a, b)
+
+
+def test_attention_of_no_rows(bpa):
+    c = make_step(np.random.default_rng(27), [20, 3], [1, 1], 4, 2, 64, 64, 16)
+    t = list(on_gpu(c, torch.bfloat16))
+    t[0], t[7] = t[0][:0], torch.zeros_like(t[7])
+    o, m, l = bpa.bpa_cache_attn(*t)
+    assert o.shape == (0, 4, 64) and m.shape == (4, 0)
+    t[0] = torch.zeros(5, 4, 64, dtype=torch.bfloat16, device="cuda")       # a padded batch of padding alone
+    o = torch.full((5, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    bpa.bpa_cache_attn(*t, o=o)
+    torch.cuda.synchronize()
+    assert (o == 7).all()
+
+
 def test_attention_without_statistics(bpa):
     c = make_step(np.random.default_rng(22), [90, 700, 30], [40, 1, 33], 32, 16, 128, 128, 32)
     for dtype in (torch.bfloat16, torch.float32):
