@@ -13,8 +13,10 @@
 //               2^15); a weight below 2^-33 of the largest is dropped.  float32: W as two halves.
 //
 // Bounded by the bytes of K and V.  So the CTAs are persistent and each takes an equal share of all
-// tiles of all items, whatever the lengths (an item counts kExtra tiles more, about what its start
-// and end cost); a share may begin and end inside an item.  Pieces of items go to the workspace as
+// cost of all items, whatever the lengths: a tile counts one, two or four where its rows take one, two
+// or four of the warps (33 requests of 8 to 48 rows: 45.3 us against 58.8 with every tile counting
+// one), and an item's start and end six more (40 requests of 16 rows a kv head: 55.5 us; three 62.1,
+// ten 56.4).  A share may begin and end inside an item.  Pieces of items go to the workspace as
 // (m, l, O) and a second, small launch joins them in ascending order, so nothing is added in an order
 // that changes.  Per CTA one
 // warp copies tiles by TMA (a page's rows at a time, swizzled) into a ring of stages and passes the
@@ -40,7 +42,8 @@ namespace {
 constexpr int kTile = 64;             // keys per stage
 constexpr int kNW = 4;                // consumer warps
 constexpr int kThreads = 32 * (kNW + 1);
-constexpr int kExtra = 6;             // tiles that an item's start and end count for in a share
+constexpr int kExtra = 6;             // what an item's start and end count for in a share
+constexpr int kCost2 = 2, kCost4 = 4; // what a tile counts for whose rows take two or four of the warps, else 1
 constexpr int kBatch = 8;             // tiles whose page ids and scales are fetched together (four lanes each)
 constexpr float kOff = 9.f;           // log2 of the largest fp16 weight right after M moved
 constexpr float kLazy = 6.f;          // M moves when it grows by more
@@ -160,20 +163,27 @@ BPA_DEV Req own_request(const Work& w, int r) {
 // written too; such a tile holds no allowed key).
 struct Tiles {
     int first, n;
+    int each;                          // what a tile counts for
+    BPA_DEV int cost() const { return n * each + kExtra; }
+    // tiles that end within the first `c` of the cost (a tile is the share's that holds its last part)
+    BPA_DEV int within(long long c) const { return c <= kExtra ? 0 : (static_cast<int>(c) - kExtra) / each; }
 };
+template <int NT>
 BPA_DEV Tiles tiles_of(const CacheAttnArgs& a, const Req& q, int rg, int rows_per) {
-    const int i0 = rg * rows_per, i1 = min(q.n * a.G, i0 + rows_per) - 1;
+    const int i0 = rg * rows_per, i1 = min(q.n * a.G, i0 + rows_per) - 1, rows = i1 - i0 + 1;
+    const int each = rows <= 8 * NT ? 1 : rows <= 16 * NT ? kCost2 : kCost4;
     int lo, hi, x;
     row_keys(a, q, i0 / a.G, lo, x);
     row_keys(a, q, i1 / a.G, x, hi);
-    if (lo > hi) return {0, 1};
-    return {lo / kTile, hi / kTile - lo / kTile + 1};
+    if (lo > hi) return {0, 1, each};
+    return {lo / kTile, hi / kTile - lo / kTile + 1, each};
 }
+template <int NT>
 BPA_DEV long long cost_of_request(const CacheAttnArgs& a, const Req& q, int rows_per) {
     if (q.n == 0) return 0;
     long long n = 0;
     const int groups = (q.n * a.G + rows_per - 1) / rows_per;
-    for (int rg = 0; rg < groups; ++rg) n += tiles_of(a, q, rg, rows_per).n + kExtra;
+    for (int rg = 0; rg < groups; ++rg) n += tiles_of<NT>(a, q, rg, rows_per).cost();
     return n * a.Hkv;
 }
 
@@ -226,11 +236,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     wait_for_previous();               // nothing of the caller's is read or written before
     if (threadIdx.x == 0) rec->flags = rec->where = 0;
 
-    // ---- this CTA's share: [begin, end) of the running sum of tiles and kExtra over the items
+    // ---- this CTA's share: [begin, end) of the running sum of the items' costs
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min(a.R, static_cast<int>(threadIdx.x) * per),
               r1 = min(a.R, r0 + per);
     long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += cost_of_request(a, own_request(w, r), rows_per);
+    for (int r = r0; r < r1; ++r) mine += cost_of_request<NT>(a, own_request(w, r), rows_per);
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -245,13 +255,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         total += s_scan[i];
     }
     before += x - mine;
-    // a share is never empty among the CTAs that take part, so the pieces of an item lie side by side
-    const int parts = static_cast<int>(min(total, static_cast<long long>(w.ctas)));
+    // a share is at least a tile among the CTAs that take part, so the pieces of an item lie side by side
+    const int most = rows_per <= 8 * NT ? 1 : rows_per <= 16 * NT ? kCost2 : kCost4;
+    const int parts = static_cast<int>(min(total / most, static_cast<long long>(w.ctas)));
     const long long begin = cta < parts ? share(total, cta, parts) : total, end = cta < parts ? share(total, cta + 1, parts) : total;
     if (begin < end && begin >= before && begin < before + mine) {
         long long at = before;
         for (int r = r0; r < r1; ++r) {
-            const long long n = cost_of_request(a, own_request(w, r), rows_per);
+            const long long n = cost_of_request<NT>(a, own_request(w, r), rows_per);
             if (begin < at + n) {
                 s_r = r;
                 s_off = begin - at;
@@ -281,13 +292,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
             rq = own_request(w, r);
             if (rq.bad && lane == 0) report(status, ST_CHECK, 0xCD1);
             groups = (rq.n * a.G + rows_per - 1) / rows_per;
-            const long long per_head = cost_of_request(a, rq, rows_per) / a.Hkv;
+            const long long per_head = cost_of_request<NT>(a, rq, rows_per) / a.Hkv;
             hk = static_cast<int>(off / per_head);
             off -= hk * per_head;
-            tl = tiles_of(a, rq, 0, rows_per);
-            while (off >= tl.n + kExtra) {
-                off -= tl.n + kExtra;
-                tl = tiles_of(a, rq, ++rg, rows_per);
+            tl = tiles_of<NT>(a, rq, 0, rows_per);
+            while (off >= tl.cost()) {
+                off -= tl.cost();
+                tl = tiles_of<NT>(a, rq, ++rg, rows_per);
             }
         }
         const int chunk = lane & 3;
@@ -314,13 +325,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                             groups = (rq.n * a.G + rows_per - 1) / rows_per;
                         }
                     }
-                    tl = tiles_of(a, rq, rg, rows_per);
+                    tl = tiles_of<NT>(a, rq, rg, rows_per);
                 }
                 started = true;
                 // [off, to) of the item's cost; its first kExtra are no tiles
-                const long long to = min(static_cast<long long>(tl.n + kExtra), off + left);
-                t = max(static_cast<int>(off) - kExtra, 0);
-                te = max(static_cast<int>(to) - kExtra, 0);
+                const long long to = min(static_cast<long long>(tl.cost()), off + left);
+                t = tl.within(off);
+                te = tl.within(to);
                 const bool lead = t > 0, trail = te < tl.n;
                 kind = lead ? F_LEAD : trail ? F_TRAIL : 0;
                 first = true;
@@ -328,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                 if (t < te) {
                     if (trail && !lead) {
                         // its pieces: up to the last CTA c with total c / parts < the end of the item's cost
-                        const long long at_end = at + (tl.n + kExtra - off);
+                        const long long at_end = at + (tl.cost() - off);
                         out.trail = static_cast<int>((at_end * parts + total - 1) / total) - cta;
                         out.row0 = rq.row0;
                         out.hk = hk;

@@ -360,6 +360,18 @@ def test_attention_many_rows_beside_few(bpa, case):
     run_and_check(bpa, make_step(np.random.default_rng(sum(case[1]) + case[4]), *case, pad=3), torch.bfloat16)
 
 
+@DTYPES
+@pytest.mark.parametrize("window", [(-1, -1), (200, -1)], ids=["all", "window"])
+@pytest.mark.parametrize("few", [False, True], ids=["many_items", "few_items"])
+def test_attention_requests_of_one_to_eight_tokens(bpa, few, window, dtype):
+    # items of one, two and four row tiles whose keys are cut between CTAs at any place
+    rng = np.random.default_rng(30 + few)
+    n = 2 if few else 24
+    new = [8, 1] if few else [1 + i % 8 for i in range(n)]
+    ctx = [int(x) for x in rng.integers(0, 1500, n)]
+    run_and_check(bpa, make_step(rng, ctx, new, 16, 2, 64, 64, 16), dtype, window=window)
+
+
 MASKS = {"window": dict(window=(20, -1)), "window_0": dict(window=(0, -1)), "not_causal": dict(causal=False),
          "band": dict(causal=False, window=(10, 5)), "right": dict(causal=False, window=(-1, 0)),
          "scale": dict(scale=0.3), "wide": dict(window=(2 ** 31 - 1, 2 ** 31 - 1), causal=False)}
