@@ -61,7 +61,7 @@ BPA_DEV float scale_for(float amax) {
 
 // One warp per (ROWS rows, head, tensor): it takes the runs that begin in its rows, one after the
 // other, reading a run twice (largest magnitude, then codes; the second time from L2).  Bounded by the
-// latency of a warp's chain (slots, rows, scale, rows again) rather than by bytes: prompts of 18,000
+// latency of a warp's chain (slots, rows, scale, rows again) rather than by bytes: prompts of 19,000
 // rows x 8 heads x (128 + 64) bf16 channels take 31 us, 2.9 TB/s of their 90 MB; sixteen loads in flight a
 // lane (four: 33 us).  ROWS = 1 when requests bring few rows (every row is then a run of its own, or
 // nearly); ROWS = 16 for prompts, whose runs are whole pages: sixteen times fewer warps that find no

@@ -12,16 +12,19 @@
 //               lie far apart keep their precision.  M moves only when it grows by more than 6 (W <=
 //               2^15); a weight below 2^-33 of the largest is dropped.  float32: W as two halves.
 //
-// Bounded by the bytes of K and V.  So the CTAs are persistent and each takes an equal share of all
-// cost of all items, whatever the lengths: a tile counts one, two or four where its rows take one, two
-// or four of the warps (33 requests of 8 to 48 rows: 45.3 us against 58.8 with every tile counting
-// one), and an item's start and end six more (40 requests of 16 rows a kv head: 55.5 us; three 62.1,
-// ten 56.4).  A share may begin and end inside an item.  Pieces of items go to the workspace as
-// (m, l, O) and a second, small launch joins them in ascending order, so nothing is added in an order
-// that changes.  Per CTA one
-// warp copies tiles by TMA (a page's rows at a time, swizzled) into a ring of stages and passes the
-// page's scales beside them; four warps take 16 keys of a tile each, or more of the keys for a part
-// of the rows.
+// Bounded by the bytes of K and V where a kv head has up to 8 rows: 64 requests of 8,192 tokens, 8 kv
+// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 98.5 us (5.7 TB/s);
+// three of 100,000 to 131,071 tokens 123 us (6.0 TB/s).  With 16 rows by the latency of the warps'
+// instructions (16 keys a step: codes to fp16, both products, 16 rows' softmax, 12 warps on an SM): 40
+// requests of up to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 55.5 us (2.4 TB/s).
+// So the CTAs are persistent and each takes an equal share of all cost of all items, whatever the
+// lengths: a tile counts one, two or four where its rows take one, two or four of the warps (33
+// requests of 8 to 48 rows: 45.3 us against 58.8 with every tile counting one), and an item's start and
+// end six more (the 40 requests above: 55.5 us; three 62.1, ten 56.4).  A share may begin and end inside
+// an item.  Pieces of items go to the workspace as (m, l, O) and a second, small launch joins them in
+// ascending order, so nothing is added in an order that changes.  Per CTA one warp copies tiles by TMA
+// (a page's rows at a time, swizzled) into a ring of stages and passes the page's scales beside them;
+// four warps take 16 keys of a tile each, or more of the keys for a part of the rows.
 //
 // Layouts without bank conflicts or shuffles: channels are permuted between Q and K so that a lane's
 // 16 consecutive bytes of a key feed four products, and keys (n odd: n ^ 4 within eight) so that

@@ -16,7 +16,10 @@
 //
 // Bounded by the softmax's instructions and the exponentials beside the products (compute, not
 // bytes): about three instructions and one exponential a score.  Two threads share a row (64 columns
-// each), so sixteen warps work on the softmax and cover each other's latencies.
+// each), so sixteen warps work on the softmax and cover each other's latencies; its loops stay rolled,
+// since unrolled ones kept the warps waiting for instructions.  Five pieces of prompts, 6,852 rows of 32
+// heads over up to 16,000 tokens, 128 channels: 1,531 us, 921 TFLOP/s (2,222 us with a thread to a row
+// and unrolled loops; 1,738 with eight converting warps; the kernel for few rows 7,225).
 // Roles (768 threads; registers moved to the softmax by setmaxnreg):
 //   warps 0-7, 8-15  softmax of row tile 0, 1; of eight warps the second four take columns 64-127.  They
 //                    also bring their rows of Q into shared memory
