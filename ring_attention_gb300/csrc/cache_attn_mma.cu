@@ -14,9 +14,9 @@
 //
 // Bounded by the bytes of K and V where a kv head has up to 8 rows: 64 requests of 8,192 tokens, 8 kv
 // heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 98.5 us (5.7 TB/s);
-// three of 100,000 to 131,071 tokens 123 us (6.0 TB/s).  With 16 rows by the latency of the warps'
-// instructions (16 keys a step: codes to fp16, both products, 16 rows' softmax, 12 warps on an SM): 40
-// requests of up to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 55.5 us (2.4 TB/s).
+// three of 100,000 to 131,071 tokens 123 us (6.0 TB/s).  Smaller pieces cost more: 40 requests of up
+// to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 55.5 us (2.4 TB/s; 44 us without the
+// arithmetic, 35 without the copies too: launches, items' starts and ends, the hand-over of tiles).
 // So the CTAs are persistent and each takes an equal share of all cost of all items, whatever the
 // lengths: a tile counts one, two or four where its rows take one, two or four of the warps (33
 // requests of 8 to 48 rows: 45.3 us against 58.8 with every tile counting one), and an item's start and
@@ -981,6 +981,9 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     if (p.DVP > p.DP) p.DP = p.DVP;
     if (p.DP == 256 && p.DVP == 64) p.DVP = 128;
     const int64_t rows = static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G;
+    // Up to 8 rows half as many registers leave more CTAs on an SM: 98.5 us against 142 with 16 rows a warp (64
+    // requests of 200 to 8,191 tokens, 4 rows a kv head).  With 16 rows one warp converts a code once: 55
+    // us against 58 with two warps of 8 rows (the 40 requests above), and with 8 to 48 rows 45.1 against 47.0.
     p.NT = rows <= 8 ? 1 : 2;
     p.RT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.rows_per = 8 * p.NT * p.RT;
@@ -1050,7 +1053,9 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     const uintptr_t qa = a.dtype == BPA_BF16 ? 7 : 15;
     w.vec_q = (reinterpret_cast<uintptr_t>(a.q) & qa) == 0 && a.qs[0] % 4 == 0 && a.qs[1] % 4 == 0;
     w.vec_o = a.dtype == BPA_BF16 && (reinterpret_cast<uintptr_t>(a.o) & 3) == 0 && a.os[0] % 2 == 0 && a.os[1] % 2 == 0;
-    // rows of a join block: few when an item is cut into many pieces
+    // Rows of a join block: few when an item is cut into many pieces, whose loads its warps then share.  Always
+    // eight: three long requests 125.6 us against 123.5, one short one 12.3 against 11.9; always one: 62.7
+    // against 45.1 (8 to 48 rows), 101.9 against 99.2 (64 requests of 4).
     const int64_t pieces = w.ctas / (static_cast<int64_t>(a.R) * a.Hkv);
     const int rpb = pieces <= 4 ? 8 : pieces <= 16 ? 4 : pieces <= 64 ? 2 : 1;
     const bool f32 = a.dtype == BPA_FP32;
