@@ -330,23 +330,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 const int first = lo <= hi ? lo / BN : 0, tiles = lo <= hi ? hi / BN - first + 1 : 0;
                 // lanes 0..7: 16 keys each; a tile's page ids are asked for two tiles ahead, its scales one
                 const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
-                auto page_of = [&](int j) {
-                    const int key = (first + j) * BN + 16 * lane;
-                    return lane < 8 && j < tiles && key < rq.len ? table[key / a.P] : INT_MIN;
-                };
-                auto scales_of = [&](int& id, float& ks, float& vs) {
+                auto there = [&](int j) { return lane < 8 && j < tiles && (first + j) * BN + 16 * lane < rq.len; };
+                auto page_of = [&](int j) { return there(j) ? table[((first + j) * BN + 16 * lane) / a.P] : -1; };
+                auto scales_of = [&](int j, int& id, float& ks, float& vs) {
                     ks = vs = 0.f;
                     if (id >= 0 && id < a.num_pages) {
                         ks = a.kscale[static_cast<int64_t>(id) * a.Hkv + hk];
                         vs = a.vscale[static_cast<int64_t>(id) * a.Hkv + hk];
                     } else {
-                        if (id != INT_MIN) report(a.status, ST_CHECK, 0xCE0);
+                        if (there(j)) report(a.status, ST_CHECK, 0xCE0);
                         id = -1;
                     }
                 };
                 int id = page_of(0), id1 = page_of(1);
                 float ks, vs;
-                scales_of(id, ks, vs);
+                scales_of(0, id, ks, vs);
                 const unsigned some = __ballot_sync(0xffffffffu, vs > 0.f);
                 const float lv0 = some ? __log2f(__shfl_sync(0xffffffffu, vs, __ffs(some) - 1)) : 0.f;
                 if (lane == 0) {
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 for (int j = 0; j < tiles; ++j, ++t) {
                     const int sl = t % kMetas, id2 = page_of(j + 2);
                     float ks1, vs1;
-                    scales_of(id1, ks1, vs1);
+                    scales_of(j + 1, id1, ks1, vs1);
                     if (t >= kMetas && !(ok = wait(C::B_ME + sl, t / kMetas - 1, 0xE6))) break;
                     TileMeta* m = metas + sl;
                     float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : -INFINITY;

@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_plan(const PlanArgs a) {
             if (bad) s_bad = 1;
         }
     }
+    __syncthreads();                      // every thread has said whether its requests are bad
     if (threadIdx.x == 0) {
         s_cu[a.R] = static_cast<int>(min(rows.carry, static_cast<long long>(a.T)));
         if (rank == 0) {                  // cleared before the barrier, so before any later report

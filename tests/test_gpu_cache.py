@@ -140,6 +140,19 @@ def test_plan_reports_bad_inputs(bpa):
     assert got[5].max() < len(c["free"]) and got[2].max() < 4 * len(c["free"])
 
 
+@pytest.mark.parametrize("R", [33, 1000, 1024, 2500])
+def test_plan_reports_a_bad_length_anywhere(bpa, R):
+    base = make_plan(np.random.default_rng(5), [3] * R, [1] * R, 4, R)
+    for r in sorted({0, 31, R // 2, R - 1}):
+        c = {**base, "ctx": np.array(base["ctx"])}
+        c["ctx"][r] = -1
+        for _ in range(10):
+            got, ws = run_plan(bpa, c)
+            with pytest.raises(bpa.BpaError):
+                bpa.bpa_check(ws)
+            assert got[0][r] == 0 and (got[0] > 0).sum() == R - 1
+
+
 # ---- append ----------------------------------------------------------------------------------------
 def random_cache(rng, pages, Hkv, P, c, spread=1.0):
     """Codes with the values +-[0, 448] and power-of-two scales, as append leaves them."""
@@ -560,6 +573,24 @@ def test_attention_reports_bad_pages_and_lengths(bpa, new):
         rows = slice(new[0], None)
         other = {**c, "q": c["q"][rows], "table": c["table"][1:], "kv": c["kv"][1:], "cu": c["cu"][1:] - new[0]}
         check_attention(other, torch.bfloat16, o[rows], m[:, rows], l[:, rows])
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 10 ** 6, 2 ** 31 - 1])
+@pytest.mark.parametrize("new", [[1] * 4, [70] * 4], ids=["step", "prompt"])
+def test_attention_reports_bad_pages_of_every_kernel(bpa, new, bad):
+    c = make_step(np.random.default_rng(16), [130, 31, 0, 63], new, 32, 8, 64, 64, 16)
+    c["table"][3, 2] = bad
+    t = on_gpu(c, torch.bfloat16)
+    need = bpa.bpa_cache_attn_workspace_size(bpa.make_cache_desc(*t[1:5], torch.bfloat16),
+                                             bpa.make_cache_batch(t[0], *t[5:], max_q=max(new)))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    o, m, l = bpa.bpa_cache_attn(*t, max_q=max(new), workspace_buf=ws)
+    torch.cuda.synchronize()
+    with pytest.raises(bpa.BpaError):
+        bpa.bpa_check(ws)
+    first = {**c, "q": c["q"][:sum(new[:3])], "table": c["table"][:3], "kv": c["kv"][:3], "cu": c["cu"][:4]}
+    rows = slice(0, sum(new[:3]))
+    check_attention(first, torch.bfloat16, o[rows], m[:, rows], l[:, rows])
 
 
 def test_attention_cache_past_32_bits(bpa):
