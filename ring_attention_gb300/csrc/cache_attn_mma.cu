@@ -812,30 +812,45 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
             }
         }
         if (!consumers_meet()) return;
-        // two channels of a row at a time
-        for (int x = threadIdx.x; x < rows * (8 * F); x += 32 * kNW) {
-            const int row = x / (8 * F), y = x - row * (8 * F), gg = y / F, i = y - gg * F;
-            const int c = (i / (CV / 2)) * 128 + CV * gg + (i % (CV / 2)) * 2;
-            const int tile = row / C::STATS, r = row - tile * C::STATS;
-            const float* at = merge + tile * C::STATE + ((i * NT + (r >> 3)) * 32 + gg * 4 + ((r & 7) >> 1)) * 4 + (r & 1);
-            float y0 = 0.f, y1 = 0.f;
+        // a warp adds four channels of 2 x 4 rows a lane, in the layout in which they were stored (no bank
+        // conflicts; two channels a thread in the order of the output had sixteen-fold ones)
+        for (int x = warp; x < RT * NT * (F / 2); x += kNW) {
+            const int tile = x / (NT * (F / 2)), y = x - tile * (NT * (F / 2)), nt = y / (F / 2), i = 2 * (y - nt * (F / 2));
+            const int r0 = tile * C::STATS + 8 * nt + 2 * j;         // this lane's rows: r0, r0 + 1
+            if (r0 >= rows) continue;
+            const float4* at = reinterpret_cast<const float4*>(merge + tile * C::STATE) + (i * NT + nt) * 32 + lane;
+            float sum[2][4] = {};
             for (int k = 0; k < slices; ++k) {
-                const float f0 = stats[k * RT * C::STATS + row].w;
-                y0 = fmaf(at[k * RT * C::STATE], f0, y0);
-                y1 = fmaf(at[k * RT * C::STATE + 2], f0, y1);
+                const float f0 = stats[k * RT * C::STATS + r0].w, f1 = stats[k * RT * C::STATS + r0 + 1].w;
+                const float4 p = at[k * RT * (C::STATE / 4)], q = at[k * RT * (C::STATE / 4) + NT * 32];
+                sum[0][0] = fmaf(p.x, f0, sum[0][0]);
+                sum[0][1] = fmaf(p.z, f0, sum[0][1]);
+                sum[0][2] = fmaf(q.x, f0, sum[0][2]);
+                sum[0][3] = fmaf(q.z, f0, sum[0][3]);
+                sum[1][0] = fmaf(p.y, f1, sum[1][0]);
+                sum[1][1] = fmaf(p.w, f1, sum[1][1]);
+                sum[1][2] = fmaf(q.y, f1, sum[1][2]);
+                sum[1][3] = fmaf(q.w, f1, sum[1][3]);
             }
-            if (flags & (F_LEAD | F_TRAIL)) {
-                const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
-                *reinterpret_cast<float2*>(w.part + slot * DVP + c) = make_float2(y0, y1);
-            } else if (c < a.dv) {
-                const int tok = (i0 + row) / a.G, head = hk * a.G + (i0 + row) - tok * a.G;
-                E* o = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] +
-                       static_cast<int64_t>(head) * a.os[1] + c;
-                if (!SPLIT && w.vec_o) {
-                    *reinterpret_cast<uint32_t*>(o) = pack_bf16(y0, y1);
-                } else {
-                    o[0] = static_cast<E>(y0);
-                    o[1] = static_cast<E>(y1);
+            const int c = (i / (CV / 2)) * 128 + CV * g + (i % (CV / 2)) * 2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = r0 + e;
+                if (row >= rows) continue;
+                if (flags & (F_LEAD | F_TRAIL)) {
+                    const int64_t slot = (2 * static_cast<int64_t>(cta) + (flags & F_TRAIL ? 1 : 0)) * rows_per + row;
+                    *reinterpret_cast<float4*>(w.part + slot * DVP + c) = make_float4(sum[e][0], sum[e][1], sum[e][2], sum[e][3]);
+                } else if (c < a.dv) {
+                    const int tok = (i0 + row) / a.G, head = hk * a.G + (i0 + row) - tok * a.G;
+                    E* o = static_cast<E*>(a.o) + static_cast<int64_t>(row0 + tok) * a.os[0] +
+                           static_cast<int64_t>(head) * a.os[1] + c;
+                    if (!SPLIT && w.vec_o) {
+                        reinterpret_cast<uint32_t*>(o)[0] = pack_bf16(sum[e][0], sum[e][1]);
+                        reinterpret_cast<uint32_t*>(o)[1] = pack_bf16(sum[e][2], sum[e][3]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) o[h] = static_cast<E>(sum[e][h]);
+                    }
                 }
             }
         }
