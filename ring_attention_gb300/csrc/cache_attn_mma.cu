@@ -13,14 +13,14 @@
 //               2^15); a weight below 2^-33 of the largest is dropped.  float32: W as two halves.
 //
 // Bounded by the bytes of K and V where a kv head has up to 8 rows: 64 requests of 8,192 tokens, 8 kv
-// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 98.5 us (5.7 TB/s);
-// three of 100,000 to 131,071 tokens 123 us (6.0 TB/s).  Smaller pieces cost more: 40 requests of up
-// to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 55.5 us (2.4 TB/s; 44 us without the
-// arithmetic, 35 without the copies too: launches, items' starts and ends, the hand-over of tiles).
+// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 97.8 us (5.7 TB/s);
+// three of 100,000 to 131,071 tokens 122 us (6.1 TB/s).  Smaller pieces cost more: 40 requests of up
+// to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 50.7 us (2.6 TB/s; mostly launches,
+// items' starts and ends and the hand-over of tiles, which stay without the arithmetic).
 // So the CTAs are persistent and each takes an equal share of all cost of all items, whatever the
 // lengths: a tile counts one, two or four where its rows take one, two or four of the warps (33
-// requests of 8 to 48 rows: 45.3 us against 58.8 with every tile counting one), and an item's start and
-// end six more (the 40 requests above: 55.5 us; three 62.1, ten 56.4).  A share may begin and end inside
+// requests of 8 to 48 rows, 41.5 us now: 45.3 against 58.8 with every tile counting one), and an item's
+// start and end six more (the 40 requests above: 51.3 us; four 53.9).  A share may begin and end inside
 // an item.  Pieces of items go to the workspace as (m, l, O) and a second, small launch joins them in
 // ascending order, so nothing is added in an order that changes.  Per CTA one warp copies tiles by TMA
 // (a page's rows at a time, swizzled) into a ring of stages and passes the page's scales beside them;
@@ -762,8 +762,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                     m[nt][e] = n;
                 }
         // Each warp's (m, l, M) and sums go to shared memory; a thread per row turns them into the
-        // slices' factors, then all threads add the slices up.  Rolled loops: this code runs seldom, and
-        // its instructions come from far.
+        // slices' factors, then all threads add the slices up (every warp working out its rows' factors
+        // itself, with one meeting less: 51.6 us against 50.7 for the 40 requests above).
         constexpr int CV = (DVP < 128 ? DVP : 128) / 8, F = DVP / 16;
         const int RT = kNW / slices, rows = min(nr - i0, RT * C::STATS);
         float4* stats = reinterpret_cast<float4*>(merge + kNW * C::STATE);   // [slice][row of the item]
@@ -783,8 +783,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         for (int row = threadIdx.x; row < rows; row += 32 * kNW) {
             const int tok = (i0 + row) / a.G, head = hk * a.G + (i0 + row) - tok * a.G;
             float mm = -INFINITY, ll = 0.f;
+#pragma unroll 4
             for (int k = 0; k < slices; ++k) mm = fmaxf(mm, stats[k * RT * C::STATS + row].x);
             const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
             for (int k = 0; k < slices; ++k) {
                 const float4 b = stats[k * RT * C::STATS + row];
                 ll += b.y * ex2(b.x - ref);
@@ -806,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                 }
                 norm = lf == 0.f ? 0.f : norm / lf;
             }
+#pragma unroll 4
             for (int k = 0; k < slices; ++k) {
                 float4& b = stats[k * RT * C::STATS + row];
                 b.w = b.z == -INFINITY ? (norm != norm ? norm : 0.f) : ex2(b.z - kOff - ref) * norm;
@@ -820,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
             if (r0 >= rows) continue;
             const float4* at = reinterpret_cast<const float4*>(merge + tile * C::STATE) + (i * NT + nt) * 32 + lane;
             float sum[2][4] = {};
+#pragma unroll 4
             for (int k = 0; k < slices; ++k) {
                 const float f0 = stats[k * RT * C::STATS + r0].w, f1 = stats[k * RT * C::STATS + r0 + 1].w;
                 const float4 p = at[k * RT * (C::STATE / 4)], q = at[k * RT * (C::STATE / 4) + NT * 32];
@@ -998,7 +1002,7 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     const int64_t rows = static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G;
     // Up to 8 rows half as many registers leave more CTAs on an SM: 98.5 us against 142 with 16 rows a warp (64
     // requests of 200 to 8,191 tokens, 4 rows a kv head).  With 16 rows one warp converts a code once: 55
-    // us against 58 with two warps of 8 rows (the 40 requests above), and with 8 to 48 rows 45.1 against 47.0.
+    // us against 58 with two warps of 8 rows (40 of up to 4,095), and with 8 to 48 rows 45.1 against 47.0.
     p.NT = rows <= 8 ? 1 : 2;
     p.RT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.rows_per = 8 * p.NT * p.RT;
