@@ -13,8 +13,8 @@
 //               2^15); a weight below 2^-33 of the largest is dropped.  float32: W as two halves.
 //
 // Bounded by the bytes of K and V where a kv head has up to 8 rows: 64 requests of 8,192 tokens, 8 kv
-// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 97.8 us (5.7 TB/s);
-// three of 100,000 to 131,071 tokens 122 us (6.1 TB/s).  Smaller pieces cost more: 40 requests of up
+// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 97.2 us (5.8 TB/s);
+// three of 100,000 to 131,071 tokens 121 us (6.1 TB/s).  Smaller pieces cost more: 40 requests of up
 // to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 50.7 us (2.6 TB/s; mostly launches,
 // items' starts and ends and the hand-over of tiles, which stay without the arithmetic).
 // So the CTAs are persistent and each takes an equal share of all cost of all items, whatever the
