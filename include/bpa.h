@@ -283,8 +283,9 @@ bpa_status bpa_select_blocks_noalloc(const void* q, const void* k, int32_t dtype
  *   infinities) and stands for code * k_scale[page, head]; likewise v_cache with dv channels.
  *   Element (page, h, t, c) sits at base + page*sp + h*sh + t*st + c for strides (sp, sh, st) in
  *   elements (= bytes), so both [pages, Hkv, page_size, d] and [pages, page_size, Hkv, d] fit.
- *   Scales are finite, float32 [num_pages, Hkv], contiguous; bpa_cache_append writes powers of
- *   two, or 0 for a page whose rows are all zero (its codes are then all zero).
+ *   Scales are finite and >= 0, float32 [num_pages, Hkv], contiguous; bpa_cache_append writes
+ *   powers of two, or 0 for a page that holds no finite value but 0 (its codes are then 0 or NaN).
+ *   Under a scale of 0 every code stands for 0, but those of NaN for NaN.
  *   Request r holds tokens 0..kv_lens[r]-1; token p sits in page page_table[r, p / page_size] at
  *   offset p % page_size.  Table entries past the request's pages are never read.
  *   Packed rows: the step's rows of all requests stand one after another, rows
@@ -388,8 +389,10 @@ size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cach
  *     m, l, o as in bpa_fwd (a sink joins m and l); a row with no allowed key gives o = 0 and
  *     m = -inf, l = 0 (with a sink: m = sink, l = 1).
  * o [T, Hq, dv]; m, l float32 [Hq, T], contiguous, both or neither NULL.  Slots past
- * kv_lens[r] may hold anything, NaN included.  A value that is not finite among a request's own
- * tokens makes that request's outputs of that kv head NaN wherever the value is read. */
+ * kv_lens[r] may hold anything, NaN included.  Codes of NaN among a request's own tokens: of k, they
+ * make o and l NaN in every row and head that may attend to the token; of v, those channels of o.  The
+ * masked rows of the same request and kv head may become NaN in the same places (the token's weight of
+ * 0 times NaN, where it shares a tile with keys that the row reads), all others keep their values. */
 bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* batch, void* o, float* m, float* l,
                           void* workspace, size_t workspace_bytes, void* stream);
 

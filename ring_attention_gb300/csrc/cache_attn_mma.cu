@@ -652,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                     move |= u[nt][e] > M[nt][e] + kLazy;
                 }
             }
-            if (!(vs > 0.f)) continue;             // a page of zeros: nothing to add (its scale is 0)
             // ---- weights in fp16, relative to M
             if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -678,8 +677,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
             uint32_t wf[NT][2], wl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float t0 = (M[nt][0] == -INFINITY ? 0.f : M[nt][0] - lv) - kOff;
-                const float t1 = (M[nt][1] == -INFINITY ? 0.f : M[nt][1] - lv) - kOff;
+                // a page of scale 0 has lv = -inf and so weights of 0, as has a row without a key so far; the
+                // product is taken all the same, for codes that stand for NaN (0 * NaN)
+                const float t0 = (M[nt][0] == -INFINITY ? INFINITY : M[nt][0] - lv) - kOff;
+                const float t1 = (M[nt][1] == -INFINITY ? INFINITY : M[nt][1] - lv) - kOff;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float y0 = ex2(z[nt][2 * k] - t0), y1 = ex2(z[nt][2 * k + 1] - t1);

@@ -701,3 +701,83 @@ def test_two_calls_at_once(bpa):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ---- values that are not finite ----------------------------------------------------------------------
+KERNELS = {   # ctx, new, Hq, Hkv, d, dv, P: 2 P + 1 and more tokens, so that a page of one token ends the first request
+    "few_rows": ([128, 70], [1, 2], 8, 4, 128, 64, 64), "few_rows_pages_of_16": ([144, 31], [1, 3], 8, 2, 64, 64, 16),
+    "many_rows": ([89, 20], [40, 30], 32, 16, 128, 128, 32), "any_shape": ([95, 30], [2, 1], 4, 2, 72, 40, 48),
+}
+
+
+def spoil(c, which, page_of, alone):
+    """A copy of the step with NaN in channels 3 to 5 of kv head 1 of a request's token: (copy, clean copy with zeros
+    in their place, the request, the token).  alone: the page's other values and so its scale are 0, as
+    append leaves a page that has no finite value but 0."""
+    r, token = page_of
+    P = c["kc"].shape[2]
+    page, off = c["table"][r, token // P], token % P
+    bad = {**c, **{n: c[n].copy() for n in ("kc", "vc", "ks", "vs")}}
+    for n in which:
+        codes, scale = bad[n + "c"], bad[n + "s"]
+        if alone:
+            codes[page, 1], scale[page, 1] = 0, 0
+        codes[page, 1, off, 3:6] = 0x7F
+    clean = {**bad, **{n: bad[n].copy() for n in ("kc", "vc")}}
+    for n in which:
+        clean[n + "c"][page, 1, off, 3:6] = 0
+    return bad, clean
+
+
+@DTYPES
+@pytest.mark.parametrize("alone", [True, False], ids=["alone", "among_others"])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_keeps_what_is_not_finite(bpa, kernel, which, alone, dtype):
+    case = KERNELS[kernel]
+    c = make_step(np.random.default_rng(31), *case)
+    end = c["kv"][0] - 1                               # the last token: only the last row of the request sees it
+    T, Hq = c["q"].shape[:2]
+    mine = np.arange(Hq) // (Hq // c["kc"].shape[1]) == 1
+    for token in (end, 0, 37):
+        bad, clean = spoil(c, which, (0, int(token)), alone)
+        got, want = (bpa.bpa_cache_attn(*on_gpu(x, dtype), max_q=c["max_q"]) for x in (bad, clean))
+        torch.cuda.synchronize()
+        check_attention(clean, dtype, *want)
+        p = c["kv"][0] - c["cu"][1] + np.arange(c["cu"][1])
+        sees = np.zeros((T, Hq), bool)
+        sees[:c["cu"][1]] = (p >= token)[:, None] & mine
+        other = np.ones((T, Hq), bool)                 # rows of other requests and heads
+        other[:c["cu"][1]] = ~mine
+        wrong = torch.zeros(got[0].shape, dtype=torch.bool)
+        wrong[torch.from_numpy(sees)] = True
+        if which == "v":
+            wrong[..., :3] = wrong[..., 6:] = False
+        assert sees.any() and torch.isnan(got[0].cpu()[wrong]).all()
+        assert torch.equal(got[0].cpu()[other], want[0].cpu()[other])
+        assert torch.equal(got[1].T.cpu()[other], want[1].T.cpu()[other]) and torch.equal(got[2].T.cpu()[other], want[2].T.cpu()[other])
+        if which == "v":                               # the weights and the other channels are what they were
+            assert torch.equal(got[0][..., 6:], want[0][..., 6:])
+            assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        else:
+            assert torch.isnan(got[2].T.cpu()[sees]).all()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf], ids=str)
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_append_then_attend_what_is_not_finite(bpa, kernel, value):
+    # the first token of a fresh page has a value head without a finite value
+    ctx, new, Hq, Hkv, d, dv, P = KERNELS[kernel]
+    c = make_step(np.random.default_rng(32), ctx, new, Hq, Hkv, d, dv, P)
+    end = int(c["kv"][0]) // P * P                     # a page's first token: the last one or one before it
+    page = int(c["table"][0, end // P])
+    t = on_gpu(c, torch.bfloat16)
+    k, v = torch.randn(1, Hkv, d, device="cuda").bfloat16(), torch.randn(1, Hkv, dv, device="cuda").bfloat16()
+    v[0, 1] = value
+    bpa.bpa_cache_append(k, v, i32([page * P + end % P]), *t[1:5], max_new=1)
+    o, m, l = bpa.bpa_cache_attn(*t, max_q=max(new))
+    torch.cuda.synchronize()
+    heads = slice(Hq // Hkv, 2 * Hq // Hkv)
+    last = int(c["cu"][1]) - 1
+    assert torch.isnan(o[last, heads]).all() and torch.isfinite(l[heads, last]).all()
+    assert torch.isfinite(o[last, :Hq // Hkv]).all() and torch.isfinite(o[last + 1:]).all()
