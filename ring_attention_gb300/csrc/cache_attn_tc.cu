@@ -52,7 +52,8 @@ constexpr float kFar = 90.f;          // log2: scales further below the item's f
 constexpr float kZeros = 20.f, kAllZeros = -80.f;   // log2 scale of a page of zeros: below the largest so far; before any
 
 struct TileMeta {
-    int key0, len, end, pad;
+    int key0, len, end;
+    uint32_t zero;                    // bit c: the v scale of chunk c is 0
     float a[8], lv[8], e[8];          // k scale * softmax scale * log2(e); log2 v scale; 2^(lv0 - lv)
 };
 struct Item {
@@ -103,6 +104,9 @@ BPA_DEV uint32_t cvt_hi(uint32_t four) {
     asm("{.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;}" : "=r"(h) : "r"(four));
     return h;
 }
+
+// Codes under a scale of 0: NaN stays NaN, whatever else they are counts as 0.
+BPA_DEV uint32_t nan_or_0(uint32_t four) { return __vcmpeq4(four & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x7f7f7f7fu; }
 
 // This thread's 64 scores of its row (columns c0 ..).  Rolled loops over 32 columns: the roles' code
 // together has to stay in the instruction caches (unrolled, the warps spent two fifths of their time
@@ -253,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             const int st = t % C::NS, use = t / C::NS, sl = t % kMetas;
             if (!wait(C::B_MF + sl, t / kMetas, 0xE0) || metas[sl].end) break;
             const int left = metas[sl].len - metas[sl].key0;
+            const uint32_t zero = metas[sl].zero >> (2 * wq) & 3;   // this warp's two 16 rows
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
             if (!wait(C::B_RF, t, 0xE1) || (use > 0 && !wait(C::B_KE + st, use - 1, 0xE2))) break;
@@ -262,6 +267,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 mbar_arrive(BAR(C::B_RE));
             }
             if (!wait(C::B_RF + 1, t, 0xE3) || (use > 0 && !wait(C::B_VE + st, use - 1, 0xE4))) break;
+            if (zero) {                // rare, and 5 % of the prompts' time inside the conversion's loop
+#pragma unroll 1
+                for (int i = lane; i < 2 * C::RBV; i += 32)       // a row is RBV / 16 pieces: 32 rows of them
+                    if (zero >> (i / C::RBV) & 1) {
+                        uint4* at = reinterpret_cast<uint4*>(smem + C::OFF_RAW + C::RAW + 32 * wq * C::RBV) + i;
+                        *at = make_uint4(nan_or_0(at->x), nan_or_0(at->y), nan_or_0(at->z), nan_or_0(at->w));
+                    }
+                __syncwarp();
+            }
             convert(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
             if (lane == 0) {
                 mbar_arrive(BAR(C::B_VF + st));
@@ -359,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     scales_of(j + 1, id1, ks1, vs1);
                     if (t >= kMetas && !(ok = wait(C::B_ME + sl, t / kMetas - 1, 0xE6))) break;
                     TileMeta* m = metas + sl;
+                    const uint32_t zero = __ballot_sync(0xffffffffu, !(vs > 0.f));
                     float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : -INFINITY;
                     lvmax = fmaxf(lvmax, lv);
 #pragma unroll
@@ -373,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         m->key0 = (first + j) * BN;
                         m->len = rq.len;
                         m->end = 0;
+                        m->zero = zero;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_MF + sl));

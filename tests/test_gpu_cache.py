@@ -781,3 +781,17 @@ def test_append_then_attend_what_is_not_finite(bpa, kernel, value):
     last = int(c["cu"][1]) - 1
     assert torch.isnan(o[last, heads]).all() and torch.isfinite(l[heads, last]).all()
     assert torch.isfinite(o[last, :Hq // Hkv]).all() and torch.isfinite(o[last + 1:]).all()
+
+
+@DTYPES
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_scale_of_zero_stands_for_zeros(bpa, kernel, dtype):
+    # pages whose codes are not zero although their scale is: whatever they hold counts as 0
+    c = make_step(np.random.default_rng(33), *KERNELS[kernel])
+    for n, pages in (("vs", (0, 2)), ("ks", (1, 2))):
+        for j in pages:
+            c[n][c["table"][0, min(j, (c["kv"][0] - 1) // c["kc"].shape[2])]] = 0
+    run_and_check(bpa, c, dtype)
+    c["vs"][:] = 0
+    o, m, l = run_and_check(bpa, c, dtype)
+    assert not o.any()
