@@ -114,14 +114,16 @@ struct CacheBox {
 bool cache_attn_mma_supported(const CacheAttnArgs& a);
 size_t cache_attn_mma_workspace(const CacheAttnArgs& a);
 CacheBox cache_attn_mma_box(const CacheAttnArgs& a);
-// few_only: requests of more than kFewRows rows are left to launch_cache_attn_tc, which has run before
-// on the same status word.
-cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, bool few_only, cudaStream_t s);
+// far: null, or the marks of launch_cache_attn_tc, which has run before on the same status word: requests
+// of more than kFewRows rows are then computed only where they are marked.
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, const uint32_t* far, cudaStream_t s);
+uint32_t* cache_attn_far(uint8_t* ws);      // the marks' place, [R]
 
 // Tensor-core kernel for requests of more than kFewRows rows (bf16, head dims in steps of 16 up to 128,
-// pages in steps of 16 tokens); the others are left alone.  counter: zero before the launch.
+// pages in steps of 16 tokens); the others are left alone.  counter, far [R]: zero before the launch; it marks
+// the requests whose v scales lie too far apart for it, whatever it has written for them.
 bool cache_attn_tc_takes(const CacheAttnArgs& a);       // supported, and there may be enough such requests
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a);      // plain (not swizzled) boxes
-cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, cudaStream_t s);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, cudaStream_t s);
 
 }  // namespace bpa

@@ -269,19 +269,21 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
         CUtensorMap maps[2];
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&
             make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows, true)) {
-            const bool many = cache_attn_tc_takes(a);   // requests of many rows first
-            if (many) {
-                st = cuda_status(cudaMemsetAsync(workspace, 0, kHeader, s), "clearing the status word");
+            uint32_t* far = nullptr;
+            if (cache_attn_tc_takes(a)) {               // requests of many rows first
+                far = cache_attn_far(static_cast<uint8_t*>(workspace));
+                const size_t used = reinterpret_cast<uint8_t*>(far + a.R) - static_cast<uint8_t*>(workspace);
+                st = cuda_status(cudaMemsetAsync(workspace, 0, used, s), "clearing the status word and the marks");
                 if (st != BPA_OK) return st;
                 const CacheBox plain = cache_attn_tc_box(a);
                 CUtensorMap raw[2];
                 if (!make_cache_map(&raw[0], a.kc, a, a.d, a.kcs, plain.cols_k, plain.rows, false) ||
                     !make_cache_map(&raw[1], a.vc, a, a.dv, a.vcs, plain.cols_v, plain.rows, false))
                     return fail(BPA_ERR_CUDA, "cache attention: no tensor map");
-                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, s), "cache attention launch");
+                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, far, s), "cache attention launch");
                 if (st != BPA_OK) return st;
             }
-            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), many, s),
+            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), far, s),
                                "cache attention launch");
         }
     }

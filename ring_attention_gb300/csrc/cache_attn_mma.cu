@@ -62,7 +62,7 @@ static_assert(sizeof(Rec) == 32, "record");
 struct Work {
     CacheAttnArgs a;
     int rows_per, ctas;               // rows of an item, CTAs
-    int few_only;                     // requests of more than kFewRows rows are another kernel's
+    const uint32_t* far;              // [R] or null (BESIDE): of the requests of more than kFewRows rows only those marked here
     int vec_q, vec_o;                 // four elements of q, two of o at a time
     Rec* recs;                        // [ctas]
     float2* ml;                       // [2 ctas][rows_per] (m in log2 units, l)
@@ -155,10 +155,12 @@ BPA_DEV void ld_q4(const __nv_bfloat16* p, float (&v)[4]) {
     v[3] = __uint_as_float(x.y & 0xffff0000u);
 }
 
-// Request r, without rows where another kernel takes it.
+// Request r; BESIDE: without rows where the kernel for many rows has taken it.  An instance of its own, since
+// the check in every instance cost generation 1 to 2 % (64 requests 98.6 us with it, 97.0 without).
+template <bool BESIDE>
 BPA_DEV Req own_request(const Work& w, int r) {
     Req q = request_of(w.a, r);
-    if (w.few_only && q.n * w.a.G > kFewRows) q.n = 0;
+    if (BESIDE && q.n * w.a.G > kFewRows && !w.far[r]) q.n = 0;
     return q;
 }
 
@@ -196,7 +198,7 @@ BPA_DEV long long share(long long total, int c, int parts) {
     return x >> 32 ? x / parts : static_cast<uint32_t>(x) / static_cast<uint32_t>(parts);
 }
 
-template <int DP, int DVP, int NT, bool SPLIT>
+template <int DP, int DVP, int NT, bool SPLIT, bool BESIDE>
 __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     k_cache_attn_mma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Work w) {
     using C = Cfg<DP, DVP, NT, SPLIT>;
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     const int per = (a.R + kThreads - 1) / kThreads, r0 = min(a.R, static_cast<int>(threadIdx.x) * per),
               r1 = min(a.R, r0 + per);
     long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += cost_of_request<NT>(a, own_request(w, r), rows_per);
+    for (int r = r0; r < r1; ++r) mine += cost_of_request<NT>(a, own_request<BESIDE>(w, r), rows_per);
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
     if (begin < end && begin >= before && begin < before + mine) {
         long long at = before;
         for (int r = r0; r < r1; ++r) {
-            const long long n = cost_of_request<NT>(a, own_request(w, r), rows_per);
+            const long long n = cost_of_request<NT>(a, own_request<BESIDE>(w, r), rows_per);
             if (begin < at + n) {
                 s_r = r;
                 s_off = begin - at;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
         Tiles tl = {};
         Rec out = {};
         if (r >= 0) {
-            rq = own_request(w, r);
+            rq = own_request<BESIDE>(w, r);
             if (rq.bad && lane == 0) report(status, ST_CHECK, 0xCD1);
             groups = (rq.n * a.G + rows_per - 1) / rows_per;
             const long long per_head = cost_of_request<NT>(a, rq, rows_per) / a.Hkv;
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<DP, DVP, NT, SPLIT>::OCC))
                             hk = 0;
                             do {
                                 if (++r >= a.R) break;      // only if the lengths changed during the call
-                                rq = own_request(w, r);
+                                rq = own_request<BESIDE>(w, r);
                                 if (rq.bad && rq.n && lane == 0) report(status, ST_CHECK, 0xCD1);
                             } while (rq.n == 0);
                             if (r >= a.R) {
@@ -884,7 +886,7 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
             }
         __syncthreads();
         if (threadIdx.x == 0) {
-            if (!w.few_only) {
+            if (!w.far) {
                 out_status[0] = s_flags;
                 out_status[1] = s_where;
             } else if (s_flags) {                  // beside what the other kernel has reported
@@ -988,10 +990,11 @@ int sm_count() {
 }
 
 constexpr int kMaxSms = 160;          // the workspace is sized for this many
+constexpr size_t kFarAt = 256;        // the marks lie behind the header
 
 struct Plan {
     int DP, DVP, NT, RT, rows_per, occ, max_ctas;
-    size_t recs, ml, part, total;     // offsets behind the header
+    size_t recs, ml, part, total;     // offsets in the workspace, behind the header and the marks
 };
 bool plan_of(const CacheAttnArgs& a, Plan& p) {
     if (a.d % 16 || a.dv % 16 || a.d > 256 || a.dv > 256) return false;
@@ -1011,17 +1014,17 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     p.max_ctas = kMaxSms * p.occ;
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     const size_t slots = 2 * static_cast<size_t>(p.max_ctas) * p.rows_per;
-    p.recs = 256;
+    p.recs = kFarAt + up(sizeof(uint32_t) * static_cast<size_t>(a.R));
     p.ml = p.recs + up(sizeof(Rec) * p.max_ctas);
     p.part = p.ml + up(slots * sizeof(float2));
     p.total = p.part + up(slots * p.DVP * sizeof(float));
     return true;
 }
 
-template <int DP, int DVP, int NT, bool SPLIT>
+template <int DP, int DVP, int NT, bool SPLIT, bool BESIDE = false>
 cudaError_t launch(const Work& w, const CUtensorMap* maps, int rpb, cudaStream_t s) {
     using C = Cfg<DP, DVP, NT, SPLIT>;
-    auto kernel = k_cache_attn_mma<DP, DVP, NT, SPLIT>;
+    auto kernel = k_cache_attn_mma<DP, DVP, NT, SPLIT, BESIDE>;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1044,6 +1047,8 @@ bool cache_attn_mma_supported(const CacheAttnArgs& a) {
     return plan_of(a, p);
 }
 
+uint32_t* cache_attn_far(uint8_t* ws) { return reinterpret_cast<uint32_t*>(ws + kFarAt); }
+
 size_t cache_attn_mma_workspace(const CacheAttnArgs& a) {
     Plan p;
     return plan_of(a, p) ? p.total : 256;
@@ -1055,13 +1060,13 @@ CacheBox cache_attn_mma_box(const CacheAttnArgs& a) {
     return {p.DP < 128 ? p.DP : 128, p.DVP < 128 ? p.DVP : 128, a.P < kTile ? a.P : kTile};
 }
 
-cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, bool few_only, cudaStream_t s) {
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, const uint32_t* far, cudaStream_t s) {
     Plan p;
     if (!plan_of(a, p)) return cudaErrorInvalidValue;
     Work w;
     w.a = a;
     w.rows_per = p.rows_per;
-    w.few_only = few_only;
+    w.far = far;
     // no more CTAs than the longest table rows have tiles
     const int64_t groups = (static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G + p.rows_per - 1) / p.rows_per;
     const int64_t most = ((static_cast<int64_t>(a.max_pages) * a.P + kTile - 1) / kTile + kExtra) * a.Hkv * a.R * groups;
@@ -1079,6 +1084,10 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     const int64_t pieces = w.ctas / (static_cast<int64_t>(a.R) * a.Hkv);
     const int rpb = pieces <= 4 ? 8 : pieces <= 16 ? 4 : pieces <= 64 ? 2 : 1;
     const bool f32 = a.dtype == BPA_FP32;
+    if (far) {                         // more than kFewRows rows (so NT is 2), bf16, head dims up to 128
+        if (p.DP == 64) return launch<64, 64, 2, false, true>(w, maps, rpb, s);
+        return p.DVP == 64 ? launch<128, 64, 2, false, true>(w, maps, rpb, s) : launch<128, 128, 2, false, true>(w, maps, rpb, s);
+    }
 #define BPA_CACHE_CASE(DP_, DVP_) \
     if (p.DP == DP_ && p.DVP == DVP_) \
         return p.NT == 1 ? f32 ? launch<DP_, DVP_, 1, true>(w, maps, rpb, s) : launch<DP_, DVP_, 1, false>(w, maps, rpb, s) \

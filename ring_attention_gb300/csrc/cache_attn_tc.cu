@@ -10,9 +10,12 @@
 //   W = exp2(u - M + 7) in fp16, M the row's running maximum of u (moved only when it grows by
 //       more than 8, so W <= 2^15);  O += W V;  L += sum W / (v scale);  o = O / L
 // One exponential serves the numerator and the denominator, with 1 / (v scale) relative to the first
-// scale lv0 that the item meets (a page below 2^-90 of that one counts as 2^-90 of it).  Pages of zeros
-// (scale 0) have no scale of their own: they count 2^-20 below the largest met so far, so their keys stay
-// in L (far below, W would leave float32's range) and do not push the others' W out of fp16's.
+// scale lv0 that the item meets.  That holds while a request's scales lie within a factor 2^40 of it: W
+// e = 2^(x + lv0 - M + 7) is then at most 2^75 (2^105 summed over 2^30 keys) and a key of the largest x has W
+// >= 2^-93.  A request with a scale outside is marked in `far`, and the kernel for few rows, which has an
+// exponential for each of the two sums and takes any scales, computes it again.  Pages of zeros (scale 0)
+// have no scale of their own: they count 2^-20 below the largest met so far, so their keys stay in L (far
+// below, W would leave float32's range) and do not push the others' W out of fp16's.
 //
 // Bounded by the softmax's instructions and the exponentials beside the products (compute, not
 // bytes): about three instructions and one exponential a score.  Two threads share a row (64 columns
@@ -48,8 +51,8 @@ constexpr int kRows = 256;            // rows of an item
 constexpr int kMetas = 4;             // records of key tiles in flight
 constexpr int kMma = 16, kAux = 17, kConv = 20;   // first warps of the roles
 constexpr float kTau = 8.f, kOff = 7.f;
-constexpr float kFar = 90.f;          // log2: scales further below the item's first count as this far below
-constexpr float kZeros = 20.f, kAllZeros = -80.f;   // log2 scale of a page of zeros: below the largest so far; before any
+constexpr float kFar = 40.f;          // log2: a scale further from the item's first makes the request another kernel's
+constexpr float kZeros = 20.f, kAllZeros = -kFar - kZeros;   // log2 scale of a page of zeros: below the largest so far; before any
 
 struct TileMeta {
     int key0, len, end;
@@ -180,7 +183,7 @@ BPA_DEV float weights(uint32_t tS, const TileMeta* mt, int c0, float f_row, floa
 
 template <int D, int DV>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_constant__ CUtensorMap tmK,
-    const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a, uint32_t* counter, int vec_q, int vec_o) {
+    const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a, uint32_t* counter, uint32_t* far, int vec_q, int vec_o) {
     using C = Cfg<D, DV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -374,7 +377,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     if (t >= kMetas && !(ok = wait(C::B_ME + sl, t / kMetas - 1, 0xE6))) break;
                     TileMeta* m = metas + sl;
                     const uint32_t zero = __ballot_sync(0xffffffffu, !(vs > 0.f));
-                    float lv = vs > 0.f ? fmaxf(__log2f(vs), lv0 - kFar) : -INFINITY;
+                    float lv = vs > 0.f ? __log2f(vs) : -INFINITY;
+                    if (vs > 0.f && !(fabsf(lv - lv0) <= kFar)) {
+                        far[r] = 1;
+                        lv = lv0;
+                    }
                     lvmax = fmaxf(lvmax, lv);
 #pragma unroll
                     for (int o = 1; o < 8; o <<= 1) lvmax = fmaxf(lvmax, __shfl_xor_sync(0xffffffffu, lvmax, o));
@@ -643,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 part = xm == -INFINITY || old == 0.f ? (old != old ? old : 0.f) : old * ex2(xm - nm) / l;   // what the keys have of the row
                 mm = nm;
             }
-            const float inv = (L == 0.f || M == -INFINITY ? (L != L ? L : 0.f) : ex2(it.lv0) / L) * part;
+            // two factors: 2^lv0 / L alone may be below float32's normal numbers
+            const float inv = (L == 0.f || M == -INFINITY ? (L != L ? L : 0.f) : 1.f / L) * part, s0 = ex2(it.lv0);
             const int64_t out_row = it.row0 + tok;
             if (there && a.m && half == 0) {
                 a.m[static_cast<int64_t>(head) * a.T + out_row] = mm == -INFINITY ? mm : mm * kLn2;
@@ -665,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     if (cc * 32 + 8 * v >= a.dv) continue;
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16(__uint_as_float(r[8 * v + 2 * e]) * inv, __uint_as_float(r[8 * v + 2 * e + 1]) * inv);
+                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16(__uint_as_float(r[8 * v + 2 * e]) * inv * s0, __uint_as_float(r[8 * v + 2 * e + 1]) * inv * s0);
                     if (vec_o) {
                         *reinterpret_cast<uint4*>(o + cc * 32 + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
@@ -694,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
 }
 
 template <int D, int DV>
-cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, cudaStream_t s) {
+cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, cudaStream_t s) {
     using C = Cfg<D, DV>;
     static std::atomic<int> sms[64];
     int dev = 0;
@@ -712,7 +720,7 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* co
     // at most the packed rows' groups and a ragged one per request
     const int64_t most = (static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
     k_cache_attn_tc<D, DV><<<static_cast<unsigned>(std::min<int64_t>(n, most)), kThreads, C::SMEM, s>>>(maps[0], maps[1], a, counter,
-                                                                                                       vec_q, vec_o);
+                                                                                                       far, vec_q, vec_o);
     return cudaGetLastError();
 }
 
@@ -732,9 +740,9 @@ bool cache_attn_tc_takes(const CacheAttnArgs& a) {
 
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a) { return {a.d <= 64 ? 64 : 128, a.dv <= 64 ? 64 : 128, 16}; }
 
-cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, cudaStream_t s) {
-    if (a.d <= 64) return launch<64, 64>(a, maps, counter, s);
-    return a.dv <= 64 ? launch<128, 64>(a, maps, counter, s) : launch<128, 128>(a, maps, counter, s);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, cudaStream_t s) {
+    if (a.d <= 64) return launch<64, 64>(a, maps, counter, far, s);
+    return a.dv <= 64 ? launch<128, 64>(a, maps, counter, far, s) : launch<128, 128>(a, maps, counter, far, s);
 }
 
 }  // namespace bpa

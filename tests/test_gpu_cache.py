@@ -795,3 +795,21 @@ def test_attention_scale_of_zero_stands_for_zeros(bpa, kernel, dtype):
     c["vs"][:] = 0
     o, m, l = run_and_check(bpa, c, dtype)
     assert not o.any()
+
+
+@DTYPES
+@pytest.mark.parametrize("first,later", [(-100, 30), (-100, 110), (110, -100), (0, 60), (60, 0), (0, 40), (40, 0), (None, None), ("0", -90), ("0", 39)], ids=str)
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_value_scales_of_the_whole_range(bpa, kernel, first, later, dtype):
+    # every scale that append writes, from 2^-100 to about 2^119, in any order within a request
+    rng = np.random.default_rng(34)
+    c = make_step(rng, *KERNELS[kernel])
+    c["vs"][:] = np.exp2(rng.integers(-100, 110, c["vs"].shape) if first is None else np.full(c["vs"].shape, later)).astype(np.float32)
+    for r in range(2):
+        if first == "0":
+            c["vs"][c["table"][r, 0]] = 0
+        elif first is not None:
+            c["vs"][c["table"][r, 0]] = 2.0 ** first
+    run_and_check(bpa, c, dtype)
+    run_and_check(bpa, c, dtype, window=(20, -1))
+    run_and_check(bpa, c, dtype, sink=np.linspace(-2, 3, c["q"].shape[1]))
