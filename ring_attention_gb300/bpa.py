@@ -343,7 +343,9 @@ def bpa_debug_wait_timeout(workspace_buf: torch.Tensor, limit_ns: int, stream=No
 # ---- paged 8-bit key / value cache --------------------------------------------------------------
 # A generation step is a few microseconds of device time, so these calls marshal leanly: descriptors
 # are packed in one go (the layouts of bpa_cache_desc and bpa_cache_batch) and each tensor is looked
-# at once.
+# at once.  stream (of any of them): a torch stream of the tensors' device instead of torch's current one;
+# as for torch's own operators, the caller orders it behind the writers of the tensors passed in and in
+# front of the readers of what comes back.
 _CACHE_PACK = struct.Struct("@I7iPP6qPP").pack
 _BATCH_PACK = struct.Struct("@I5iP4qPPPf3iP").pack
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
@@ -362,28 +364,34 @@ def _i32_buffer(t, name, shape, dev):
 
 
 def _enter(dev, stream):
-    """(guard, stream pointer, other) for device number dev: the device to leave again (None: it is
-    current), the stream of the call (``stream``, or torch's current one) and, where that is not
-    torch's current one, itself."""
+    """(guard, stream pointer, other) for device number dev: what to leave again (None: nothing), the
+    stream of the call (``stream``, or torch's current one) and whether that is not torch's current one.
+    It is then made current for the call: torch's allocator orders memory by the stream that it was
+    asked for on, so what the call makes must come from the stream whose kernels use it."""
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream must be one of the tensors' device {dev}, got one of {stream.device}")
+    ptr = torch._C._cuda_getCurrentRawStream(dev)
+    other = stream is not None and stream.cuda_stream != ptr
     guard = None
-    if dev != _current_device():
+    if other:
+        guard, ptr = torch.cuda.stream(stream), stream.cuda_stream
+    elif dev != _current_device():
         guard = torch.cuda.device(dev)
+    if guard is not None:
         guard.__enter__()
-    here = torch._C._cuda_getCurrentRawStream(dev)
-    if stream is None:
-        return guard, here, None
-    return guard, stream.cuda_stream, stream if stream.cuda_stream != here else None
+    return guard, ptr, other
 
 
-def _leave(guard, other, made):
-    """Undoes _enter; what the call made for itself on another stream than torch's is marked for it."""
+def _leave(guard, other, dev, outs):
+    """Undoes _enter; outputs made on another stream than torch's current one are marked for that one,
+    where the caller may use and drop them."""
     if guard is not None:
         guard.__exit__(None, None, None)
-    if other is not None:
-        for t in made:
-            t.record_stream(other)
+    if other:
+        for t in outs:
+            t.record_stream(torch.cuda.current_stream(dev))
 
 
 def _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype):
@@ -460,11 +468,10 @@ def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, pa
                 made.append(outs[i])
         if workspace_buf is None:
             workspace_buf = _empty(256, dtype=_U8, device=where)
-            made.append(workspace_buf)
         st = lib().bpa_cache_plan(R, T, int(page_size), num_pages, max_pages, *ins, *[t.data_ptr() for t in outs],
                                   workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
-        _leave(guard, other, made)
+        _leave(guard, other, dev, made)
     if st:
         _raise_if(st, "bpa_cache_plan")
     return tuple(outs)
@@ -481,15 +488,13 @@ def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_
     vs = _rows_strides(v, "v", (T, Hkv, dv), dtype, dev)
     slots = _i32_buffer(slot_map, "slot_map", (T,), dev)
     guard, ptr, other = _enter(dev, stream)
-    made = ()
     try:
         if workspace_buf is None:
             workspace_buf = _empty(256, dtype=_U8, device=k.device)
-            made = (workspace_buf,)
         st = lib().bpa_cache_append(cache, k.data_ptr(), v.data_ptr(), _TWO_PACK(ks[0], ks[1]), _TWO_PACK(vs[0], vs[1]),
                                     slots, T, int(max_new), workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
-        _leave(guard, other, made)
+        _leave(guard, other, dev, ())
     if st:
         _raise_if(st, "bpa_cache_append")
 
@@ -557,11 +562,10 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
             if need == 0:
                 _raise_if(BPA_ERR_INVALID_ARG, "bpa_cache_attn_workspace_size")
             workspace_buf = _empty(need, dtype=_U8, device=where)
-            made.append(workspace_buf)
         st = L.bpa_cache_attn(cache, batch, o.data_ptr(), m.data_ptr(), l.data_ptr(), workspace_buf.data_ptr(),
                               workspace_buf.numel(), ptr)
     finally:
-        _leave(guard, other, made)
+        _leave(guard, other, dev, made)
     if st:
         _raise_if(st, "bpa_cache_attn")
     return o, m, l

@@ -242,3 +242,108 @@ def test_oracle_attention_closed_forms():
     np.testing.assert_allclose(o[0, 0], val[1:5].mean(0))
     np.testing.assert_allclose(o[1, 0], val[2:6].mean(0))
     assert l[0].tolist() == [4, 4, 0] and m[0, 2] == -np.inf and not o[2].any()
+
+
+# ---- calls on another stream than torch's current one --------------------------------------------------
+class _Fake:
+    """A CPU tensor that says it is on GPU 0 and remembers the stream that was current when it was made."""
+
+    def __init__(self, t, made_on=None):
+        self.t, self.made_on, self.recorded = t, made_on, []
+
+    def get_device(self):
+        return 0
+
+    def record_stream(self, s):
+        self.recorded.append(s.cuda_stream)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class _Stream:
+    def __init__(self, ptr, index=0):
+        self.cuda_stream, self.device = ptr, torch.device("cuda", index)
+
+
+@pytest.fixture
+def streams(bpa, monkeypatch):
+    """The binding over a library and an allocator that note streams: (current stream, made tensors, launches)."""
+    now, made, launched = [_Stream(0x10)], [], []
+
+    class Enter:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            now.append(self.s)
+
+        def __exit__(self, *_):
+            now.pop()
+
+    def empty(shape, dtype=None, device=None):
+        made.append(_Fake(torch.empty(shape, dtype=dtype), now[-1].cuda_stream))
+        return made[-1]
+
+    class Lib:
+        bpa_cache_attn_workspace_size = staticmethod(lambda *a: 512)
+
+        def __getattr__(self, name):
+            return lambda *a: launched.append((name, a[-1])) or 0
+
+    monkeypatch.setattr(bpa, "_empty", empty)
+    monkeypatch.setattr(bpa, "_current_device", lambda: 0)
+    monkeypatch.setattr(bpa, "lib", Lib)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: now[-1].cuda_stream, raising=False)
+    monkeypatch.setattr(torch.cuda, "stream", Enter)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: now[-1])
+    return now, made, launched
+
+
+def _cache_calls(bpa):
+    f = {n: _Fake(x) for n, x in _tensors().items()}
+    i32 = dict(dtype=torch.int32)
+    rows = dict(k=_Fake(torch.zeros(5, 2, 64, dtype=torch.bfloat16)), v=_Fake(torch.zeros(5, 2, 32, dtype=torch.bfloat16)),
+                slot_map=_Fake(torch.zeros(5, **i32)), **{n: f[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale")})
+    plan = dict(ctx_lens=_Fake(torch.zeros(3, **i32)), new_lens=_Fake(torch.zeros(3, **i32)),
+                page_table=_Fake(torch.zeros(3, 4, **i32)), free_pages=_Fake(torch.zeros(9, **i32)),
+                free_count=_Fake(torch.zeros(1, **i32)), page_size=16, T=8)
+    return {"plan": lambda **kw: bpa.bpa_cache_plan(**plan, **kw), "append": lambda **kw: bpa.bpa_cache_append(**rows, **kw),
+            "attn": lambda **kw: bpa.bpa_cache_attn(**f, **kw)}
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "attn"])
+def test_buffers_are_made_on_the_stream_that_uses_them(bpa, streams, name):
+    # memory that the current stream may still be writing must not be handed to another stream's kernels
+    now, made, launched = streams
+    call = _cache_calls(bpa)[name]
+    returned = call(stream=_Stream(0x20)) or ()
+    assert [p for _, p in launched] == [0x20] and len(now) == 1
+    assert made and all(t.made_on == 0x20 for t in made)
+    assert all(t.recorded == [0x10] for t in returned)      # they may be used, and dropped, on the current one
+    made.clear()
+    returned = call() or ()
+    assert launched[-1][1] == 0x10 and all(t.made_on == 0x10 for t in made)
+    assert not any(t.recorded for t in made)
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "attn"])
+def test_streams_of_another_device_are_refused(bpa, streams, name):
+    now, made, launched = streams
+    for ptr in (0x10, 0x20):
+        with pytest.raises(ValueError, match="stream"):
+            _cache_calls(bpa)[name](stream=_Stream(ptr, 1))
+    assert not launched and not made and len(now) == 1
+
+
+def test_a_failed_call_leaves_the_other_stream(bpa, streams, monkeypatch):
+    now, made, launched = streams
+
+    def fails(*a, **kw):
+        raise RuntimeError("out of memory")
+
+    monkeypatch.setattr(bpa, "_empty", fails)
+    for call in _cache_calls(bpa).values():
+        with pytest.raises(RuntimeError):
+            call(stream=_Stream(0x20))
+    assert len(now) == 1 and not launched

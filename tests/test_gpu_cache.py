@@ -813,3 +813,36 @@ def test_attention_value_scales_of_the_whole_range(bpa, kernel, first, later, dt
     run_and_check(bpa, c, dtype)
     run_and_check(bpa, c, dtype, window=(20, -1))
     run_and_check(bpa, c, dtype, sink=np.linspace(-2, 3, c["q"].shape[1]))
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "attn"])
+def test_buffers_of_another_stream_are_not_the_current_ones(bpa, name):
+    """Tensors dropped while the current stream has still to write them: a call on another stream, which is free
+    at once, must not get their memory for its outputs and workspace."""
+    t = on_gpu(make_step(np.random.default_rng(35), [900, 300], [1, 2], 8, 2, 128, 128, 64), torch.bfloat16)
+    p = make_plan(np.random.default_rng(36), [3] * 300, [2] * 300, 16, 400)
+    plan = (i32(p["ctx"]), i32(p["new"]), i32(p["table"]), i32(p["free"]), i32([p["count"]]))
+    k, v, slots = torch.randn(3, 2, 128, device="cuda").bfloat16(), torch.randn(3, 2, 128, device="cuda").bfloat16(), i32([0, 1, 64])
+
+    def call(stream=None):                        # the same again gives the same
+        if name == "plan":
+            return bpa.bpa_cache_plan(*plan, page_size=16, T=p["T"], stream=stream)
+        if name == "append":
+            bpa.bpa_cache_append(k, v, slots, *t[1:5], max_new=2, stream=stream)
+            return t[1:5]
+        return bpa.bpa_cache_attn(*t, max_q=2, stream=stream)
+
+    want = [x.clone() for x in call()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    sizes = [256, 512, 1200, 2400, 4096, 6144] + [1 << n for n in range(13, 23)]
+    junk = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(6)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                 # about ten milliseconds of the current stream
+    for x in junk:
+        x.fill_(0xFF)
+    del junk, x
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
