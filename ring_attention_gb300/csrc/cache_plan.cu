@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_plan(const PlanArgs a) {
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s) {
     const size_t smem = sizeof(int) * (3 * static_cast<size_t>(a.R) + 1);
-    if (smem > 48 * 1024) {
+    // a kernel has 48 KB without asking, its static part (the scans, below 1 KB) included
+    if (smem > 47 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k_cache_plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(sizeof(int) * (3 * kPlanMaxR + 1)));
         if (e != cudaSuccess) return e;

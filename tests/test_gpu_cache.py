@@ -14,6 +14,9 @@ with A = sum p |v| / l (the same attention over |v|) and Z = the largest sum_c |
   * the output is rounded once: 2^-8 |o| in bf16, 2^-24 |o| in float32.
 """
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -846,3 +849,19 @@ def test_buffers_of_another_stream_are_not_the_current_ones(bpa, name):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_plan_of_any_number_of_requests_in_a_fresh_process():
+    # about 4,050 to 4,095 requests need more shared memory than a kernel has without asking for it, once its
+    # static part is counted; an earlier plan of more requests in the process would have asked already
+    body = """
+import numpy as np, torch
+from ring_attention_gb300 import bpa
+from tests.test_gpu_cache import check_plan, make_plan
+for R in (3900, 4049, 4050, 4051, 4095, 4096, 8192):
+    rng = np.random.default_rng(R)
+    check_plan(bpa, make_plan(rng, rng.integers(0, 40, R), rng.integers(0, 3, R), 16, 5))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", body], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
