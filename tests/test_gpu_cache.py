@@ -865,3 +865,23 @@ for R in (3900, 4049, 4050, 4051, 4095, 4096, 8192):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", body], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+WIDE = [     # head dims of 129 to 256 with more than 8 rows of a kv head, in one, two and four row tiles
+    ([700], [1], 32, 2, 256, 256, 64), ([300, 33], [3, 5], 8, 2, 256, 256, 16), ([90, 0, 400], [20, 1, 7], 8, 2, 192, 128, 64),
+    ([130], [1], 12, 1, 256, 64, 32), ([20, 250], [33, 2], 12, 4, 64, 192, 128), ([40, 10, 900], [9, 4, 2], 4, 2, 208, 240, 16),
+    ([600, 31, 0], [1, 2, 1], 48, 2, 192, 128, 32), ([100, 5], [70, 131], 16, 4, 256, 256, 64), ([100, 5], [70, 131], 16, 4, 192, 112, 64),
+]
+
+
+@DTYPES
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: f"H{c[2]}_{c[3]}_d{c[4]}_{c[5]}_P{c[6]}_q{max(c[1])}")
+def test_attention_many_rows_of_wide_heads(bpa, case, dtype):
+    rng = np.random.default_rng(sum(case[0]) + case[5])
+    c = make_step(rng, *case, pad=2)
+    run_and_check(bpa, c, dtype)
+    run_and_check(bpa, c, dtype, window=(70, -1), sink=rng.standard_normal(case[2]))
+    c["kv"] = c["kv"].copy()
+    c["kv"][-1] = 0
+    c["vs"][:] = np.exp2(rng.integers(-30, 30, c["vs"].shape) - 7.0).astype(np.float32)
+    run_and_check(bpa, c, dtype, causal=False)
