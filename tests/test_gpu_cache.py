@@ -885,3 +885,43 @@ def test_attention_many_rows_of_wide_heads(bpa, case, dtype):
     c["kv"][-1] = 0
     c["vs"][:] = np.exp2(rng.integers(-30, 30, c["vs"].shape) - 7.0).astype(np.float32)
     run_and_check(bpa, c, dtype, causal=False)
+
+
+@pytest.mark.parametrize("kernel", ["few_rows", "many_rows", "any_shape"])
+@DTYPES
+def test_attention_weights_keep_eleven_bits(bpa, kernel, dtype):
+    """Two keys of scores delta and 0 with values 1 and -1: o = tanh(delta / 2), small beside A = 1, so the rounding of
+    the weights shows.  Bound: the one of the module's text with n = 2, the weights' own part half a step of fp16,
+    2^-11 (float32: two halves, 2^-21), and a largest weight of 2^7 at least: n 2^-32 448 H, H <= 1.
+    Weights of bf16 would break it, which is checked first."""
+    R, rows, Hq, Hkv, d, dv, P = {"few_rows": (20, 1, 64, 8, 64, 64, 16), "many_rows": (2, 40, 32, 16, 64, 64, 16),
+                                  "any_shape": (4, 3, 32, 8, 72, 40, 8)}[kernel]
+    T = R * rows
+    q = np.zeros((T, Hq, d))
+    q[..., 0] = np.linspace(0, 0.02, T * Hq).reshape(T, Hq)
+    c = dict(q=q, kc=np.zeros((1, Hkv, P, d), np.uint8), vc=np.zeros((1, Hkv, P, dv), np.uint8),
+             ks=np.ones((1, Hkv), np.float32), vs=np.ones((1, Hkv), np.float32), table=np.zeros((R, 1), int),
+             kv=np.full(R, 2), cu=np.arange(R + 1) * rows, max_q=rows)
+    c["kc"][:, :, 0, 0], c["vc"][:, :, 0], c["vc"][:, :, 1] = 0x38, 0x38, 0xB8      # 1, 1 and -1
+    delta = as_dtype(q, dtype)[1][..., :1]
+    want = np.tanh(delta / 2)
+    half, weight = (2.0 ** -8, 2.0 ** -11) if dtype == torch.bfloat16 else (2.0 ** -24, 2.0 ** -21)
+    dz = (d + 4) * 2.0 ** -23 * 0.02 + 2.0 ** -21
+    bound = half * np.abs(want) + (2 * dz + weight + 2 * 2.0 ** -23 + 2 * 2.0 ** -32 * 448) * (1 + half)
+    low = torch.from_numpy(np.exp(-delta)).to(torch.bfloat16).double().numpy()
+    assert (np.abs((1 - low) / (1 + np.exp(-delta)) - want) > bound).any()
+    o, m, l = bpa.bpa_cache_attn(*on_gpu(c, dtype), max_q=rows, causal=False, scale=1.0)
+    torch.cuda.synchronize()
+    assert (np.abs(f64(o) - want) <= bound).all()
+
+
+@DTYPES
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_repeats_itself(bpa, kernel, dtype):
+    ctx, new, *rest = KERNELS[kernel]
+    c = make_step(np.random.default_rng(37), [900 + 13 * i for i in range(6)] + ctx, [1, 2, 1, 3, 1, 1] + new, *rest)
+    t = on_gpu(c, dtype)
+    first = bpa.bpa_cache_attn(*t, max_q=c["max_q"])
+    for _ in range(20):
+        for a, b in zip(bpa.bpa_cache_attn(*t, max_q=c["max_q"]), first):
+            assert torch.equal(a, b)
