@@ -293,7 +293,7 @@ bpa_status bpa_select_blocks_noalloc(const void* q, const void* k, int32_t dtype
  *   rows from cu_q[R] on are neither read nor written.
  *
  * A fault that only the device can see (a page id outside [0, num_pages), a length past the
- * table, a slot outside the cache) is recorded as BPA_ERR_DEVICE_CHECK for bpa_check; the
+ * table, a slot outside the cache other than -1) is recorded as BPA_ERR_DEVICE_CHECK for bpa_check; the
  * kernels skip what they cannot address, and what they write for that request is unspecified.
  * The functions below are an addition of this library; the pages that the other entry points
  * follow have no counterpart.  BPA_VERSION counts the versions of bpa_attn_desc only. */

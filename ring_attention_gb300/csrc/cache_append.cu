@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
         if (threadIdx.x == 0) s_bad = 0;
         __syncthreads();
         for (int t = threadIdx.x; t < a.T; t += 128)
-            if (a.slots[t] >= cap) s_bad = 1;
+            if (static_cast<uint32_t>(a.slots[t]) + 1u > static_cast<uint32_t>(cap)) s_bad = 1;   // outside [-1, cap)
         __syncthreads();
         if (threadIdx.x < 2) a.status[threadIdx.x] = !s_bad ? 0u : threadIdx.x ? 0xCB0u : static_cast<uint32_t>(ST_CHECK);
         return;

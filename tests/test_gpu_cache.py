@@ -925,3 +925,16 @@ def test_attention_repeats_itself(bpa, kernel, dtype):
     for _ in range(20):
         for a, b in zip(bpa.bpa_cache_attn(*t, max_q=c["max_q"]), first):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bad", [-2, -17, -2 ** 31])
+def test_append_reports_slots_below_minus_one(bpa, bad):
+    rng = np.random.default_rng(38)
+    kc, ks = random_cache(rng, 4, 1, 16, 16)
+    x = torch.randn(3, 1, 16, device="cuda")
+    (gc, gs, *_), ws = run_append(bpa, x, x, [3, bad, -1], kc, kc, ks, ks)
+    with pytest.raises(bpa.BpaError):
+        bpa.bpa_check(ws)
+    wc, wsc = ora.append(f64(x), [3, -1, -1], kc, ks)
+    np.testing.assert_array_equal(gc, wc)
+    np.testing.assert_array_equal(gs, wsc)
