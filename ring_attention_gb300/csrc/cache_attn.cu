@@ -4,11 +4,12 @@
 // key for the scores (the row of q in shared memory), then a lane per channel for p V, with a running
 // (max, denominator, numerator) of the warp; the four are merged at the end.
 //
-// Takes what the other kernels do not: head dims that are no multiple of 16 or above 256, pages that
-// are no multiple of 16, strides or bases that TMA does not take.  Bounded by its instructions (every
-// q head reads and decodes the codes of its kv head again): 8 requests of 1,000 tokens with 8 heads over
-// 2 of 72 channels 94 us, of 512 channels 383 us; 64 requests of 8,192 tokens, 32 heads over 8 of 128
-// channels, pages of 50 tokens 8.6 ms where pages of 64 let the matrix instructions take 0.155 ms.
+// Takes what the other kernels do not: head dims that are no multiple of 16 or above 256, pages other
+// than 16, 32 or a multiple of 64 tokens, strides or bases that TMA does not take, more than 2^30 rows of
+// a kv head in all.  Bounded by its instructions (every q head reads and decodes the codes of its kv head
+// again): 8 requests of 1,000 tokens with 8 heads over 2 of 72 channels 94 us, of 512 channels 383 us; 64
+// requests of 8,192 tokens, 32 heads over 8 of 128 channels, pages of 50 tokens 8.6 ms where pages of 64
+// let the matrix instructions take 0.155 ms.
 #include <cuda_fp8.h>
 
 #include "cache.h"

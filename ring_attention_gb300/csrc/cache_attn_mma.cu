@@ -998,6 +998,7 @@ struct Plan {
 };
 bool plan_of(const CacheAttnArgs& a, Plan& p) {
     if (a.d % 16 || a.dv % 16 || a.d > 256 || a.dv > 256) return false;
+    if (static_cast<int64_t>(a.T) * a.G > int64_t{1} << 30) return false;   // a request's rows are numbered in 32 bits
     if (a.P % 16 || (a.P < kTile ? kTile % a.P : a.P % kTile)) return false;
     p.DP = a.d <= 64 ? 64 : a.d <= 128 ? 128 : 256;
     p.DVP = a.dv <= 64 ? 64 : a.dv <= 128 ? 128 : 256;
@@ -1069,9 +1070,9 @@ cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* map
     w.far = far;
     // no more CTAs than the longest table rows have tiles
     const int64_t groups = (static_cast<int64_t>(a.max_q > 0 ? a.max_q : 1) * a.G + p.rows_per - 1) / p.rows_per;
-    const int64_t most = ((static_cast<int64_t>(a.max_pages) * a.P + kTile - 1) / kTile + kExtra) * a.Hkv * a.R * groups;
+    const double most = ((static_cast<int64_t>(a.max_pages) * a.P + kTile - 1) / kTile + kExtra) * static_cast<double>(a.Hkv) * a.R * groups;
     const int64_t ctas = static_cast<int64_t>(std::min(sm_count(), kMaxSms)) * p.occ;
-    w.ctas = static_cast<int>(most < ctas ? most : ctas);
+    w.ctas = static_cast<int>(std::min(most, static_cast<double>(ctas)));
     w.recs = reinterpret_cast<Rec*>(ws + p.recs);
     w.ml = reinterpret_cast<float2*>(ws + p.ml);
     w.part = reinterpret_cast<float*>(ws + p.part);

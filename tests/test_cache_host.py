@@ -347,3 +347,17 @@ def test_a_failed_call_leaves_the_other_stream(bpa, streams, monkeypatch):
         with pytest.raises(RuntimeError):
             call(stream=_Stream(0x20))
     assert len(now) == 1 and not launched
+
+
+# ---- sizes past 32 bits --------------------------------------------------------------------------------
+def test_rows_of_a_kv_head_past_two_to_the_30(bpa):
+    """Kernels that number a request's rows (tokens times q heads of a kv head) in 32 bits are left to calls of at most
+    2^30; the kernel for any shape, which numbers tokens and heads apart, takes the rest: its workspace is
+    the header alone."""
+    L = bpa.lib()
+
+    def need(T, Hq, Hkv):
+        return L.bpa_cache_attn_workspace_size(ctypes.byref(_cache(bpa, Hkv=Hkv)), ctypes.byref(_batch(bpa, T=T, Hq=Hq)))
+
+    assert need(1 << 20, 1 << 10, 1) > 256 and need(1 << 27, 64, 8) > 256
+    assert need((1 << 20) + 1, 1 << 10, 1) == 256 and need(1 << 30, 2, 1) == 256 and need(1 << 16, 65535, 1) == 256
