@@ -363,6 +363,11 @@ def _i32_buffer(t, name, shape, dev):
     return t.data_ptr()
 
 
+def _check_workspace(t, dev):
+    if t is not None and (t.dtype is not _U8 or not t.is_contiguous() or t.get_device() != dev):
+        raise ValueError("workspace_buf must be a contiguous uint8 tensor on the device of the other tensors")
+
+
 def _enter(dev, stream):
     """(guard, stream pointer, other) for device number dev: what to leave again (None: nothing), the
     stream of the call (``stream``, or torch's current one) and whether that is not torch's current one.
@@ -458,6 +463,7 @@ def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, pa
     for t, name, shape in zip(outs, ("kv_lens", "cu_q", "slot_map", "positions", "ctx_lens_out", "free_count_out"), shapes):
         if t is not None:
             _i32_buffer(t, name, shape, dev)
+    _check_workspace(workspace_buf, dev)
     guard, ptr, other = _enter(dev, stream)
     made = []
     try:
@@ -487,6 +493,7 @@ def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_
     ks = _rows_strides(k, "k", (T, Hkv, d), dtype, dev)
     vs = _rows_strides(v, "v", (T, Hkv, dv), dtype, dev)
     slots = _i32_buffer(slot_map, "slot_map", (T,), dev)
+    _check_workspace(workspace_buf, dev)
     guard, ptr, other = _enter(dev, stream)
     try:
         if workspace_buf is None:
@@ -544,6 +551,7 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
             raise ValueError(f"{name} must be a contiguous float32 [Hq, T] tensor on q's device")
     st = (Hq * dv, dv) if o is None else _rows_strides(o, "o", (T, Hq, dv), dtype, dev)
     batch = _pack_batch(q, st[0], st[1], page_table, kv_lens, cu_q, max_q, causal, window, scale, sink)
+    _check_workspace(workspace_buf, dev)
     guard, ptr, other = _enter(dev, stream)
     made = []
     try:

@@ -361,3 +361,18 @@ def test_rows_of_a_kv_head_past_two_to_the_30(bpa):
 
     assert need(1 << 20, 1 << 10, 1) > 256 and need(1 << 27, 64, 8) > 256
     assert need((1 << 20) + 1, 1 << 10, 1) == 256 and need(1 << 30, 2, 1) == 256 and need(1 << 16, 65535, 1) == 256
+
+
+# ---- arguments that would reach memory that is not theirs ----------------------------------------------
+@pytest.mark.parametrize("name", ["plan", "append", "attn"])
+def test_binding_refuses_workspaces_that_are_not_memory_of_the_device(bpa, streams, name):
+    now, made, launched = streams
+    call = _cache_calls(bpa)[name]
+    for bad in (torch.zeros(1024, dtype=torch.uint8),                             # the CPU's
+                _Fake(torch.zeros(1, dtype=torch.uint8).expand(1024)),            # one byte
+                _Fake(torch.zeros(2048, dtype=torch.uint8)[::2]), _Fake(torch.zeros(1024, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace_buf=bad)
+    assert not launched and not made
+    call(workspace_buf=_Fake(torch.zeros(1024, dtype=torch.uint8)))
+    assert len(launched) == 1
