@@ -322,7 +322,7 @@ typedef struct bpa_cache_batch {
                                 * choice of kernel; a larger request is still computed in full */
     const void* q;             /* [T, Hq, d] */
     int64_t q_strides[2];      /* (row, head) of q, last dim contiguous */
-    int64_t o_strides[2];      /* (row, head) of o */
+    int64_t o_strides[2];      /* (row, head) of o, above 0 where there is more than one */
     const int32_t* page_table; /* [R, max_pages], contiguous */
     const int32_t* kv_lens;    /* [R] tokens in the cache, the step's own included */
     const int32_t* cu_q;       /* [R + 1] first row of each request, ascending */

@@ -258,6 +258,8 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
     if (!a.table || !a.kv_lens || !a.cu_q || (a.T && (!a.q || !o)))
         return fail(BPA_ERR_INVALID_ARG, "q, o, page_table, kv_lens or cu_q is NULL");
     if (!m != !l) return fail(BPA_ERR_INVALID_ARG, "m and l: both or neither");
+    if ((a.T > 1 && a.os[0] == 0) || (a.Hq > 1 && a.os[1] == 0))
+        return fail(BPA_ERR_INVALID_ARG, "o_strides must be above 0: rows of o would lie over one another");
     if ((st = check_ws(workspace, workspace_bytes, cache_attn_mma_workspace(a))) != BPA_OK) return st;
     a.o = o;
     a.m = m;

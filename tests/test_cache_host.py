@@ -376,3 +376,18 @@ def test_binding_refuses_workspaces_that_are_not_memory_of_the_device(bpa, strea
     assert not launched and not made
     call(workspace_buf=_Fake(torch.zeros(1024, dtype=torch.uint8)))
     assert len(launched) == 1
+
+
+def test_attention_refuses_outputs_that_lie_over_one_another(bpa):
+    # strides of 0 (a descriptor whose o_strides were never filled in): rows would overwrite one another
+    L, p = bpa.lib(), 0x40000
+
+    def call(row, head, **over):
+        b = _batch(bpa, **over)
+        b.o_strides[:] = (row, head)
+        return L.bpa_cache_attn(ctypes.byref(_cache(bpa)), ctypes.byref(b), p, p, p, p, 256, None)
+
+    assert call(0, 64) == 1 and b"o_strides" in L.bpa_last_error()
+    assert call(256, 0) == 1 and b"o_strides" in L.bpa_last_error()
+    assert call(256, 64) == 3                            # past that check: the workspace is too small
+    assert call(0, 64, T=1) == 3                         # a single row never steps
