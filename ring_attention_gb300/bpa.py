@@ -363,6 +363,13 @@ def _i32_buffer(t, name, shape, dev):
     return t.data_ptr()
 
 
+def _int32(x, name):
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must lie in [-2^31, 2^31), got {x}")
+    return x
+
+
 def _check_workspace(t, dev):
     if t is not None and (t.dtype is not _U8 or not t.is_contiguous() or t.get_device() != dev):
         raise ValueError("workspace_buf must be a contiguous uint8 tensor on the device of the other tensors")
@@ -450,7 +457,7 @@ def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, pa
     all int32.  ctx_lens_out=ctx_lens and free_count_out=free_count update in place."""
     if ctx_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("ctx_lens must be [R], page_table [R, max_pages], free_pages [num_pages]")
-    dev, R, T = ctx_lens.get_device(), ctx_lens.shape[0], int(T)
+    dev, R, T, page_size = ctx_lens.get_device(), ctx_lens.shape[0], _int32(T, "T"), _int32(page_size, "page_size")
     rows, max_pages = page_table.shape
     if rows != R:
         raise ValueError(f"page_table has {rows} rows for {R} requests")
@@ -474,7 +481,7 @@ def bpa_cache_plan(ctx_lens, new_lens, page_table, free_pages, free_count, *, pa
                 made.append(outs[i])
         if workspace_buf is None:
             workspace_buf = _empty(256, dtype=_U8, device=where)
-        st = lib().bpa_cache_plan(R, T, int(page_size), num_pages, max_pages, *ins, *[t.data_ptr() for t in outs],
+        st = lib().bpa_cache_plan(R, T, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs],
                                   workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
         _leave(guard, other, dev, made)
@@ -492,14 +499,14 @@ def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_
     T = k.shape[0]
     ks = _rows_strides(k, "k", (T, Hkv, d), dtype, dev)
     vs = _rows_strides(v, "v", (T, Hkv, dv), dtype, dev)
-    slots = _i32_buffer(slot_map, "slot_map", (T,), dev)
+    slots, max_new = _i32_buffer(slot_map, "slot_map", (T,), dev), _int32(max_new, "max_new")
     _check_workspace(workspace_buf, dev)
     guard, ptr, other = _enter(dev, stream)
     try:
         if workspace_buf is None:
             workspace_buf = _empty(256, dtype=_U8, device=k.device)
         st = lib().bpa_cache_append(cache, k.data_ptr(), v.data_ptr(), _TWO_PACK(ks[0], ks[1]), _TWO_PACK(vs[0], vs[1]),
-                                    slots, T, int(max_new), workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
+                                    slots, T, max_new, workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
         _leave(guard, other, dev, ())
     if st:
@@ -517,10 +524,10 @@ def _pack_batch(q, o_row, o_head, page_table, kv_lens, cu_q, max_q, causal, wind
                              sink.get_device() != dev):
         raise ValueError("sink must be a contiguous float32 [Hq] tensor on q's device")
     wl, wr = (-1, -1) if window is None else window
-    return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, int(max_q), q.data_ptr(), st[0], st[1], o_row, o_head,
+    return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, _int32(max_q, "max_q"), q.data_ptr(), st[0], st[1], o_row, o_head,
                        _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
                        _i32_buffer(cu_q, "cu_q", (R + 1,), dev), 0.0 if scale is None else float(scale),
-                       1 if causal else 0, int(wl), int(wr), 0 if sink is None else sink.data_ptr())
+                       1 if causal else 0, _int32(wl, "window"), _int32(wr, "window"), 0 if sink is None else sink.data_ptr())
 
 
 def make_cache_batch(q, page_table, kv_lens, cu_q, *, max_q=0, causal=True, window=(-1, -1), scale=None,

@@ -391,3 +391,22 @@ def test_attention_refuses_outputs_that_lie_over_one_another(bpa):
     assert call(256, 0) == 1 and b"o_strides" in L.bpa_last_error()
     assert call(256, 64) == 3                            # past that check: the workspace is too small
     assert call(0, 64, T=1) == 3                         # a single row never steps
+
+
+# ---- numbers that 32 bits do not hold --------------------------------------------------------------------
+@pytest.mark.parametrize("name,kw", [("plan", dict(T=(1 << 32) + 8)), ("plan", dict(page_size=(1 << 32) + 16)), ("plan", dict(T=-(1 << 32) + 8)),
+                                     ("append", dict(max_new=1 << 32)), ("attn", dict(max_q=1 << 32)),
+                                     ("attn", dict(window=(1 << 31, -1))), ("attn", dict(window=(-1, -(1 << 33))))],
+                         ids=["T", "page_size", "T_negative", "max_new", "max_q", "left", "right"])
+def test_binding_refuses_numbers_past_32_bits(bpa, streams, name, kw):
+    now, made, launched = streams
+    f = {n: _Fake(x) for n, x in _tensors().items()}
+    i32 = dict(dtype=torch.int32)
+    args = {"plan": dict(ctx_lens=_Fake(torch.zeros(3, **i32)), new_lens=_Fake(torch.zeros(3, **i32)), page_table=_Fake(torch.zeros(3, 4, **i32)),
+                         free_pages=_Fake(torch.zeros(9, **i32)), free_count=_Fake(torch.zeros(1, **i32)), page_size=16, T=8),
+            "append": dict(k=_Fake(torch.zeros(5, 2, 64, dtype=torch.bfloat16)), v=_Fake(torch.zeros(5, 2, 32, dtype=torch.bfloat16)),
+                           slot_map=_Fake(torch.zeros(5, **i32)), **{n: f[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale")}),
+            "attn": f}[name]
+    with pytest.raises(ValueError, match="2\\^31"):
+        getattr(bpa, "bpa_cache_" + name)(**{**args, **kw})
+    assert not launched and not made
