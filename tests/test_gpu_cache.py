@@ -938,3 +938,83 @@ def test_append_reports_slots_below_minus_one(bpa, bad):
     wc, wsc = ora.append(f64(x), [3, -1, -1], kc, ks)
     np.testing.assert_array_equal(gc, wc)
     np.testing.assert_array_equal(gs, wsc)
+
+
+def test_attention_prompts_under_a_graph(bpa):
+    """A captured call with requests of many and of few rows, replayed on other values: scales that send a request from
+    one kernel to the other, a page that is no longer there, and back; the workspace is the same throughout."""
+    rng = np.random.default_rng(39)
+    cases = [make_step(rng, [130, 37, 250], [70, 1, 33], 32, 8, 128, 128, 64) for _ in range(4)]
+    for c in cases[1:]:
+        for n in ("table", "kv", "cu"):
+            c[n] = cases[0][n]
+    for c in cases:                                # the rows behind the last token of each
+        for n in ("kc", "vc"):
+            c[n][(c[n] & 0x7F) == 0x7F] = 0
+    cases[1]["vs"][:] = np.exp2(rng.integers(-100, 100, cases[1]["vs"].shape)).astype(np.float32)
+    cases[2]["kv"] = np.array([200, 0, 40])
+    ts = [on_gpu(c, torch.bfloat16) for c in cases]
+    t = [x.clone() for x in ts[0]]
+    D, B = bpa.make_cache_desc(*t[1:5], torch.bfloat16), bpa.make_cache_batch(t[0], *t[5:], max_q=70)
+    ws = torch.full((bpa.bpa_cache_attn_workspace_size(D, B),), 255, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        bpa.bpa_cache_attn(*t, max_q=70, workspace_buf=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            o, m, l = bpa.bpa_cache_attn(*t, max_q=70, workspace_buf=ws)
+        for i in (0, 1, 2, 3, 1, 0):
+            for dst, src in zip(t, ts[i]):
+                dst.copy_(src)
+            g.replay()
+            s.synchronize()
+            bpa.bpa_check(ws)
+            check_attention(cases[i], torch.bfloat16, o, m, l)
+
+
+@DTYPES
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_attention_shared_pages_and_leading_rows(bpa, kernel, dtype):
+    # two requests over the same first pages, one page twice in a row of the table, rows in front of the first request
+    c = make_step(np.random.default_rng(40), *KERNELS[kernel])
+    P = c["kc"].shape[2]
+    n = min(c["kv"]) // P                          # whole pages of both
+    c["table"] = c["table"].copy()
+    c["table"][1, :n] = c["table"][0, :n]
+    c["table"][0, 1] = c["table"][0, 0]
+    c["q"] = np.concatenate([np.full((3,) + c["q"].shape[1:], np.nan), c["q"]])
+    c["cu"] = c["cu"] + 3
+    t = on_gpu(c, dtype)
+    o = torch.full((len(c["q"]), t[0].shape[1], c["vc"].shape[3]), 77.0, dtype=dtype, device="cuda")
+    _, m, l = bpa.bpa_cache_attn(*t, max_q=c["max_q"], o=o)
+    torch.cuda.synchronize()
+    check_attention({**c, "q": np.nan_to_num(c["q"])}, dtype, o, m, l)      # its bound takes every row's q
+    assert (o[:3] == 77).all()
+
+
+HEADS_ALONE = [([300, 0], [65, 200], 32, 32, 128, 128, 64), ([0, 129], [300, 1], 32, 32, 64, 64, 16), ([7], [513], 16, 16, 128, 64, 32)]
+
+
+@pytest.mark.parametrize("case", HEADS_ALONE, ids=lambda c: f"d{c[4]}_{c[5]}_q{max(c[1])}")
+def test_attention_many_rows_of_heads_of_their_own(bpa, case):
+    c = make_step(np.random.default_rng(41), *case)
+    run_and_check(bpa, c, torch.bfloat16)
+    run_and_check(bpa, c, torch.bfloat16, window=(130, -1))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_append_of_a_slot_twice_leaves_other_pages(bpa, rows):
+    # what the page of the two rows holds is unspecified, everything else is not
+    rng = np.random.default_rng(42)
+    kc, ks = random_cache(rng, 9, 2, 16, 32)
+    x = rng.standard_normal((rows + 3, 2, 32)).astype(np.float32)
+    slots = np.concatenate([[5 * 16 + 3, 5 * 16 + 3, 5 * 16 + 3], np.arange(16, 16 + rows)])
+    tx = torch.from_numpy(x).cuda()
+    (gc, gs, vc, vs), ws = run_append(bpa, tx, tx, slots, kc, kc, ks, ks, max_new=rows)
+    bpa.bpa_check(ws)
+    wc, wsc = ora.append(x.astype(np.float64), np.concatenate([[-1] * 3, slots[3:]]), kc, ks)
+    rest = np.arange(9) != 5
+    for codes, scales in ((gc, gs), (vc, vs)):
+        np.testing.assert_array_equal(codes[rest], wc[rest])
+        np.testing.assert_array_equal(scales[rest], wsc[rest])
