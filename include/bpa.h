@@ -319,7 +319,8 @@ typedef struct bpa_cache_batch {
     int32_t R, T, Hq;          /* requests, packed rows (<= 2^30), q heads (a multiple of Hkv, <= 65535) */
     int32_t max_pages;         /* columns of page_table; page_size * max_pages <= 2^30 */
     int32_t max_q;             /* no request has more rows than this; 0 selects T.  It guides the
-                                * choice of kernel; a larger request is still computed in full */
+                                * choice of kernel; a larger request is still computed in full.  Set it
+                                * for generation: single tokens take half as long again without it */
     const void* q;             /* [T, Hq, d] */
     int64_t q_strides[2];      /* (row, head) of q, last dim contiguous */
     int64_t o_strides[2];      /* (row, head) of o, above 0 where there is more than one */

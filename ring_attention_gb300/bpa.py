@@ -546,7 +546,7 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
                    window=(-1, -1), scale=None, sink=None, o=None, m=None, l=None, workspace_buf=None, stream=None):
     """Attention of packed rows q [T, Hq, d] over the cache.  Returns (o, m, l): o [T, Hq, dv]; m and
     l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  max_q: the most rows of a
-    request (0: unknown), guides the choice of kernel."""
+    request (0: unknown, and single tokens then take half as long again), guides the choice of kernel."""
     dtype = q.dtype
     cache, _, d, dv, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)
     if q.dim() != 3 or q.shape[2] != d or q.get_device() != dev:

@@ -9,9 +9,10 @@
 
 namespace bpa {
 
-// Query rows of a kv head up to which a request is one of few rows.  Measured with 33 requests of 8 to 48
-// rows (1 to 6 drafted tokens of 8 heads): 58.5 us at 64; at 32, where those of more go to the tensor
-// cores, 64.4; at 15, 73.5.  Pieces of prompts (thousands of rows) take 1,531 us there and 7,225 here.
+// Query rows of a kv head up to which a request is one of few rows.  Measured at 64, 32 and 15, requests of
+// more going to the tensor cores: 33 requests of 8 to 48 rows (1 to 6 drafted tokens of 8 heads, window
+// 1,024) 41.2, 59.9 and 73.4 us; 33 of 8 to 64 rows over up to 8,000 tokens, 128 channels 222, 194 and
+// 230.  Pieces of prompts (thousands of rows) take 1,540 us there and 7.1 ms here.
 constexpr int kFewRows = 64;
 constexpr int kPlanMaxR = 8192;      // requests of one plan: their lengths and offsets sit in shared memory
 

@@ -62,12 +62,14 @@ BPA_DEV float scale_for(float amax) {
 // One warp per (ROWS rows, head, tensor): it takes the runs that begin in its rows, one after the
 // other, reading a run twice (largest magnitude, then codes; the second time from L2).  Bounded by the
 // latency of a warp's chain (slots, rows, scale, rows again) rather than by bytes: prompts of 19,000
-// rows x 8 heads x (128 + 64) bf16 channels take 31 us, 2.9 TB/s of their 90 MB; sixteen loads in flight a
-// lane (four: 33 us).  ROWS = 1 when requests bring few rows (every row is then a run of its own, or
-// nearly); ROWS = 16 for prompts, whose runs are whole pages: sixteen times fewer warps that find no
-// beginning.  The last block looks the slots over for the status word, so that nothing has to clear it
-// before.  ONE: a row takes no more than 32 lanes, so the loops over rows are the only ones and their
-// loads overlap (with a loop over a row's units inside: 41 us).
+// rows x 8 heads x (128 + 64) bf16 channels take 31 us, 2.9 TB/s of their 90 MB; loops over rows are
+// unrolled sixteen times (four: 33 us), though a thread's 64 registers do not hold sixteen loads at once.
+// ROWS = 1 when requests bring few rows (every row is then a run of its own, or nearly); ROWS = 16 for
+// prompts, whose runs are whole pages: sixteen times fewer warps that find no beginning.  The last block
+// looks the slots over for the status word, so that nothing has to clear it before; as it starts late,
+// that is 0.7 of the 31 us, and 11 of the 95 that four times the rows take.  ONE: a row takes no more than
+// 32 lanes, so the loops over rows are the only ones and their loads overlap (with a loop over a row's
+// units inside: 41 us).
 template <typename E, int VE, int ROWS, bool ONE>
 __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
     wait_for_previous();

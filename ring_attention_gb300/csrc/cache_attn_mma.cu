@@ -13,13 +13,13 @@
 //               2^15); a weight below 2^-33 of the largest is dropped.  float32: W as two halves.
 //
 // Bounded by the bytes of K and V where a kv head has up to 8 rows: 64 requests of 8,192 tokens, 8 kv
-// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 97.2 us (5.8 TB/s);
-// three of 100,000 to 131,071 tokens 121 us (6.1 TB/s).  Smaller pieces cost more: 40 requests of up
-// to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 50.7 us (2.6 TB/s; mostly launches,
+// heads of 128 channels, 4 q heads each 155 us (6.9 TB/s); of 200 to 8,191 tokens 98.2 us (5.7 TB/s);
+// three of 100,000 to 131,071 tokens 122 us (6.1 TB/s).  Smaller pieces cost more: 40 requests of up
+// to 4,095 tokens, 16 q heads a kv head, 128 + 64 channels 49.6 us (2.7 TB/s; mostly launches,
 // items' starts and ends and the hand-over of tiles, which stay without the arithmetic).
 // So the CTAs are persistent and each takes an equal share of all cost of all items, whatever the
 // lengths: a tile counts one, two or four where its rows take one, two or four of the warps (33
-// requests of 8 to 48 rows, 41.5 us now: 45.3 against 58.8 with every tile counting one), and an item's
+// requests of 8 to 48 rows, 41.7 us now: 45.3 against 58.8 with every tile counting one), and an item's
 // start and end six more (the 40 requests above: 51.3 us; four 53.9).  A share may begin and end inside
 // an item.  Pieces of items go to the workspace as (m, l, O) and a second, small launch joins them in
 // ascending order, so nothing is added in an order that changes.  Per CTA one warp copies tiles by TMA
@@ -1008,6 +1008,8 @@ bool plan_of(const CacheAttnArgs& a, Plan& p) {
     // Up to 8 rows half as many registers leave more CTAs on an SM: 98.5 us against 142 with 16 rows a warp (64
     // requests of 200 to 8,191 tokens, 4 rows a kv head).  With 16 rows one warp converts a code once: 55
     // us against 58 with two warps of 8 rows (40 of up to 4,095), and with 8 to 48 rows 45.1 against 47.0.
+    // The host knows only max_q: one token of many requests beside a request of more, or with max_q
+    // unknown, is computed 16 rows a warp too (98 us -> 151).
     p.NT = rows <= 8 ? 1 : 2;
     p.RT = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.rows_per = 8 * p.NT * p.RT;

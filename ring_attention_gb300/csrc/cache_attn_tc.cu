@@ -21,7 +21,7 @@
 // bytes): about three instructions and one exponential a score.  Two threads share a row (64 columns
 // each), so sixteen warps work on the softmax and cover each other's latencies; its loops stay rolled,
 // since unrolled ones kept the warps waiting for instructions.  Five pieces of prompts, 6,852 rows of 32
-// heads over up to 16,000 tokens, 128 channels: 1,531 us, 921 TFLOP/s (2,222 us with a thread to a row
+// heads over up to 16,000 tokens, 128 channels: 1,540 us, 917 TFLOP/s (2,222 us with a thread to a row
 // and unrolled loops; 1,738 with eight converting warps; the kernel for few rows 7,225).
 // Roles (768 threads; registers moved to the softmax by setmaxnreg):
 //   warps 0-7, 8-15  softmax of row tile 0, 1; of eight warps the second four take columns 64-127.  They
@@ -732,8 +732,11 @@ bool cache_attn_tc_takes(const CacheAttnArgs& a) {
     if (rows <= kFewRows) return false;
     // An item's keys are not shared between CTAs here, as they are in the kernel for few rows: with few
     // items (one token of 128 heads over a long context) that one fills the GPU and this one does not.
-    // With all CTAs busy this one is 4.7 times faster (pieces of prompts 1531 and 7225 us), so from about
-    // a fifth of them on it wins.
+    // With all CTAs busy this one is 4.6 times faster (pieces of prompts 1,540 us and 7.1 ms).  The border, one
+    // request over 131,072 tokens, 4 q heads on each of 8 kv heads, this kernel and that one: 16 items
+    // (128 tokens) 2,383 and 1,367 us, 24 items 2,387 and 2,036, 32 items 2,388 and 2,703; over 4,096 tokens 16
+    // items 108 and 70 us, 32 items 109 and 118; four requests over 8,192, 32 items 184 and 199 us, but 155 and
+    // 113 where the items are half full (32 tokens).
     const int64_t items = std::min(a.R * ((rows + kRows - 1) / kRows), static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
     return items >= 32;
 }

@@ -7,10 +7,10 @@
 // find their request by a binary search over the sums in shared memory.
 //
 // Bounded by latency: a step of 256 generating requests moves 7 KB, so its time is the launch, one
-// round trip for the lengths, the scans and one dependent round trip for the page ids: 4 us.  A
+// round trip for the lengths, the scans and one dependent round trip for the page ids: 5.3 us.  A
 // cluster of eight CTAs shares the rows (each repeats the scans, which cost less than handing the
-// sums over): 64 requests of 64,000 rows in all 11 us against 56 with one CTA, 4,096 rows 5.0 against
-// 7.8, and one row for each of 256 requests 4.0 against 4.1, so that no size wants fewer.  The cluster
+// sums over): 64 requests of 64,000 rows in all 11.1 us against 53.8 with one CTA, 4,096 rows 5.5 against
+// 8.6, and one row for each of 256 requests 5.3 against 5.3, so that no size wants fewer.  The cluster
 // barrier between the last read of the lengths and the first write is what lets ctx_lens_out and
 // free_count_out overwrite their inputs.
 #include <cooperative_groups.h>
@@ -30,6 +30,7 @@ struct Scan {
     long long warp[kThreads / 32];
     long long carry;
 };
+static_assert(2 * sizeof(Scan) + 64 <= 1024, "the kernel's static shared memory");   // launch_cache_plan counts on it
 
 // Exclusive running sum of v over the block, continued from s.carry, which moves on by the total.
 __device__ long long block_scan(Scan& s, long long v) {
