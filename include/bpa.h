@@ -273,6 +273,58 @@ bpa_status bpa_select_blocks_noalloc(const void* q, const void* k, int32_t dtype
                                      int32_t block_size, int32_t top_n,
                                      int32_t* block_idx_out, void* stream);
 
+/* ---- norms of q and k with the position rotation --------------------------------------------
+ *
+ * What a model does to q and k between their projections and bpa_fwd / bpa_cache_append /
+ * bpa_cache_attn, in one pass, and its backward pass (behind bpa_bwd).  An addition of this
+ * library; the pages have no counterpart.  For each row (b, s) and head of q (and likewise of k):
+ *   norm:      n = q_weight * q / sqrt(mean over the head's d channels of q^2 + eps)
+ *   rotation:  for pair i < rot / 2 of channels (x, y) = (i, i + rot / 2) of n, or (2i, 2i + 1) when
+ *              interleaved, with t = positions[b, s] * inv_freq[i]:
+ *                x' = x cos t - y sin t,   y' = y cos t + x sin t;
+ *              channels from rot on keep n.
+ * Norms and angles are exact products and float32 sums whatever the dtype; the angle of a far position
+ * loses nothing; results are rounded once.  A row whose position is negative (bpa_cache_plan gives -1
+ * to rows without a place) is skipped: forward leaves its outputs as they were, backward gives it
+ * gradients of 0 and nothing to the weights'. */
+typedef struct bpa_rope_desc {
+    uint32_t struct_size;      /* = sizeof(bpa_rope_desc); zero-initialise the rest */
+    int32_t dtype;             /* bpa_dtype of q, k and what is computed from them */
+    int32_t B, S;              /* B >= 1, S >= 0, B * S <= 2^30 (packed rows: B 1, S = T) */
+    int32_t Hq, Hkv;           /* heads of q and k; 0: that tensor is left out */
+    int32_t d;                 /* head dim, 1..512 */
+    int32_t rot;               /* rotated channels, even, 0..d */
+    int32_t interleaved;       /* nonzero: pairs are neighbours */
+    int32_t norm;              /* nonzero: RMS norm of each head */
+    float eps;                 /* of the norm, a positive normal number */
+    int32_t reserved;          /* must be 0 */
+    const void* q;             /* [B, S, Hq, d] before norm and rotation */
+    const void* k;             /* [B, S, Hkv, d] */
+    int64_t q_strides[3];      /* (b, s, h) strides of q and dq, >= 0, last dim contiguous */
+    int64_t k_strides[3];      /* ... of k and dk */
+    int64_t qo_strides[3];     /* ... of q_out and dq_out */
+    int64_t ko_strides[3];     /* ... of k_out and dk_out */
+    const int32_t* positions;  /* [B, S], contiguous, or NULL: s */
+    const float* inv_freq;     /* [rot / 2] radians per position */
+    const float* q_weight;     /* [d] or NULL (ones); only with norm */
+    const float* k_weight;
+} bpa_rope_desc;
+
+/* q_out [B, S, Hq, d], k_out [B, S, Hkv, d].  An output may be its input where their strides agree, and
+ * must not overlap an input in any other way.  Needs no workspace. */
+bpa_status bpa_rope_fwd(const bpa_rope_desc* desc, void* q_out, void* k_out, void* stream);
+
+/* Bytes of workspace bpa_rope_bwd needs (a multiple of 256); 0 if the descriptor is invalid. */
+size_t bpa_rope_workspace_size(const bpa_rope_desc* desc);
+
+/* dq, dk from the gradients dq_out, dk_out of the outputs and from q, k (the inputs of the forward
+ * pass; not read without norm), and, where not NULL, the float32 gradients dq_weight, dk_weight [d] of
+ * the weights, summed over rows and heads in an order that does not change from call to call.  dq may
+ * be q or dq_out (dk likewise) where the strides agree, and must not overlap an input in any other
+ * way. */
+bpa_status bpa_rope_bwd(const bpa_rope_desc* desc, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                        float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- paged 8-bit key / value cache --------------------------------------------------------
  *
  * The step of a program that answers with a trained model: plan the step, append the new

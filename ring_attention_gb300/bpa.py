@@ -78,6 +78,20 @@ class bpa_cache_batch(ctypes.Structure):
     ]
 
 
+class bpa_rope_desc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("dtype", ctypes.c_int32),
+        ("B", ctypes.c_int32), ("S", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+        ("qo_strides", ctypes.c_int64 * 3), ("ko_strides", ctypes.c_int64 * 3),
+        ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+    ]
+
+
 _CACHE_SIZE, _BATCH_SIZE = ctypes.sizeof(bpa_cache_desc), ctypes.sizeof(bpa_cache_batch)
 _TWO_PACK = struct.Struct("@2q").pack
 
@@ -126,6 +140,9 @@ def lib() -> ctypes.CDLL:
         L.bpa_cache_attn_workspace_size.argtypes, L.bpa_cache_attn_workspace_size.restype = [P, P], sz
         L.bpa_cache_attn.argtypes = [P, P, P, P, P, P, sz, P]
         L.bpa_cache_attn.restype = ctypes.c_int
+        L.bpa_rope_fwd.argtypes, L.bpa_rope_fwd.restype = [P, P, P, P], ctypes.c_int
+        L.bpa_rope_workspace_size.argtypes, L.bpa_rope_workspace_size.restype = [P], sz
+        L.bpa_rope_bwd.argtypes, L.bpa_rope_bwd.restype = [P, P, P, P, P, P, P, P, sz, P], ctypes.c_int
         _lib = L
     return _lib
 
@@ -584,3 +601,153 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
     if st:
         _raise_if(st, "bpa_cache_attn")
     return o, m, l
+
+
+# ---- norms of q and k with the position rotation ---------------------------------------------------
+# The same lean marshalling (one packed bpa_rope_desc) and the same meaning of stream as above.
+_ROPE_PACK = struct.Struct("@I9ifiPP12qPPPP").pack
+_ROPE_SIZE = ctypes.sizeof(bpa_rope_desc)
+
+
+def _heads_of(t, name, shape, dtype, dev):
+    """(b, s, h) strides of a [B, S, H, d] or packed [T, H, d] tensor."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor on the device of the others, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    return st[:3] if len(shape) == 4 else (0, st[0], st[1])
+
+
+def _pack_rope(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, interleaved, q_like, k_like):
+    """Packed bpa_rope_desc; q_like, k_like: the tensors that give the strides behind norm and rotation."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
+    shape, dtype, dev = first.shape, first.dtype, first.get_device()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"tensors must be bfloat16 or float32, got {dtype}")
+    if len(shape) not in (3, 4):
+        raise ValueError("q and k must be [B, S, H, d] or packed [T, H, d]")
+    rows, d = shape[:-2], shape[-1]
+    B, S = rows if len(rows) == 2 else (1, rows[0])
+    sides = []
+    for t, like, name in ((q, q_like, "q"), (k, k_like, "k")):
+        if t is None:
+            sides.append((0, 0, (0, 0, 0), (0, 0, 0)))
+            continue
+        if t.dim() != len(shape) or t.shape[:-2] != rows or t.shape[-1] != d:
+            raise ValueError("q and k must share rows and head dim")
+        st = _heads_of(t, name, t.shape, dtype, dev)
+        sides.append((t.shape[-2], t.data_ptr(), st, st if like is None else _heads_of(like, name + "'s output or its gradient",
+                                                                                      t.shape, dtype, dev)))
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype is not _F32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or inv_freq.get_device() != dev:
+            raise ValueError("inv_freq must be a contiguous float32 [rot / 2] tensor on the device of the others")
+        rot = 2 * inv_freq.shape[0]
+    for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
+        if w is not None and (w.dtype is not _F32 or w.shape != (d,) or not w.is_contiguous() or w.get_device() != dev):
+            raise ValueError(f"{name} must be a contiguous float32 [d] tensor on the device of the others")
+        if w is not None and t is None:
+            raise ValueError(f"{name} without its tensor")
+    pos = 0 if positions is None else _i32_buffer(positions, "positions", rows, dev)
+    (Hq, qp, qs, qo), (Hkv, kp, ks, ko) = sides
+    return _ROPE_PACK(_ROPE_SIZE, code, B, S, Hq, Hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, float(eps), 0, qp, kp,
+                      *qs, *ks, *qo, *ko, pos, 0 if inv_freq is None else inv_freq.data_ptr(),
+                      0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr()), dev
+
+
+def make_rope_desc(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, *, norm=True, eps=1e-6, interleaved=False,
+                   q_out=None, k_out=None) -> bpa_rope_desc:
+    """A bpa_rope_desc of the tensors (no data is touched); arguments as bpa_rope_fwd's."""
+    return bpa_rope_desc.from_buffer_copy(_pack_rope(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, interleaved,
+                                                     q_out, k_out)[0])
+
+
+def _dense(t):
+    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def bpa_rope_fwd(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, *, norm=True, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of each head of q [B, S, Hq, d] and k [B, S, Hkv, d] (or packed [T, H, d]; one of them
+    may be None) and the rotation of its first 2 len(inv_freq) channels by positions [B, S] or [T] (int32; None:
+    0, 1, ..).  Returns (q_out, k_out); q_out=q and k_out=k work in place.  Rows of negative position are
+    left as they are."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
+    for t, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if t is None and out is not None:
+            raise ValueError(f"{name} without its tensor")
+    dev = first.get_device()
+    guard, ptr, other = _enter(dev, stream)
+    made = []
+    try:
+        if q is not None and q_out is None:
+            q_out = _dense(q)
+            made.append(q_out)
+        if k is not None and k_out is None:
+            k_out = _dense(k)
+            made.append(k_out)
+        desc, _ = _pack_rope(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, interleaved, q_out, k_out)
+        st = lib().bpa_rope_fwd(desc, _ptr(q_out), _ptr(k_out), ptr)
+    finally:
+        _leave(guard, other, dev, made)
+    if st:
+        _raise_if(st, "bpa_rope_fwd")
+    return q_out, k_out
+
+
+def bpa_rope_workspace_size(desc: bpa_rope_desc) -> int:
+    return int(lib().bpa_rope_workspace_size(ctypes.byref(desc)))
+
+
+def bpa_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weight=None, k_weight=None, *, norm=True, eps=1e-6,
+                 interleaved=False, dq=None, dk=None, workspace_buf=None, stream=None):
+    """Backward of bpa_rope_fwd: q, k its inputs, dq_out, dk_out the gradients of its outputs.  Returns
+    (dq, dk, dq_weight, dk_weight): dq, dk with the strides of q, k (made dense where q, k are); the weights'
+    float32 [d] gradients, None without norm or tensor.  dq may be q or dq_out where the strides agree."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
+    dev = first.get_device()
+    for t, g, out, name in ((q, dq_out, dq, "dq"), (k, dk_out, dk, "dk")):
+        if (t is None) != (g is None) or (t is None and out is not None):
+            raise ValueError(f"{name}_out and {name} go with their tensor")
+        if out is not None and _heads_of(out, name, t.shape, t.dtype, dev) != _heads_of(t, name[1:], t.shape, t.dtype, dev):
+            raise ValueError(f"{name} must share the strides of its input")
+    desc, _ = _pack_rope(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, interleaved, dq_out, dk_out)
+    _check_workspace(workspace_buf, dev)
+    guard, ptr, other = _enter(dev, stream)
+    made = []
+    try:
+        grads, weights = [dq, dk], [None, None]
+        for i, t in enumerate((q, k)):
+            if t is None:
+                continue
+            if grads[i] is None:
+                grads[i] = torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
+                made.append(grads[i])
+            if norm:
+                weights[i] = _empty((t.shape[-1],), dtype=_F32, device=t.device)
+                made.append(weights[i])
+        if workspace_buf is None:
+            need = lib().bpa_rope_workspace_size(desc)
+            if need == 0:
+                _raise_if(BPA_ERR_INVALID_ARG, "bpa_rope_workspace_size")
+            workspace_buf = _empty(need, dtype=_U8, device=first.device)
+        st = lib().bpa_rope_bwd(desc, _ptr(dq_out), _ptr(dk_out), _ptr(grads[0]), _ptr(grads[1]), _ptr(weights[0]),
+                                _ptr(weights[1]), workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
+    finally:
+        _leave(guard, other, dev, made)
+    if st:
+        _raise_if(st, "bpa_rope_bwd")
+    return grads[0], grads[1], weights[0], weights[1]
