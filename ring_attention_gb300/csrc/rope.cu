@@ -342,7 +342,7 @@ struct Round {
 constexpr int kFirst = 1 << 30;
 
 template <typename E, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps, (BWD ? 4 : 5)) k_rope(const RopeArgs a, const Split sp, const float inv_d) {
+__global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeArgs a, const Split sp, const float inv_d) {
     constexpr int VE = Unit<E>::VE, N = VE / 2, PIECES = BWD ? 4 : 2;
     __shared__ __align__(16) Shared sh;
     __shared__ __align__(16) uint4 s_ring[kWarps][kStages][PIECES][32];
@@ -363,36 +363,40 @@ __global__ void __launch_bounds__(32 * kWarps, (BWD ? 4 : 5)) k_rope(const RopeA
         const RopeSide& t = a.side[side];
         walk.begin(sp.chunks[side]);
         const int64_t x_round = t.xs[2] * sp.per, y_round = t.ys[2] * sp.per;
-        const int64_t x_lane = gi * t.xs[2] + pl.ch[0], y_lane = gi * t.ys[2] + pl.ch[0];
-        int64_t x_at = 0, y_at = 0;    // the round that is read next: its elements, heads left of the item, position
-        int left = 0, pos_at = 0;
+        const E* const x_lane = static_cast<const E*>(t.x) + gi * t.xs[2] + pl.ch[0];
+        const E* const g_lane = static_cast<const E*>(t.dy) + gi * t.ys[2] + pl.ch[0];
+        E* const to_lane = static_cast<E*>(t.y) + gi * (BWD ? t.xs[2] : t.ys[2]) + pl.ch[0];
+        const E *x = nullptr, *g = nullptr;    // the round that is read next: this lane's units,
+        int64_t out_at = 0;                    // the round's elements in the output,
+        int left = 0, pos_at = 0;              // heads left of the item and its position
         auto open = [&]() {            // the item's first round
             const int h0 = walk.at * sp.chunk, b = walk.row / a.S, s = walk.row - b * a.S;
             left = min(t.H - h0, sp.chunk);
             pos_at = a.pos ? *(a.pos + walk.row) : s;
-            x_at = b * t.xs[0] + s * t.xs[1] + h0 * t.xs[2];
-            y_at = b * t.ys[0] + s * t.ys[1] + h0 * t.ys[2];
+            const int64_t x_at = b * t.xs[0] + s * t.xs[1] + h0 * t.xs[2], y_at = b * t.ys[0] + s * t.ys[1] + h0 * t.ys[2];
+            x = x_lane + x_at;
+            if (BWD) g = g_lane + y_at;
+            out_at = BWD ? x_at : y_at;
         };
         bool first = true;
         auto issue = [&](int st) {     // the next round into stage st
             if (left > 0) {
                 const bool on = mine && gi < left && pos_at >= 0, on_x = on && (!BWD || a.norm);
                 const uint32_t to = ring + st * (PIECES * 512);
-                const E* x = static_cast<const E*>(t.x) + x_at + x_lane;
                 copy16(to, x, on_x);
                 copy16(to + 512, x + other, on_x);
                 if (BWD) {
-                    const E* g = static_cast<const E*>(t.dy) + y_at + y_lane;
                     copy16(to + 1024, g, on);
                     copy16(to + 1536, g + other, on);
                 }
             }
             copies_close();
-            if (lane == 0) s_round[warp][st] = {BWD ? x_at : y_at, pos_at, left <= 0 ? 0 : first ? left | kFirst : left};
+            if (lane == 0) s_round[warp][st] = {out_at, pos_at, left <= 0 ? 0 : first ? left | kFirst : left};
             if (left <= 0) return;
             left -= sp.per;
-            x_at += x_round;
-            y_at += y_round;
+            x += x_round;
+            if (BWD) g += y_round;
+            out_at += BWD ? x_round : y_round;
             first = left <= 0;
             if (!first) return;
             walk.next();
@@ -409,6 +413,15 @@ __global__ void __launch_bounds__(32 * kWarps, (BWD ? 4 : 5)) k_rope(const RopeA
                 w[h][i] = t.w && mine ? f2_pack(__ldg(at), __ldg(at + 1)) : f2_pack(1.f, 1.f);
                 dw[h][i] = 0;
             }
+        // channels that are not rotated keep what they had (0 times an infinity beside them would not)
+        auto rotated = [&](const uint64_t (&from)[2][N], uint64_t (&to)[2][N]) {
+            if (!part) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (pl.pair[h] < 0)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) to[h][i] = from[h][i];
+        };
         // the rotation's coefficients; forward: with the weights in them, so of either side
         constexpr int SIDES = INTER || !BWD ? 2 : 1;
         uint64_t P[SIDES][N], Q[SIDES][N];
@@ -450,11 +463,10 @@ __global__ void __launch_bounds__(32 * kWarps, (BWD ? 4 : 5)) k_rope(const RopeA
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        uint64_t o = INTER ? swapped(g[h][i]) : g[1 - h][i];
-                        if (part && pl.pair[h] < 0) o = 0;        // not rotated: whatever lies beside it stays out
-                        const uint64_t q = Q[h % SIDES][i];
+                        const uint64_t o = INTER ? swapped(g[h][i]) : g[1 - h][i], q = Q[h % SIDES][i];
                         y[h][i] = ffma2(g[h][i], P[h % SIDES][i], fmul2(INTER || h ? minus2(o) : o, q));
                     }
+                rotated(g, y);
 #pragma unroll
                 for (int i = 0; i < 2 * N; ++i) g[i / N][i % N] = y[i / N][i % N];
             }
@@ -489,11 +501,16 @@ __global__ void __launch_bounds__(32 * kWarps, (BWD ? 4 : 5)) k_rope(const RopeA
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        uint64_t o = INTER ? swapped(v[h][i]) : v[1 - h][i];
-                        if (part && pl.pair[h] < 0) o = 0;
-                        g[h][i] = fmul2(ffma2(v[h][i], P[h][i], fmul2(o, Q[h][i])), r2);
-                    }
+                    for (int i = 0; i < N; ++i)
+                        g[h][i] = ffma2(v[h][i], P[h][i], fmul2(INTER ? swapped(v[h][i]) : v[1 - h][i], Q[h][i]));
+                if (part) {
+                    uint64_t vw[2][N];
+#pragma unroll
+                    for (int i = 0; i < 2 * N; ++i) vw[i / N][i % N] = fmul2(v[i / N][i % N], w[i / N][i % N]);
+                    rotated(vw, g);
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * N; ++i) g[i / N][i % N] = fmul2(g[i / N][i % N], r2);
             } else if (a.norm) {
                 const uint64_t m2 = f2_pack(m, m), f2 = f2_pack(r * scale, r * scale);
 #pragma unroll
@@ -504,7 +521,7 @@ __global__ void __launch_bounds__(32 * kWarps, (BWD ? 4 : 5)) k_rope(const RopeA
                 }
             }
             if (mine && gi < (now.left & ~kFirst) && (BWD || pos >= 0)) {
-                E* p = static_cast<E*>(t.y) + now.out + (BWD ? x_lane : y_lane);
+                E* p = to_lane + now.out;
                 Unit<E> z;
                 z.set(g[0]);
                 *reinterpret_cast<uint4*>(p) = z.v;
@@ -595,7 +612,7 @@ template <typename E, bool BWD>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
     constexpr int VE = Unit<E>::VE;
     const bool vec = wide(a, VE);
-    const int blocks_most = std::min((BWD ? 4 : 5) * sm_count(), kRopeMaxBlocks);
+    const int blocks_most = std::min(4 * sm_count(), kRopeMaxBlocks);
     const Split sp = split_of(a, vec ? a.d / (2 * VE) : (a.d + 1) / 2, blocks_most * kWarps);
     const int64_t items = static_cast<int64_t>(a.B) * a.S * (sp.chunks[0] + sp.chunks[1]);
     const int blocks = static_cast<int>(std::min<int64_t>((items + kWarps - 1) / kWarps, blocks_most));

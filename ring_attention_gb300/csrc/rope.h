@@ -30,7 +30,7 @@ struct RopeArgs {
     uint32_t* status;                  // backward: the workspace's status word
 };
 
-constexpr int kRopeMaxBlocks = 800;    // blocks of a backward pass at most (five on each of 160 SMs)
+constexpr int kRopeMaxBlocks = 640;    // blocks of a call at most (four on each of 160 SMs)
 
 cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t s);
