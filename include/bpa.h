@@ -384,6 +384,11 @@ typedef struct bpa_cache_batch {
     int32_t window_left;       /* inclusive; -1 = unbounded */
     int32_t window_right;
     const float* sink;         /* [Hq] sink logits or NULL */
+    /* Fields below came later; a caller that sets struct_size = offsetof(bpa_cache_batch, tree) has none. */
+    const uint32_t* tree;      /* [T, tree_words] masks of a tree of drafted tokens, contiguous, or NULL: see
+                                * bpa_cache_attn.  Needs causal */
+    int32_t tree_words;        /* 1..32 */
+    int32_t reserved;          /* must be 0 */
 } bpa_cache_batch;
 
 /* Block tables and slot maps of one step, built on the device.
@@ -431,6 +436,78 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
                             const int64_t k_strides[2], const int64_t v_strides[2], const int32_t* slot_map,
                             int32_t T, int32_t max_new, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Masks and positions of trees of drafted tokens.  Row i of request r (of n rows, kv_lens[r] tokens with
+ * them) is a drafted token that follows its row parents[row], an index of the same request's rows below
+ * i, or the context's last token (-1).  With ctx = kv_lens[r] - n:
+ *     tree[row] = its own bit i and the bits of all its ancestors (bit j: word j / 32, bit j % 32),
+ *     positions[row] = ctx + the number of its ancestors among the rows (positions may be NULL).
+ * Rows of a request that waits (kv_lens 0, from bpa_cache_plan) and rows of no request get masks of 0 and
+ * positions -1.  A parent that is none (below -1, or not in front of its row) counts as -1; a
+ * request with more rows than tokens or than 32 * words gets masks of 0 and positions -1: both are
+ * BPA_ERR_DEVICE_CHECK.  1 <= words <= 32.  Workspace: 256 bytes (the status word). */
+bpa_status bpa_cache_tree(int32_t R, int32_t T, int32_t words, const int32_t* parents, const int32_t* kv_lens,
+                          const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Keeps the accepted tokens of a step in the cache (once per layer): token keep[r][i] of request r's n new
+ * ones, at place kv_lens[r] - n + keep[r][i] of its sequence, moves to place kv_lens[r] - n + i, for
+ * i < keep_count[r]; keep [R, max_keep] is ascending in each row (a path of a tree, say), entries from
+ * keep_count[r] on are not read.  A request of keep_count 0 is left alone.
+ *   For each page that a kept token lies in afterwards, head and tensor: scale = the largest of the page's
+ *   own, where tokens in front of the step's lie in it, and those of the pages that its kept
+ *   tokens come from, as they were before the call; codes from a smaller scale become e4m3(code * (old / scale))
+ *   (0 / 0 counts as 1).  Places behind the last kept token hold what they held, whatever it now stands for.
+ *   What the caller then does: new lengths kv_lens - n + keep_count, and bpa_cache_release for the pages
+ *   that this leaves over.
+ * The pages that are written must be the request's own (those of bpa_cache_plan and bpa_cache_fork are).  A count
+ * outside [0, min(n, max_keep)], entries that do not ascend within [0, n), a length or a page id that
+ * does not fit: BPA_ERR_DEVICE_CHECK, the request is left alone.
+ *   R * Hkv <= 2^30.  Workspace: 256 bytes (the status word). */
+bpa_status bpa_cache_keep(const bpa_cache_desc* cache, int32_t R, int32_t T, int32_t max_pages, const int32_t* keep,
+                          int32_t max_keep, const int32_t* keep_count, const int32_t* kv_lens, const int32_t* cu_q,
+                          const int32_t* page_table, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Pages held by several requests.  page_refs [num_pages] counts the holders of a page beyond the first: 0
+ * for a free page and for one that bpa_cache_plan has given out, so a program that forks starts it at 0
+ * and lets bpa_cache_fork and bpa_cache_release keep it.  A page that is not full has one holder.
+ *
+ * bpa_cache_fork: for each i < N, request dst[i] (without tokens: ctx_lens 0) becomes another holder of what
+ * src[i] holds: the full pages of its ctx_lens[src] tokens are entered into dst's row of page_table
+ * and counted, and for a last page that is not full dst gets one of its own off the end of the free list
+ * (in ascending i), for bpa_cache_copy: copy_src[i], copy_dst[i] name the two pages (-1, -1: no copy).
+ * As in bpa_cache_plan a fork that needs a page is granted if its page and those of all needing
+ * forks before it fit the free list; one that is not leaves dst as it was (ctx_lens_out 0), copies nothing.
+ *   ctx_lens_out = ctx_lens but for granted dst; it may be ctx_lens, free_count_out may be free_count, and no
+ *   other buffers may overlap.  A request may be src several times.  A request out of range, a dst that
+ *   holds tokens, is named twice or is also a src, a length past the table: BPA_ERR_DEVICE_CHECK, not
+ *   granted.  A bad page id: BPA_ERR_DEVICE_CHECK, entered as -1.
+ *   0 <= N, R <= 8192; the other limits as bpa_cache_plan's.  Workspace: 256 bytes.  One launch. */
+bpa_status bpa_cache_fork(int32_t N, int32_t R, int32_t page_size, int32_t num_pages, int32_t max_pages,
+                          const int32_t* src, const int32_t* dst, const int32_t* ctx_lens, int32_t* page_table,
+                          int32_t* page_refs, const int32_t* free_pages, const int32_t* free_count, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* ctx_lens_out, int32_t* free_count_out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Copies whole pages with their scales, all heads of k and v (once per layer): page src[i] to page dst[i]
+ * for i < N; a pair of -1 is skipped, a pair out of range too (BPA_ERR_DEVICE_CHECK).  No page may be dst twice or
+ * both src and dst of different pairs.  N * Hkv <= 2^29.  Workspace: 256 bytes.  One launch. */
+bpa_status bpa_cache_copy(const bpa_cache_desc* cache, int32_t N, const int32_t* src, const int32_t* dst, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Gives pages back: request r, of ctx_lens[r] tokens, keeps its first keep_lens[r] (all of them: nothing
+ * happens; 0: it is over) and is no holder any more of the pages behind them.  Each of these pages loses
+ * one holder; those without any left are appended to free_pages behind its *free_count entries, in ascending
+ * order of their ids, and count 0 in page_refs again.  ctx_lens_out = keep_lens, *free_count_out = the new count.
+ *   ctx_lens_out may be ctx_lens, free_count_out may be free_count; no other buffers may overlap.
+ *   A length outside [0, ctx_lens[r]], or a cut inside a page that has other holders (before the call):
+ *   BPA_ERR_DEVICE_CHECK, the request keeps all of its tokens.  A bad page id is skipped, a page given up more
+ *   often than it is held is freed once, ids that free_pages has no room for are dropped: BPA_ERR_DEVICE_CHECK.
+ *   1 <= R <= 8192; the other limits as bpa_cache_plan's.  Workspace: 256 bytes.  One launch. */
+bpa_status bpa_cache_release(int32_t R, int32_t page_size, int32_t num_pages, int32_t max_pages, const int32_t* ctx_lens,
+                             const int32_t* keep_lens, const int32_t* page_table, int32_t* page_refs, int32_t* free_pages,
+                             const int32_t* free_count, int32_t* ctx_lens_out, int32_t* free_count_out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace bpa_cache_attn needs (a multiple of 256); 0 if a descriptor is invalid. */
 size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cache_batch* batch);
 
@@ -441,6 +518,11 @@ size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cach
  *           && (window_right < 0 || k <= p + window_right)
  *     m, l, o as in bpa_fwd (a sink joins m and l); a row with no allowed key gives o = 0 and
  *     m = -inf, l = 0 (with a sink: m = sink, l = 1).
+ * Under a tree (batch->tree, from bpa_cache_tree or the caller's own) the step's own tokens are seen by mask
+ * instead: with n rows and ctx = kv_lens[r] - n, row i sees key k
+ *     k < ctx:   where window_left < 0 or k >= ctx + depth - window_left, depth the number of bits below i
+ *                in the row's mask;
+ *     k >= ctx:  where bit k - ctx of the row's mask is set (tokens past the mask's words are not seen).
  * o [T, Hq, dv]; m, l float32 [Hq, T], contiguous, both or neither NULL.  Slots past
  * kv_lens[r] may hold anything, NaN included.  Codes of NaN among a request's own tokens: of k, they
  * make o and l NaN in every row and head that may attend to the token; of v, those channels of o.  The

@@ -87,9 +87,92 @@ def append(x, slots, codes, scale):
     return codes, scale
 
 
+def tree_set(words):
+    """The rows that a mask names."""
+    return {32 * w + j for w, x in enumerate(np.asarray(words).astype(np.int64) & 0xFFFFFFFF) for j in range(32) if x >> j & 1}
+
+
+def tree_masks(parents, kv_lens, cu_q, words):
+    """(tree [T, words] as int32 bits, positions [T]) for valid inputs."""
+    T = len(parents)
+    tree, pos = np.zeros((T, words), np.int64), np.full(T, -1)
+    for r, L in enumerate(kv_lens):
+        a, b = cu_q[r], cu_q[r + 1]
+        if L == 0:
+            continue
+        for i in range(b - a):
+            p = parents[a + i]
+            if p >= 0:
+                tree[a + i] = tree[a + p]
+            tree[a + i, i // 32] |= 1 << i % 32
+            pos[a + i] = pos[a + p] + 1 if p >= 0 else L - (b - a)
+    return np.where(tree >= 2 ** 31, tree - 2 ** 32, tree).astype(np.int32), pos.astype(np.int32)
+
+
+def keep(codes, scale, paths, kv_lens, cu_q, table):
+    """Tokens paths[r] (ascending indexes of request r's new rows) to the end of its context: (codes, scale)."""
+    old, olds = codes, scale.astype(np.float64)
+    codes, scale = codes.copy(), olds.copy()
+    P, val = codes.shape[2], e4m3_values()
+    for r, path in enumerate(paths):
+        ctx = kv_lens[r] - (cu_q[r + 1] - cu_q[r])
+        where = lambda p: (table[r][p // P], p % P)                                    # noqa: E731
+        for j in range(ctx // P, -(-(ctx + len(path)) // P) if len(path) else 0):
+            page = table[r][j]
+            moves = [(where(ctx + x), i) for i, x in enumerate(path) if (ctx + i) // P == j]
+            front = max(0, ctx - j * P)
+            if not moves:
+                continue
+            for h in range(codes.shape[1]):
+                s = max([olds[p, h] for (p, _), _ in moves] + ([olds[page, h]] if front else []))
+                at = lambda c, o: c if o == s or s == 0 else e4m3_round(val[c] * (o / s))   # noqa: E731
+                codes[page, h, :front] = at(old[page, h, :front], olds[page, h])
+                for (p, t), i in moves:
+                    codes[page, h, (ctx + i) % P] = at(old[p, h, t], olds[p, h])
+                scale[page, h] = s
+    return codes, scale
+
+
+def fork(src, dst, ctx, table, refs, free, count, P):
+    """(copy_src, copy_dst, ctx_out, table, refs, count_out) for valid inputs."""
+    ctx, table, refs = np.array(ctx), np.array(table), np.array(refs)
+    out, copies, wanted, left = ctx.copy(), [], 0, count
+    for s, d in zip(src, dst):
+        need = int(ctx[s] % P > 0)
+        wanted += need
+        pair = (-1, -1)
+        if not need or wanted <= count:
+            full = ctx[s] // P
+            table[d, :full] = table[s, :full]
+            np.add.at(refs, table[s, :full], 1)
+            if need:
+                left -= 1
+                table[d, full] = free[left]
+                pair = (table[s, full], free[left])
+            out[d] = ctx[s]
+        copies.append(pair)
+    a = np.array(copies, np.int64).reshape(-1, 2)
+    return a[:, 0], a[:, 1], out, table, refs, left
+
+
+def release(ctx, keep_lens, table, refs, free, count, P):
+    """(ctx_out, refs, free, count_out) for valid inputs."""
+    refs, free = np.array(refs), np.array(free)
+    for r, (n, k) in enumerate(zip(ctx, keep_lens)):
+        for j in range(-(-k // P), -(-n // P)):
+            refs[table[r][j]] -= 1
+    for page in range(len(refs)):
+        if refs[page] < 0:
+            free[count] = page
+            count += 1
+            refs[page] = 0
+    return np.array(keep_lens), refs, free, count
+
+
 def attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_lens, cu_q, *, causal=True, window=(-1, -1),
-              scale=None, sink=None, heaviest=False):
+              scale=None, sink=None, heaviest=False, tree=None):
     """q [T, Hq, d] float64 over the cache.  Returns (o, m, l); rows behind cu_q[-1] are NaN.
+    tree: [T, words] masks (32 bits each) over a request's own rows.
     heaviest: also the largest softmax weight times v scale of each row, [T, Hq, 1]."""
     T, Hq, d = q.shape
     Hkv, P, dv = k_codes.shape[1], k_codes.shape[2], v_codes.shape[3]
@@ -109,9 +192,13 @@ def attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_lens, cu_q, *, ca
             for t in range(a, b):
                 p = L - (b - a) + (t - a)
                 ok = np.ones(L, bool)
-                if causal:
+                if tree is not None:
+                    first, seen = L - (b - a), tree_set(tree[t])
+                    depth = sum(j < t - a for j in seen)
+                    ok = (key < first) & ((wl < 0) | (key >= first + depth - wl)) | np.isin(key - first, sorted(seen)) & (key >= first)
+                elif causal:
                     ok &= key <= p
-                if wl >= 0:
+                if wl >= 0 and tree is None:
                     ok &= key >= p - wl
                 if wr >= 0:
                     ok &= key <= p + wr

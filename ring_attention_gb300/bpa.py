@@ -75,6 +75,7 @@ class bpa_cache_batch(ctypes.Structure):
         ("scale", ctypes.c_float), ("causal", ctypes.c_int32),
         ("window_left", ctypes.c_int32), ("window_right", ctypes.c_int32),
         ("sink", ctypes.c_void_p),
+        ("tree", ctypes.c_void_p), ("tree_words", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -140,6 +141,12 @@ def lib() -> ctypes.CDLL:
         L.bpa_cache_attn_workspace_size.argtypes, L.bpa_cache_attn_workspace_size.restype = [P, P], sz
         L.bpa_cache_attn.argtypes = [P, P, P, P, P, P, sz, P]
         L.bpa_cache_attn.restype = ctypes.c_int
+        L.bpa_cache_tree.argtypes, L.bpa_cache_tree.restype = [i32, i32, i32, P, P, P, P, P, P, sz, P], ctypes.c_int
+        L.bpa_cache_keep.argtypes = [P, i32, i32, i32, P, i32, P, P, P, P, P, sz, P]
+        L.bpa_cache_keep.restype = ctypes.c_int
+        L.bpa_cache_fork.argtypes, L.bpa_cache_fork.restype = [i32] * 5 + [P] * 12 + [sz, P], ctypes.c_int
+        L.bpa_cache_release.argtypes, L.bpa_cache_release.restype = [i32] * 4 + [P] * 9 + [sz, P], ctypes.c_int
+        L.bpa_cache_copy.argtypes, L.bpa_cache_copy.restype = [P, i32, P, P, P, sz, P], ctypes.c_int
         L.bpa_rope_fwd.argtypes, L.bpa_rope_fwd.restype = [P, P, P, P], ctypes.c_int
         L.bpa_rope_workspace_size.argtypes, L.bpa_rope_workspace_size.restype = [P], sz
         L.bpa_rope_bwd.argtypes, L.bpa_rope_bwd.restype = [P, P, P, P, P, P, P, P, sz, P], ctypes.c_int
@@ -364,7 +371,7 @@ def bpa_debug_wait_timeout(workspace_buf: torch.Tensor, limit_ns: int, stream=No
 # as for torch's own operators, the caller orders it behind the writers of the tensors passed in and in
 # front of the readers of what comes back.
 _CACHE_PACK = struct.Struct("@I7iPP6qPP").pack
-_BATCH_PACK = struct.Struct("@I5iP4qPPPf3iP").pack
+_BATCH_PACK = struct.Struct("@I5iP4qPPPf3iPP2i").pack
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
 _CODES = {torch.bfloat16: BPA_BF16, torch.float32: BPA_FP32}
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
@@ -421,6 +428,31 @@ def _leave(guard, other, dev, outs):
     if other:
         for t in outs:
             t.record_stream(torch.cuda.current_stream(dev))
+
+
+class _call:
+    """One call on device number dev: (stream pointer, workspace) inside, what it makes listed in `made`."""
+
+    def __init__(self, dev, stream, workspace_buf, made):
+        _check_workspace(workspace_buf, dev)
+        self.dev, self.stream, self.ws, self.made = dev, stream, workspace_buf, made
+
+    def __enter__(self):
+        self.guard, ptr, self.other = _enter(self.dev, self.stream)
+        try:
+            if self.ws is None:
+                self.ws = _empty(256, dtype=_U8, device=torch.device("cuda", self.dev))
+        except BaseException:
+            self.__exit__()
+            raise
+        return ptr, self.ws
+
+    def __exit__(self, *_):
+        _leave(self.guard, self.other, self.dev, self.made)
+
+
+def _masks(tree):
+    return 0 if tree is None else tree.data_ptr()
 
 
 def _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype):
@@ -530,7 +562,7 @@ def bpa_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, max_
         _raise_if(st, "bpa_cache_append")
 
 
-def _pack_batch(q, o_row, o_head, page_table, kv_lens, cu_q, max_q, causal, window, scale, sink):
+def _pack_batch(q, o_row, o_head, page_table, kv_lens, cu_q, max_q, causal, window, scale, sink, tree):
     """Packed bpa_cache_batch; o_row, o_head: the output's strides."""
     if q.dim() != 3 or page_table.dim() != 2:
         raise ValueError("q must be [T, Hq, d], page_table [R, max_pages]")
@@ -540,19 +572,25 @@ def _pack_batch(q, o_row, o_head, page_table, kv_lens, cu_q, max_q, causal, wind
     if sink is not None and (sink.dtype is not _F32 or sink.shape != (Hq,) or not sink.is_contiguous() or
                              sink.get_device() != dev):
         raise ValueError("sink must be a contiguous float32 [Hq] tensor on q's device")
+    words = 0
+    if tree is not None:
+        if tree.dtype is not _I32 or tree.dim() != 2 or tree.shape[0] != T or not tree.is_contiguous() or tree.get_device() != dev:
+            raise ValueError("tree must be a contiguous int32 [T, words] tensor on q's device")
+        words = tree.shape[1]
     wl, wr = (-1, -1) if window is None else window
     return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, _int32(max_q, "max_q"), q.data_ptr(), st[0], st[1], o_row, o_head,
                        _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
                        _i32_buffer(cu_q, "cu_q", (R + 1,), dev), 0.0 if scale is None else float(scale),
-                       1 if causal else 0, _int32(wl, "window"), _int32(wr, "window"), 0 if sink is None else sink.data_ptr())
+                       1 if causal else 0, _int32(wl, "window"), _int32(wr, "window"), 0 if sink is None else sink.data_ptr(),
+                       _masks(tree), words, 0)
 
 
 def make_cache_batch(q, page_table, kv_lens, cu_q, *, max_q=0, causal=True, window=(-1, -1), scale=None,
-                     sink=None) -> bpa_cache_batch:
+                     sink=None, tree=None) -> bpa_cache_batch:
     """A bpa_cache_batch (all but o_strides) of the step's tensors (no data is touched); keywords as
     bpa_cache_attn's."""
     return bpa_cache_batch.from_buffer_copy(_pack_batch(q, 0, 0, page_table, kv_lens, cu_q, max_q, causal, window, scale,
-                                                        sink))
+                                                        sink, tree))
 
 
 def bpa_cache_attn_workspace_size(cache: bpa_cache_desc, batch: bpa_cache_batch) -> int:
@@ -560,10 +598,11 @@ def bpa_cache_attn_workspace_size(cache: bpa_cache_desc, batch: bpa_cache_batch)
 
 
 def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, cu_q, *, max_q=0, causal=True,
-                   window=(-1, -1), scale=None, sink=None, o=None, m=None, l=None, workspace_buf=None, stream=None):
+                   window=(-1, -1), scale=None, sink=None, tree=None, o=None, m=None, l=None, workspace_buf=None, stream=None):
     """Attention of packed rows q [T, Hq, d] over the cache.  Returns (o, m, l): o [T, Hq, dv]; m and
     l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  max_q: the most rows of a
-    request (0: unknown, and single tokens then take half as long again), guides the choice of kernel."""
+    request (0: unknown, and single tokens then take half as long again), guides the choice of kernel.
+    tree: int32 [T, words] masks of drafted trees (bpa_cache_tree's, or the caller's)."""
     dtype = q.dtype
     cache, _, d, dv, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)
     if q.dim() != 3 or q.shape[2] != d or q.get_device() != dev:
@@ -574,7 +613,7 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
         if t is not None and (t.dtype is not _F32 or t.shape != stats or not t.is_contiguous() or t.get_device() != dev):
             raise ValueError(f"{name} must be a contiguous float32 [Hq, T] tensor on q's device")
     st = (Hq * dv, dv) if o is None else _rows_strides(o, "o", (T, Hq, dv), dtype, dev)
-    batch = _pack_batch(q, st[0], st[1], page_table, kv_lens, cu_q, max_q, causal, window, scale, sink)
+    batch = _pack_batch(q, st[0], st[1], page_table, kv_lens, cu_q, max_q, causal, window, scale, sink, tree)
     _check_workspace(workspace_buf, dev)
     guard, ptr, other = _enter(dev, stream)
     made = []
@@ -601,6 +640,120 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
     if st:
         _raise_if(st, "bpa_cache_attn")
     return o, m, l
+
+
+def bpa_cache_tree(parents, kv_lens, cu_q, *, words, tree=None, positions=None, workspace_buf=None, stream=None):
+    """Masks of drafted trees: parents [T] names each packed row's parent among its request's rows (-1: the
+    context).  Returns (tree [T, words], positions [T]), int32: a row's own bit and its ancestors', and its place
+    in the sequence.  words: of 32 rows each, for the largest request."""
+    if parents.dim() != 1 or kv_lens.dim() != 1:
+        raise ValueError("parents must be [T], kv_lens [R]")
+    dev, T, R, words = parents.get_device(), parents.shape[0], kv_lens.shape[0], _int32(words, "words")
+    ins = (_i32_buffer(parents, "parents", (T,), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
+           _i32_buffer(cu_q, "cu_q", (R + 1,), dev))
+    if tree is None and not 1 <= words <= 32:
+        raise ValueError(f"words must lie in [1, 32], got {words}")
+    for t, name, shape in ((tree, "tree", (T, words)), (positions, "positions", (T,))):
+        if t is not None:
+            _i32_buffer(t, name, shape, dev)
+    outs, made = [tree, positions], []
+    with _call(dev, stream, workspace_buf, made) as (ptr, ws):
+        for i, shape in enumerate(((T, words), (T,))):
+            if outs[i] is None:
+                outs[i] = _empty(shape, dtype=_I32, device=parents.device)
+                made.append(outs[i])
+        st = lib().bpa_cache_tree(R, T, words, *ins, outs[0].data_ptr(), outs[1].data_ptr(), ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        _raise_if(st, "bpa_cache_tree")
+    return outs[0], outs[1]
+
+
+def bpa_cache_keep(keep, keep_count, kv_lens, cu_q, page_table, k_cache, v_cache, k_scale, v_scale, *, workspace_buf=None,
+                   stream=None):
+    """Keep the accepted tokens keep [R, max_keep] (ascending indexes of a request's new rows, the first
+    keep_count [R] of them) at the end of the context, in place in k_cache, v_cache, k_scale, v_scale.
+    kv_lens, cu_q: of the step that appended them."""
+    cache, _, _, _, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, torch.bfloat16)
+    if keep.dim() != 2 or page_table.dim() != 2:
+        raise ValueError("keep must be [R, max_keep], page_table [R, max_pages]")
+    (R, max_keep), max_pages = keep.shape, page_table.shape[1]
+    ins = (_i32_buffer(keep_count, "keep_count", (R,), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
+           _i32_buffer(cu_q, "cu_q", (R + 1,), dev), _i32_buffer(page_table, "page_table", (R, max_pages), dev))
+    rows = _i32_buffer(keep, "keep", (R, max_keep), dev)
+    with _call(dev, stream, workspace_buf, ()) as (ptr, ws):
+        st = lib().bpa_cache_keep(cache, R, 1 << 30, max_pages, rows, max_keep, *ins, ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        _raise_if(st, "bpa_cache_keep")
+
+
+def bpa_cache_fork(src, dst, ctx_lens, page_table, page_refs, free_pages, free_count, *, page_size, copy_src=None, copy_dst=None,
+                   ctx_lens_out=None, free_count_out=None, workspace_buf=None, stream=None):
+    """Requests dst [N] become holders of what src [N] hold: full pages are shared (page_table and page_refs
+    [num_pages] updated in place), a last page that is not full gets one off the free list.  Returns
+    (copy_src [N], copy_dst [N], ctx_lens_out [R], free_count_out [1]), int32, the first two for
+    bpa_cache_copy.  ctx_lens_out=ctx_lens and free_count_out=free_count update in place."""
+    if src.dim() != 1 or ctx_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("src must be [N], ctx_lens [R], page_table [R, max_pages], free_pages [num_pages]")
+    dev, N, R, page_size = src.get_device(), src.shape[0], ctx_lens.shape[0], _int32(page_size, "page_size")
+    max_pages, num_pages = page_table.shape[1], free_pages.shape[0]
+    ins = (_i32_buffer(src, "src", (N,), dev), _i32_buffer(dst, "dst", (N,), dev), _i32_buffer(ctx_lens, "ctx_lens", (R,), dev),
+           _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(page_refs, "page_refs", (num_pages,), dev),
+           _i32_buffer(free_pages, "free_pages", (num_pages,), dev), _i32_buffer(free_count, "free_count", (1,), dev))
+    outs, shapes, made = [copy_src, copy_dst, ctx_lens_out, free_count_out], ((N,), (N,), (R,), (1,)), []
+    for t, name, shape in zip(outs, ("copy_src", "copy_dst", "ctx_lens_out", "free_count_out"), shapes):
+        if t is not None:
+            _i32_buffer(t, name, shape, dev)
+    with _call(dev, stream, workspace_buf, made) as (ptr, ws):
+        for i in range(4):
+            if outs[i] is None:
+                outs[i] = _empty(shapes[i], dtype=_I32, device=src.device)
+                made.append(outs[i])
+        st = lib().bpa_cache_fork(N, R, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs], ws.data_ptr(),
+                                  ws.numel(), ptr)
+    if st:
+        _raise_if(st, "bpa_cache_fork")
+    return tuple(outs)
+
+
+def bpa_cache_copy(src, dst, k_cache, v_cache, k_scale, v_scale, *, workspace_buf=None, stream=None):
+    """Copy pages src [N] to pages dst [N] with their scales (-1, -1: skipped)."""
+    cache, _, _, _, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, torch.bfloat16)
+    if src.dim() != 1:
+        raise ValueError("src must be [N]")
+    N = src.shape[0]
+    a, b = _i32_buffer(src, "src", (N,), dev), _i32_buffer(dst, "dst", (N,), dev)
+    with _call(dev, stream, workspace_buf, ()) as (ptr, ws):
+        st = lib().bpa_cache_copy(cache, N, a, b, ws.data_ptr(), ws.numel(), ptr)
+    if st:
+        _raise_if(st, "bpa_cache_copy")
+
+
+def bpa_cache_release(ctx_lens, keep_lens, page_table, page_refs, free_pages, free_count, *, page_size, ctx_lens_out=None,
+                      free_count_out=None, workspace_buf=None, stream=None):
+    """Requests of ctx_lens [R] tokens keep the first keep_lens [R]; pages that no request holds any more go
+    to the end of free_pages, ascending (free_pages and page_refs updated in place).  Returns (ctx_lens_out [R],
+    free_count_out [1]); ctx_lens_out=ctx_lens and free_count_out=free_count update in place."""
+    if ctx_lens.dim() != 1 or page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("ctx_lens must be [R], page_table [R, max_pages], free_pages [num_pages]")
+    dev, R, page_size = ctx_lens.get_device(), ctx_lens.shape[0], _int32(page_size, "page_size")
+    max_pages, num_pages = page_table.shape[1], free_pages.shape[0]
+    ins = (_i32_buffer(ctx_lens, "ctx_lens", (R,), dev), _i32_buffer(keep_lens, "keep_lens", (R,), dev),
+           _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(page_refs, "page_refs", (num_pages,), dev),
+           _i32_buffer(free_pages, "free_pages", (num_pages,), dev), _i32_buffer(free_count, "free_count", (1,), dev))
+    outs, shapes, made = [ctx_lens_out, free_count_out], ((R,), (1,)), []
+    for t, name, shape in zip(outs, ("ctx_lens_out", "free_count_out"), shapes):
+        if t is not None:
+            _i32_buffer(t, name, shape, dev)
+    with _call(dev, stream, workspace_buf, made) as (ptr, ws):
+        for i in range(2):
+            if outs[i] is None:
+                outs[i] = _empty(shapes[i], dtype=_I32, device=ctx_lens.device)
+                made.append(outs[i])
+        st = lib().bpa_cache_release(R, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs], ws.data_ptr(),
+                                     ws.numel(), ptr)
+    if st:
+        _raise_if(st, "bpa_cache_release")
+    return tuple(outs)
 
 
 # ---- norms of q and k with the position rotation ---------------------------------------------------
@@ -667,10 +820,6 @@ def make_rope_desc(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=
                                                      q_out, k_out)[0])
 
 
-def _dense(t):
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -692,10 +841,10 @@ def bpa_rope_fwd(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=No
     made = []
     try:
         if q is not None and q_out is None:
-            q_out = _dense(q)
+            q_out = _empty(q.shape, dtype=q.dtype, device=q.device)
             made.append(q_out)
         if k is not None and k_out is None:
-            k_out = _dense(k)
+            k_out = _empty(k.shape, dtype=k.dtype, device=k.device)
             made.append(k_out)
         desc, _ = _pack_rope(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, interleaved, q_out, k_out)
         st = lib().bpa_rope_fwd(desc, _ptr(q_out), _ptr(k_out), ptr)

@@ -15,6 +15,7 @@ namespace bpa {
 // 230.  Pieces of prompts (thousands of rows) take 1,540 us there and 7.1 ms here.
 constexpr int kFewRows = 64;
 constexpr int kPlanMaxR = 8192;      // requests of one plan: their lengths and offsets sit in shared memory
+constexpr int kMaxTreeWords = 32;    // words of a row's mask: 1,024 rows of a request
 
 struct PlanArgs {
     int R, T, P, num_pages, max_pages;
@@ -35,6 +36,50 @@ struct AppendArgs {
     uint32_t* status;
 };
 
+struct TreeArgs {
+    int R, T, words;
+    const int32_t *parents, *kv_lens, *cu_q;
+    uint32_t* tree;                  // [T, words]
+    int32_t* positions;              // [T]
+    uint32_t* status;
+};
+
+struct KeepArgs {
+    int R, T, Hkv, d, dv, P, num_pages, max_pages, max_keep;
+    uint8_t *kc, *vc;
+    int64_t kcs[3], vcs[3];          // (page, head, token) strides
+    float *kscale, *vscale;          // [num_pages, Hkv]
+    const int32_t *table, *kv_lens, *cu_q, *keep, *count;
+    uint32_t* status;
+};
+
+struct ForkArgs {
+    int N, R, P, num_pages, max_pages;
+    const int32_t *src, *dst, *ctx;
+    int32_t *table, *refs;
+    const int32_t *free_pages, *free_count;
+    int32_t *copy_src, *copy_dst, *ctx_out, *count_out;
+    uint32_t* status;
+};
+
+struct ReleaseArgs {
+    int R, P, num_pages, max_pages;
+    const int32_t *ctx, *keep, *table;
+    int32_t *refs, *free_pages;
+    const int32_t* free_count;
+    int32_t *ctx_out, *count_out;
+    uint32_t* status;
+};
+
+struct CopyArgs {
+    int N, Hkv, d, dv, P, num_pages;
+    uint8_t *kc, *vc;
+    int64_t kcs[3], vcs[3];
+    float *kscale, *vscale;
+    const int32_t *src, *dst;
+    uint32_t* status;
+};
+
 struct CacheAttnArgs {
     int dtype, R, T, Hq, Hkv, G, d, dv, P, num_pages, max_pages, max_q;
     float scale;
@@ -48,6 +93,8 @@ struct CacheAttnArgs {
     const float *kscale, *vscale;
     const int32_t *table, *kv_lens, *cu_q;
     const float* sink;
+    const uint32_t* tree;            // [T, tree_words] masks over a request's own rows, or null
+    int tree_words;
     uint32_t* status;
 };
 
@@ -100,10 +147,40 @@ __device__ __forceinline__ void row_keys(const CacheAttnArgs& a, const Req& q, i
     if (a.wr >= 0) hi = static_cast<int>(min(static_cast<int64_t>(hi), static_cast<int64_t>(p) + a.wr));
     if (a.wl >= 0) lo = static_cast<int>(max(static_cast<int64_t>(0), static_cast<int64_t>(p) - a.wl));
 }
+
+// The same under a tree: of the tokens in front of the step's, those from lo on; of the step's own, those whose
+// bit the row's mask has.
+struct TreeRow {
+    int lo, ctx;                     // first key of the window, tokens in front of the step's (may be negative)
+    const uint32_t* bits;
+    int words;
+    __device__ __forceinline__ bool allows(int k) const {
+        if (k < ctx) return k >= lo;
+        const int64_t j = static_cast<int64_t>(k) - ctx;
+        return j < 32 * static_cast<int64_t>(words) && (__ldg(bits + (j >> 5)) >> (j & 31) & 1);
+    }
+};
+__device__ __forceinline__ TreeRow tree_row(const CacheAttnArgs& a, const Req& q, int i) {
+    TreeRow t = {0, q.len - q.n, a.tree + static_cast<int64_t>(q.row0 + i) * a.tree_words, a.tree_words};
+    if (a.wl >= 0) {                 // the row stands as deep as it has ancestors among the step's tokens
+        int depth = 0;
+        for (int w = 0; w < t.words && 32 * w < i; ++w) {
+            const uint32_t before = i - 32 * w >= 32 ? 0xffffffffu : (1u << (i - 32 * w)) - 1;
+            depth += __popc(__ldg(t.bits + w) & before);
+        }
+        t.lo = static_cast<int>(max(static_cast<int64_t>(0), static_cast<int64_t>(t.ctx) + depth - a.wl));
+    }
+    return t;
+}
 #endif
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s);
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_tree(const TreeArgs& a, cudaStream_t s);             // status word clear
+cudaError_t launch_cache_keep(const KeepArgs& a, cudaStream_t s);             // status word clear
+cudaError_t launch_cache_fork(const ForkArgs& a, cudaStream_t s);
+cudaError_t launch_cache_release(const ReleaseArgs& a, cudaStream_t s);
+cudaError_t launch_cache_copy(const CopyArgs& a, cudaStream_t s);
 cudaError_t launch_cache_attn_simt(const CacheAttnArgs& a, cudaStream_t s);   // any shape
 
 // Matrix-instruction kernels for few rows: head dims in steps of 16 up to 256, pages of 16, 32 or a

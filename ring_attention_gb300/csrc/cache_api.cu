@@ -1,6 +1,7 @@
 // cache_api.cu - the C entry points of the paged 8-bit cache (declared in include/bpa.h):
 // argument checks, workspace and launches.
 #include <math.h>
+#include <stddef.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -82,6 +83,19 @@ bpa_status check_cache_pointers(const bpa_cache_desc* c) {
     return BPA_OK;
 }
 
+// A cache that is written: no two pages, heads or tokens over one another for a stride of 0.
+bpa_status check_written(const bpa_cache_desc* c) {
+    const int32_t extents[3] = {c->num_pages, c->Hkv, c->page_size};
+    for (int i = 0; i < 3; ++i)
+        if (extents[i] > 1 && (c->k_cache_strides[i] == 0 || c->v_cache_strides[i] == 0))
+            return fail(BPA_ERR_INVALID_ARG, "a cache that is written needs strides above 0");
+    return BPA_OK;
+}
+
+bpa_status clear_status(void* workspace, cudaStream_t s) {
+    return cuda_status(cudaMemsetAsync(workspace, 0, 2 * sizeof(uint32_t), s), "clearing the status word");
+}
+
 // A cache as a 4-D map (channel, token, head, page) of bytes; false where its layout does not suit TMA
 // (16-byte aligned base, strides in multiples of 16 bytes).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -121,9 +135,17 @@ bpa_status make_attn(const bpa_cache_desc* c, const bpa_cache_batch* b, CacheAtt
     bpa_status st = check_cache(c, dv);
     if (st != BPA_OK) return st;
     if (!b) return fail(BPA_ERR_INVALID_ARG, "batch descriptor is NULL");
-    if (b->struct_size != sizeof(bpa_cache_batch))
+    // a caller of before the tree fields has none
+    const bool trees = b->struct_size == sizeof(bpa_cache_batch);
+    if (!trees && b->struct_size != offsetof(bpa_cache_batch, tree))
         return fail(BPA_ERR_INVALID_ARG, "batch->struct_size is %u, expected %zu", b->struct_size,
                     sizeof(bpa_cache_batch));
+    if (trees && b->reserved) return fail(BPA_ERR_INVALID_ARG, "batch->reserved must be 0");
+    if (trees && b->tree) {
+        if (b->tree_words < 1 || b->tree_words > kMaxTreeWords)
+            return fail(BPA_ERR_INVALID_ARG, "tree_words %d outside [1, %d]", b->tree_words, kMaxTreeWords);
+        if (!b->causal) return fail(BPA_ERR_INVALID_ARG, "a tree needs causal attention");
+    }
     if (b->R < 1 || b->T < 0 || b->T > kMost) return fail(BPA_ERR_INVALID_ARG, "need R >= 1, 0 <= T <= 2^30");
     if (b->Hq < 1 || b->Hq % c->Hkv)
         return fail(BPA_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", b->Hq, c->Hkv);
@@ -168,6 +190,8 @@ bpa_status make_attn(const bpa_cache_desc* c, const bpa_cache_batch* b, CacheAtt
     a.kv_lens = b->kv_lens;
     a.cu_q = b->cu_q;
     a.sink = b->sink;
+    a.tree = trees ? b->tree : nullptr;
+    a.tree_words = trees ? b->tree_words : 0;
     return BPA_OK;
 }
 
@@ -207,10 +231,7 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
         return fail(BPA_ERR_INVALID_ARG, "k, v, their strides or slot_map is NULL");
     for (int i = 0; i < 2; ++i)
         if (k_strides[i] < 0 || v_strides[i] < 0) return fail(BPA_ERR_INVALID_ARG, "strides must be >= 0");
-    const int32_t extents[3] = {cache->num_pages, cache->Hkv, cache->page_size};
-    for (int i = 0; i < 3; ++i)
-        if (extents[i] > 1 && (cache->k_cache_strides[i] == 0 || cache->v_cache_strides[i] == 0))
-            return fail(BPA_ERR_INVALID_ARG, "a cache that is written needs strides above 0");
+    if ((st = check_written(cache)) != BPA_OK) return st;
     if (static_cast<int64_t>(T) * cache->Hkv > kMost)
         return fail(BPA_ERR_UNSUPPORTED, "T * Hkv above 2^30");
     if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
@@ -243,6 +264,131 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
     return cuda_status(launch_cache_append(a, static_cast<cudaStream_t>(stream)), "append launch");
 }
 
+bpa_status bpa_cache_tree(int32_t R, int32_t T, int32_t words, const int32_t* parents, const int32_t* kv_lens,
+                          const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const NvtxRange range("bpa_cache_tree");
+    if (R < 1 || T < 0 || T > kMost) return fail(BPA_ERR_INVALID_ARG, "need R >= 1, 0 <= T <= 2^30");
+    if (words < 1 || words > kMaxTreeWords) return fail(BPA_ERR_INVALID_ARG, "words %d outside [1, %d]", words, kMaxTreeWords);
+    if (!kv_lens || !cu_q || (T && (!parents || !tree)))
+        return fail(BPA_ERR_INVALID_ARG, "a buffer other than positions is NULL");
+    bpa_status st = check_ws(workspace, workspace_bytes, kHeader);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (st != BPA_OK || (st = clear_status(workspace, s)) != BPA_OK || T == 0) return st;
+    const TreeArgs a = {R, T, words, parents, kv_lens, cu_q, tree, positions, static_cast<uint32_t*>(workspace)};
+    return cuda_status(launch_cache_tree(a, s), "tree launch");
+}
+
+bpa_status bpa_cache_keep(const bpa_cache_desc* cache, int32_t R, int32_t T, int32_t max_pages, const int32_t* keep,
+                          int32_t max_keep, const int32_t* keep_count, const int32_t* kv_lens, const int32_t* cu_q,
+                          const int32_t* page_table, void* workspace, size_t workspace_bytes, void* stream) {
+    const NvtxRange range("bpa_cache_keep");
+    int dv = 0;
+    bpa_status st = check_cache(cache, dv);
+    if (st != BPA_OK || (st = check_cache_pointers(cache)) != BPA_OK || (st = check_written(cache)) != BPA_OK) return st;
+    if ((st = check_table(cache->page_size, max_pages)) != BPA_OK) return st;
+    if (R < 1 || T < 0 || T > kMost || max_keep < 0) return fail(BPA_ERR_INVALID_ARG, "need R >= 1, 0 <= T <= 2^30, max_keep >= 0");
+    if (static_cast<int64_t>(R) * cache->Hkv > kMost) return fail(BPA_ERR_UNSUPPORTED, "R * Hkv above 2^30");
+    if ((!keep && max_keep) || !keep_count || !kv_lens || !cu_q || !page_table)
+        return fail(BPA_ERR_INVALID_ARG, "keep, keep_count, kv_lens, cu_q or page_table is NULL");
+    if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = clear_status(workspace, s)) != BPA_OK) return st;
+    KeepArgs a;
+    memset(&a, 0, sizeof a);
+    a.R = R;
+    a.T = T;
+    a.Hkv = cache->Hkv;
+    a.d = cache->d;
+    a.dv = dv;
+    a.P = cache->page_size;
+    a.num_pages = cache->num_pages;
+    a.max_pages = max_pages;
+    a.max_keep = max_keep;
+    a.kc = static_cast<uint8_t*>(cache->k_cache);
+    a.vc = static_cast<uint8_t*>(cache->v_cache);
+    for (int i = 0; i < 3; ++i) {
+        a.kcs[i] = cache->k_cache_strides[i];
+        a.vcs[i] = cache->v_cache_strides[i];
+    }
+    a.kscale = cache->k_scale;
+    a.vscale = cache->v_scale;
+    a.table = page_table;
+    a.kv_lens = kv_lens;
+    a.cu_q = cu_q;
+    a.keep = keep;
+    a.count = keep_count;
+    a.status = static_cast<uint32_t*>(workspace);
+    return cuda_status(launch_cache_keep(a, s), "keep launch");
+}
+
+bpa_status bpa_cache_fork(int32_t N, int32_t R, int32_t page_size, int32_t num_pages, int32_t max_pages, const int32_t* src,
+                          const int32_t* dst, const int32_t* ctx_lens, int32_t* page_table, int32_t* page_refs,
+                          const int32_t* free_pages, const int32_t* free_count, int32_t* copy_src, int32_t* copy_dst,
+                          int32_t* ctx_lens_out, int32_t* free_count_out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const NvtxRange range("bpa_cache_fork");
+    if (R < 1 || N < 0) return fail(BPA_ERR_INVALID_ARG, "need R >= 1, N >= 0");
+    if (R > kPlanMaxR || N > kPlanMaxR) return fail(BPA_ERR_UNSUPPORTED, "%d requests, %d forks: more than %d", R, N, kPlanMaxR);
+    bpa_status st = check_paging(page_size, num_pages);
+    if (st != BPA_OK || (st = check_table(page_size, max_pages)) != BPA_OK) return st;
+    if (!ctx_lens || !page_table || !page_refs || !free_pages || !free_count || !ctx_lens_out || !free_count_out ||
+        (N && (!src || !dst || !copy_src || !copy_dst)))
+        return fail(BPA_ERR_INVALID_ARG, "a buffer is NULL");
+    if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
+    const ForkArgs a = {N, R, page_size, num_pages, max_pages, src, dst, ctx_lens, page_table, page_refs, free_pages,
+                        free_count, copy_src, copy_dst, ctx_lens_out, free_count_out, static_cast<uint32_t*>(workspace)};
+    return cuda_status(launch_cache_fork(a, static_cast<cudaStream_t>(stream)), "fork launch");
+}
+
+bpa_status bpa_cache_release(int32_t R, int32_t page_size, int32_t num_pages, int32_t max_pages, const int32_t* ctx_lens,
+                             const int32_t* keep_lens, const int32_t* page_table, int32_t* page_refs, int32_t* free_pages,
+                             const int32_t* free_count, int32_t* ctx_lens_out, int32_t* free_count_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    const NvtxRange range("bpa_cache_release");
+    if (R < 1) return fail(BPA_ERR_INVALID_ARG, "need R >= 1");
+    if (R > kPlanMaxR) return fail(BPA_ERR_UNSUPPORTED, "%d requests, more than %d", R, kPlanMaxR);
+    bpa_status st = check_paging(page_size, num_pages);
+    if (st != BPA_OK || (st = check_table(page_size, max_pages)) != BPA_OK) return st;
+    if (!ctx_lens || !keep_lens || !page_table || !page_refs || !free_pages || !free_count || !ctx_lens_out || !free_count_out)
+        return fail(BPA_ERR_INVALID_ARG, "a buffer is NULL");
+    if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
+    const ReleaseArgs a = {R, page_size, num_pages, max_pages, ctx_lens, keep_lens, page_table, page_refs, free_pages,
+                           free_count, ctx_lens_out, free_count_out, static_cast<uint32_t*>(workspace)};
+    return cuda_status(launch_cache_release(a, static_cast<cudaStream_t>(stream)), "release launch");
+}
+
+bpa_status bpa_cache_copy(const bpa_cache_desc* cache, int32_t N, const int32_t* src, const int32_t* dst, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    const NvtxRange range("bpa_cache_copy");
+    int dv = 0;
+    bpa_status st = check_cache(cache, dv);
+    if (st != BPA_OK || (st = check_cache_pointers(cache)) != BPA_OK || (st = check_written(cache)) != BPA_OK) return st;
+    if (N < 0 || (N && (!src || !dst))) return fail(BPA_ERR_INVALID_ARG, "need N >= 0, src and dst");
+    if (static_cast<int64_t>(N) * cache->Hkv > kMost / 2) return fail(BPA_ERR_UNSUPPORTED, "N * Hkv above 2^29");
+    if ((st = check_ws(workspace, workspace_bytes, kHeader)) != BPA_OK) return st;
+    CopyArgs a;
+    memset(&a, 0, sizeof a);
+    a.N = N;
+    a.Hkv = cache->Hkv;
+    a.d = cache->d;
+    a.dv = dv;
+    a.P = cache->page_size;
+    a.num_pages = cache->num_pages;
+    a.kc = static_cast<uint8_t*>(cache->k_cache);
+    a.vc = static_cast<uint8_t*>(cache->v_cache);
+    for (int i = 0; i < 3; ++i) {
+        a.kcs[i] = cache->k_cache_strides[i];
+        a.vcs[i] = cache->v_cache_strides[i];
+    }
+    a.kscale = cache->k_scale;
+    a.vscale = cache->v_scale;
+    a.src = src;
+    a.dst = dst;
+    a.status = static_cast<uint32_t*>(workspace);
+    return cuda_status(launch_cache_copy(a, static_cast<cudaStream_t>(stream)), "copy launch");
+}
+
 size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cache_batch* batch) {
     CacheAttnArgs a;
     if (make_attn(cache, batch, a) != BPA_OK) return 0;
@@ -266,7 +412,7 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
     a.l = l;
     a.status = static_cast<uint32_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a.T > 0 && cache_attn_mma_supported(a)) {
+    if (a.T > 0 && !a.tree && cache_attn_mma_supported(a)) {
         const CacheBox box = cache_attn_mma_box(a);
         CUtensorMap maps[2];
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&

@@ -6,10 +6,9 @@
 // scale if it grew, and the run's rows are rounded to e4m3 once.  Powers of two make a move exact
 // except below e4m3's smallest normal number (2^-6 of the new scale), where it rounds again: at most
 // 2^-10 of the scale, half of e4m3's smallest step, per doubling.
-#include <cuda_fp8.h>
-
 #include "cache.h"
 #include "common.cuh"
+#include "e4m3.cuh"
 
 namespace bpa {
 namespace {
@@ -40,14 +39,6 @@ BPA_DEV void load_row(const __nv_bfloat16* p, uint32_t (&v)[VE]) {
             v[2 * i + 1] = w[i] & 0xffff0000u;
         }
     }
-}
-
-// round to nearest even; |x| <= 448 here, NaN gives NaN, infinities 448
-BPA_DEV uint32_t e4m3_pair(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-BPA_DEV float from_e4m3(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
 
 // The smallest power of two s >= 2^-100 with amax <= 448 s = 1.75 * 2^8 s; 0 for amax = 0.  From the
@@ -156,11 +147,7 @@ __global__ void __launch_bounds__(128) k_cache_append(const AppendArgs a) {
                         } else {
                             uint32_t* q = reinterpret_cast<uint32_t*>(p);
 #pragma unroll
-                            for (int k = 0; k < VE / 4; ++k) {
-                                const uint32_t y = q[k];
-                                q[k] = e4m3_pair(from_e4m3(y & 0xff) * ratio, from_e4m3((y >> 8) & 0xff) * ratio) |
-                                       e4m3_pair(from_e4m3((y >> 16) & 0xff) * ratio, from_e4m3(y >> 24) * ratio) << 16;
-                            }
+                            for (int k = 0; k < VE / 4; ++k) q[k] = rescaled4(q[k], ratio);
                         }
                     }
         }

@@ -42,7 +42,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_attn_simt(const CacheAttn
     const Req rq = request_of(a, r);
     if (rq.bad && threadIdx.x == 0) report(a.status, ST_CHECK, 0xCC1);
     int k0, k1;
-    row_keys(a, rq, t - rq.row0, k0, k1);
+    TreeRow tree = {};
+    if (a.tree) {
+        tree = tree_row(a, rq, t - rq.row0);
+        k0 = min(tree.lo, max(tree.ctx, 0));
+        k1 = rq.len - 1;
+    } else {
+        row_keys(a, rq, t - rq.row0, k0, k1);
+    }
     const E* q = static_cast<const E*>(a.q) + t * a.qs[0] + h * a.qs[1];
     for (int j = threadIdx.x; j < a.d; j += kWarps * 32) s_q[j] = load_f32(q + j);
     __syncthreads();
@@ -54,7 +61,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache_attn_simt(const CacheAttn
         const int key = static_cast<int>(base) + lane;
         float z = -INFINITY, vscale = 0.f;
         int64_t at = -1;                  // the key's row of v, -1: none
-        if (key <= k1) {
+        if (key <= k1 && (!a.tree || tree.allows(key))) {
             const int pg = key / a.P, off = key - pg * a.P, id = __ldg(table + pg);
             if (id >= 0 && id < a.num_pages) {
                 const uint8_t* k = a.kc + id * a.kcs[0] + hk * a.kcs[1] + off * a.kcs[2];
