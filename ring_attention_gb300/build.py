@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libbpa.so")
 
 SOURCES = ["fwd_tc.cu", "fwd_tc_drop.cu", "fwd_band.cu", "api.cu", "simt.cu", "aux.cu", "bwd_tc.cu", "select.cu", "gather.cu",
            "noalloc.cu", "cache_api.cu", "cache_plan.cu", "cache_append.cu", "cache_attn.cu",
-           "cache_attn_mma.cu", "cache_attn_tc.cu", "cache_tree.cu",
+           "cache_attn_mma.cu", "cache_attn_mma_tree.cu", "cache_attn_tc.cu", "cache_tree.cu",
            "cache_keep.cu", "cache_pages.cu", "rope.cu", "rope_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

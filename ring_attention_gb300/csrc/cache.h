@@ -172,6 +172,12 @@ __device__ __forceinline__ TreeRow tree_row(const CacheAttnArgs& a, const Req& q
     }
     return t;
 }
+// Keys [lo, hi] that hold whatever the rows of a request see under a tree (empty: lo > hi).
+__device__ __forceinline__ void tree_span(const CacheAttnArgs& a, const Req& q, int& lo, int& hi) {
+    const int ctx = max(q.len - q.n, 0);
+    lo = a.wl >= 0 ? static_cast<int>(max(static_cast<int64_t>(0), static_cast<int64_t>(ctx) - a.wl)) : 0;
+    hi = q.len - 1;
+}
 #endif
 
 cudaError_t launch_cache_plan(const PlanArgs& a, cudaStream_t s);

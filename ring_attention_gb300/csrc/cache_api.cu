@@ -412,13 +412,13 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
     a.l = l;
     a.status = static_cast<uint32_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a.T > 0 && !a.tree && cache_attn_mma_supported(a)) {
+    if (a.T > 0 && cache_attn_mma_supported(a)) {
         const CacheBox box = cache_attn_mma_box(a);
         CUtensorMap maps[2];
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&
             make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows, true)) {
             uint32_t* far = nullptr;
-            if (cache_attn_tc_takes(a)) {               // requests of many rows first
+            if (!a.tree && cache_attn_tc_takes(a)) {               // requests of many rows first
                 far = cache_attn_far(static_cast<uint8_t*>(workspace));
                 const size_t used = reinterpret_cast<uint8_t*>(far + a.R) - static_cast<uint8_t*>(workspace);
                 st = cuda_status(cudaMemsetAsync(workspace, 0, used, s), "clearing the status word and the marks");
