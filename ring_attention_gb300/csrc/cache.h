@@ -208,6 +208,8 @@ uint32_t* cache_attn_far(uint8_t* ws);      // the marks' place, [R]
 // the requests whose v scales lie too far apart for it, whatever it has written for them.
 bool cache_attn_tc_takes(const CacheAttnArgs& a);       // supported, and there may be enough such requests
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a);      // plain (not swizzled) boxes
-cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, cudaStream_t s);
+// ws: of trees, cache_attn_tc_workspace bytes
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, uint8_t* ws, cudaStream_t s);
+size_t cache_attn_tc_workspace(const CacheAttnArgs& a);
 
 }  // namespace bpa

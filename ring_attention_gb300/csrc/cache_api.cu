@@ -195,6 +195,10 @@ bpa_status make_attn(const bpa_cache_desc* c, const bpa_cache_batch* b, CacheAtt
     return BPA_OK;
 }
 
+size_t attn_workspace(const CacheAttnArgs& a) {
+    return cache_attn_mma_workspace(a) + (cache_attn_mma_supported(a) ? cache_attn_tc_workspace(a) : 0);
+}
+
 }  // namespace
 
 extern "C" {
@@ -392,7 +396,7 @@ bpa_status bpa_cache_copy(const bpa_cache_desc* cache, int32_t N, const int32_t*
 size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cache_batch* batch) {
     CacheAttnArgs a;
     if (make_attn(cache, batch, a) != BPA_OK) return 0;
-    return cache_attn_mma_workspace(a);
+    return attn_workspace(a);
 }
 
 bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* batch, void* o, float* m, float* l,
@@ -406,7 +410,7 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
     if (!m != !l) return fail(BPA_ERR_INVALID_ARG, "m and l: both or neither");
     if ((a.T > 1 && a.os[0] == 0) || (a.Hq > 1 && a.os[1] == 0))
         return fail(BPA_ERR_INVALID_ARG, "o_strides must be above 0: rows of o would lie over one another");
-    if ((st = check_ws(workspace, workspace_bytes, cache_attn_mma_workspace(a))) != BPA_OK) return st;
+    if ((st = check_ws(workspace, workspace_bytes, attn_workspace(a))) != BPA_OK) return st;
     a.o = o;
     a.m = m;
     a.l = l;
@@ -418,7 +422,7 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&
             make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows, true)) {
             uint32_t* far = nullptr;
-            if (!a.tree && cache_attn_tc_takes(a)) {               // requests of many rows first
+            if (cache_attn_tc_takes(a)) {               // requests of many rows first
                 far = cache_attn_far(static_cast<uint8_t*>(workspace));
                 const size_t used = reinterpret_cast<uint8_t*>(far + a.R) - static_cast<uint8_t*>(workspace);
                 st = cuda_status(cudaMemsetAsync(workspace, 0, used, s), "clearing the status word and the marks");
@@ -428,7 +432,7 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
                 if (!make_cache_map(&raw[0], a.kc, a, a.d, a.kcs, plain.cols_k, plain.rows, false) ||
                     !make_cache_map(&raw[1], a.vc, a, a.dv, a.vcs, plain.cols_v, plain.rows, false))
                     return fail(BPA_ERR_CUDA, "cache attention: no tensor map");
-                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, far, s), "cache attention launch");
+                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, far, static_cast<uint8_t*>(workspace) + cache_attn_mma_workspace(a), s), "cache attention launch");
                 if (st != BPA_OK) return st;
             }
             return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), far, s),

@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "cache.h"
+#include "cache_attn_mma.cuh"
 #include "common.cuh"
 
 namespace bpa {
@@ -62,7 +63,13 @@ struct TileMeta {
 struct Item {
     int valid, row0, n, len, hk, i0, first, tiles;   // first key tile, tiles
     float lv0;
-    int pad[3];
+    int slot, alt, pad;               // trees: place of a piece (-1: a whole item), even and odd key tiles apart
+};
+using cache_mma::Rec;
+struct Pieces {                       // of trees
+    Rec* recs;                        // [CTAs]
+    float2* ml;                       // [2 CTAs][kRows] (m in log2 units, l)
+    float* part;                      // [2 CTAs][kRows][DV] relative to m
 };
 
 template <int D, int DV>
@@ -79,7 +86,7 @@ struct Cfg {
     static constexpr int B_Q = 0, B_KF = 2, B_KE = B_KF + NS, B_VF = B_KE + NS, B_VE = B_VF + NS, B_S = B_VE + NS,
                          B_P = B_S + 2, B_O = B_P + 2, B_OE = B_O + 2, B_MF = B_OE + 2, B_ME = B_MF + kMetas,
                          B_IF = B_ME + kMetas, B_IE = B_IF + 2, B_RF = B_IE + 2, B_RE = B_RF + 2, B_PAIR = B_RE + 2,
-                         B_FIN = B_PAIR + 8, NBAR = B_FIN + 1;
+                         B_FIN = B_PAIR + 8, B_X = B_FIN + 1, NBAR = B_X + 1;
     static constexpr int SMEM = 1024 + OFF_BAR + 8 * NBAR + 16;
     static_assert(SMEM <= 232448, "shared memory");
     static constexpr uint32_t F16 = 1u << 4;                     // float32 sums, both operands fp16
@@ -113,15 +120,21 @@ BPA_DEV uint32_t nan_or_0(uint32_t four) { return __vcmpeq4(four & 0x7f7f7f7fu, 
 
 // This thread's 64 scores of its row (columns c0 ..).  Rolled loops over 32 columns: the roles' code
 // together has to stay in the instruction caches (unrolled, the warps spent two fifths of their time
-// waiting for instructions).  EDGE: keys outside [kmin, kmax] are masked.
+// waiting for instructions).  EDGE 1: keys outside [kmin, kmax] are masked; 2 (trees): those whose bit of `seen` is not set.
+enum { E_NONE = 0, E_RANGE = 1, E_BITS = 2 };
+template <int EDGE>
+BPA_DEV bool masked(int k, int kmin, int kmax, uint32_t seen, int bit) {
+    return EDGE == E_RANGE ? k < kmin || k > kmax : !(seen >> bit & 1);
+}
 
 // The maxima of u and x.
-template <bool EDGE>
-BPA_DEV void maxima(uint32_t tS, const TileMeta* mt, int c0, float f_row, int k0, int kmin, int kmax, float& umax, float& xmax) {
+template <int EDGE>
+BPA_DEV void maxima(uint32_t tS, const TileMeta* mt, int c0, float f_row, int k0, int kmin, int kmax, uint64_t seen, float& umax, float& xmax) {
     umax = xmax = -INFINITY;
 #pragma unroll 1
     for (int c = c0; c < c0 + 64; c += 32) {
         uint32_t s[32];
+        const uint32_t bits = static_cast<uint32_t>(seen >> (c - c0));
         tmem_ld32(tS + c, s);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -132,8 +145,8 @@ BPA_DEV void maxima(uint32_t tS, const TileMeta* mt, int c0, float f_row, int k0
                 float s0 = __uint_as_float(s[16 * h + i]), s1 = __uint_as_float(s[16 * h + i + 1]);
                 if (EDGE) {
                     const int k = k0 + c + 16 * h + i;
-                    s0 = k < kmin || k > kmax ? -INFINITY : s0 * a;
-                    s1 = k + 1 < kmin || k + 1 > kmax ? -INFINITY : s1 * a;
+                    s0 = masked<EDGE>(k, kmin, kmax, bits, 16 * h + i) ? -INFINITY : s0 * a;
+                    s1 = masked<EDGE>(k + 1, kmin, kmax, bits, 16 * h + i + 1) ? -INFINITY : s1 * a;
                 }
                 mx = fmax3(mx, s0, s1);
             }
@@ -145,12 +158,13 @@ BPA_DEV void maxima(uint32_t tS, const TileMeta* mt, int c0, float f_row, int k0
 }
 
 // The weights as fp16 pairs over the scores (columns c0 .. c0 + 31); returns their sum of W e.
-template <bool EDGE>
-BPA_DEV float weights(uint32_t tS, const TileMeta* mt, int c0, float f_row, float mref, int k0, int kmin, int kmax) {
+template <int EDGE>
+BPA_DEV float weights(uint32_t tS, const TileMeta* mt, int c0, float f_row, float mref, int k0, int kmin, int kmax, uint64_t seen) {
     float sum = 0.f;
 #pragma unroll 1
     for (int cc = 0; cc < 2; ++cc) {
         const int c = c0 + 32 * cc;
+        const uint32_t bits = static_cast<uint32_t>(seen >> (32 * cc));
         uint32_t s[32], pk[16];
         tmem_ld32(tS + c, s);
 #pragma unroll
@@ -164,8 +178,8 @@ BPA_DEV float weights(uint32_t tS, const TileMeta* mt, int c0, float f_row, floa
                 f2_unpack(ffma2(f2_pack(__uint_as_float(s[16 * h + 2 * i]), __uint_as_float(s[16 * h + 2 * i + 1])), a2, b2), y0, y1);
                 if (EDGE) {
                     const int k = k0 + c + 16 * h + 2 * i;
-                    y0 = k < kmin || k > kmax ? -INFINITY : y0;
-                    y1 = k + 1 < kmin || k + 1 > kmax ? -INFINITY : y1;
+                    y0 = masked<EDGE>(k, kmin, kmax, bits, 16 * h + 2 * i) ? -INFINITY : y0;
+                    y1 = masked<EDGE>(k + 1, kmin, kmax, bits, 16 * h + 2 * i + 1) ? -INFINITY : y1;
                 }
                 const float w0 = ex2(y0), w1 = ex2(y1);
                 r2 = fadd2(r2, f2_pack(w0, w1));
@@ -181,9 +195,52 @@ BPA_DEV float weights(uint32_t tS, const TileMeta* mt, int c0, float f_row, floa
     return sum;
 }
 
-template <int D, int DV>
+// Trees: which of the 64 keys from k0 on the row sees.
+BPA_DEV uint64_t seen_from(const TreeRow& t, int k0, int len) {
+    auto ones = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+    auto word = [&](int w) { return w < t.words ? __ldg(t.bits + w) : 0u; };
+    if (k0 >= len) return 0;
+    uint64_t seen = ones(t.ctx - k0) & ~ones(t.lo - k0);      // in front of the step's tokens
+    const int j = k0 - t.ctx;                                 // of the step's tokens, the first here
+    if (j >= 0) {
+        const int w = j >> 5;
+        const uint32_t a = word(w), b = word(w + 1), c = word(w + 2);
+        seen = __funnelshift_r(a, b, j & 31) | static_cast<uint64_t>(__funnelshift_r(b, c, j & 31)) << 32;
+    } else if (j > -64) {
+        seen |= (word(0) | static_cast<uint64_t>(word(1)) << 32) << -j;
+    }
+    return seen & ones(len - k0);
+}
+
+// Trees: items are cut between CTAs.  Each takes an equal share of the cost of all items (a key tile counts what its
+// rows take, an item's start and end kExtra), as in the kernel for few rows, and leaves pieces of items
+// for the same join.  An item of up to 128 rows has its even key tiles on one row tile and its odd ones on the other, the same rows on
+// both, so that all warps work; they are added up at its end.
+constexpr int kTwo = 4, kAlt = 3, kExtra = 8;
+struct Cut {                          // of an item: first key tile, tiles (at least one), what a tile counts for
+    int first, n, each;
+    bool keys;                        // no: the one tile is none
+    BPA_DEV int cost() const { return n * each + kExtra; }
+    BPA_DEV int within(long long c) const { return c <= kExtra ? 0 : (static_cast<int>(c) - kExtra) / each; }
+};
+BPA_DEV Cut cut_of(const CacheAttnArgs& a, const Req& q, int g) {
+    int lo, hi;
+    tree_span(a, q, lo, hi);
+    const int each = q.n * a.G - g * kRows > 128 ? kTwo : kAlt;
+    if (lo > hi) return {0, 1, each, false};
+    return {lo / BN, hi / BN - lo / BN + 1, each, true};
+}
+BPA_DEV long long cost_of(const CacheAttnArgs& a, const Req& q) {
+    const int groups = groups_of(a, q);
+    if (groups == 0) return 0;
+    return ((groups - 1) * static_cast<long long>(cut_of(a, q, 0).cost()) + cut_of(a, q, groups - 1).cost()) * a.Hkv;
+}
+
+// TREE: of the kernel's CTAs, what the join of their pieces reads; otherwise empty.
+template <int D, int DV, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_constant__ CUtensorMap tmK,
-    const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a, uint32_t* counter, uint32_t* far, int vec_q, int vec_o) {
+    const __grid_constant__ CUtensorMap tmV, const CacheAttnArgs a, uint32_t* counter, uint32_t* far, int vec_q, int vec_o,
+    const Pieces pieces) {
     using C = Cfg<D, DV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -219,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
         }
         for (int i = 0; i < 8; ++i) mbar_init(BAR(C::B_PAIR + i), 2);
         mbar_init(BAR(C::B_FIN), 1);
+        mbar_init(BAR(C::B_X), 16);            // the softmax warps
         *abort = 0;
         fence_mbar_init();
     }
@@ -297,14 +355,113 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     mbar_arrive(BAR(C::B_MF + t % kMetas));
                 }
             };
+            // trees: this CTA's share of the cost of all items, and its pieces one after the other
+            struct {
+                int r, hk, g, groups;
+                Req rq;
+                long long total, at, off, left;
+                int parts;
+                bool first;
+                Rec rec;
+            } own = {};
+            if (TREE) {
+                long long total = 0;
+                for (int r = lane; r < a.R; r += 32) total += cost_of(a, request_of(a, r));
+#pragma unroll
+                for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+                const int ctas = gridDim.x, cta = blockIdx.x;
+                // a share is at least a tile among the CTAs that take part, so the pieces of an item lie side by side
+                own.parts = static_cast<int>(min(total / kTwo, static_cast<long long>(ctas)));
+                own.total = total;
+                const long long begin = cta < own.parts ? cache_mma::share(total, cta, own.parts) : total;
+                own.left = (cta < own.parts ? cache_mma::share(total, cta + 1, own.parts) : total) - begin;
+                own.at = begin;
+                own.first = true;
+                long long before = 0;
+                for (int base = 0; own.left > 0 && base < a.R; base += 32) {
+                    const long long c = base + lane < a.R ? cost_of(a, request_of(a, base + lane)) : 0;
+                    long long x = c;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                        if (lane >= o) x += y;
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, begin < before + x);
+                    if (hit) {
+                        const int src = __ffs(hit) - 1;
+                        own.r = base + src;
+                        own.off = begin - before - __shfl_sync(0xffffffffu, x - c, src);
+                        break;
+                    }
+                    before += __shfl_sync(0xffffffffu, x, 31);
+                }
+                if (own.left > 0) {
+                    own.rq = request_of(a, own.r);
+                    own.groups = groups_of(a, own.rq);
+                    const long long per_head = cost_of(a, own.rq) / a.Hkv;
+                    own.hk = static_cast<int>(own.off / per_head);
+                    own.off -= own.hk * per_head;
+                    while (own.g + 1 < own.groups && own.off >= cut_of(a, own.rq, own.g).cost()) own.off -= cut_of(a, own.rq, own.g++).cost();
+                }
+            }
+            // the next piece: key tiles [t0, t1) of item (own.r, own.hk, g)
+            auto next_piece = [&](int& g, int& t0, int& t1, int& slot, Cut& cut) {
+                while (own.left > 0) {
+                    if (!own.first && ++own.g == own.groups) {
+                        own.g = 0;
+                        if (++own.hk == a.Hkv) {
+                            own.hk = 0;
+                            do {
+                                if (++own.r >= a.R) {      // only if the lengths changed during the call
+                                    if (lane == 0) report(a.status, ST_CHECK, 0xCE5);
+                                    own.left = 0;
+                                    return false;
+                                }
+                                own.rq = request_of(a, own.r);
+                                own.groups = groups_of(a, own.rq);
+                            } while (own.groups == 0);
+                        }
+                    }
+                    own.first = false;
+                    cut = cut_of(a, own.rq, own.g);
+                    const long long off = own.off, to = min(static_cast<long long>(cut.cost()), off + own.left);
+                    g = own.g;
+                    t0 = cut.within(off);
+                    t1 = cut.within(to);
+                    const bool lead = t0 > 0, trail = t1 < cut.n;
+                    slot = lead ? 2 * static_cast<int>(blockIdx.x) : trail ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+                    if (t0 < t1 && trail && !lead) {
+                        // its pieces: up to the last CTA c with total c / parts < the end of the item's cost
+                        const long long at_end = own.at + (cut.cost() - off);
+                        own.rec.trail = static_cast<int>((at_end * own.parts + own.total - 1) / own.total) - blockIdx.x;
+                        own.rec.row0 = own.rq.row0;
+                        own.rec.hk = own.hk;
+                        own.rec.i0 = g * kRows;
+                        own.rec.nrows = min(own.rq.n * a.G - g * kRows, kRows);
+                    }
+                    own.left -= to - off;
+                    own.at += to - off;
+                    own.off = 0;
+                    if (t0 < t1) return true;
+                }
+                return false;
+            };
             for (int k = 0;; ++k) {
                 if (k >= 2 && !wait(C::B_IE + (k & 1), (k >> 1) - 1, 0xE5)) break;
+                Req rq = {};
+                int r = -1, groups = 0;
                 uint32_t idx = 0;
+                int g = 0, t0 = 0, t1 = 0, slot = -1;
+                Cut cut = {};
+                if (TREE) {
+                    if (next_piece(g, t0, t1, slot, cut)) {
+                        r = own.r;
+                        rq = own.rq;
+                    }
+                } else {
                 if (lane == 0) idx = atomicAdd(counter, 1u);
                 idx = __shfl_sync(0xffffffffu, idx, 0);
                 // the item's request: a running sum over the requests, 32 at a time
-                Req rq = {};
-                int r = -1, groups = 0;
                 for (int base = 0; base < a.R; base += 32) {
                     Req q = {};
                     if (base + lane < a.R) q = request_of(a, base + lane);
@@ -330,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     }
                     idx -= __shfl_sync(0xffffffffu, x, 31);
                 }
+                }
                 Item* it = items + (k & 1);
                 if (r < 0) {
                     if (lane == 0) {
@@ -339,12 +497,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     break;
                 }
                 if (rq.bad && lane == 0) report(a.status, ST_CHECK, 0xCE1);
-                const int hk = idx % a.Hkv, i0 = (groups - 1 - static_cast<int>(idx / a.Hkv)) * kRows;   // last rows first
-                const int last = min(rq.n * a.G, i0 + kRows) - 1;
-                int lo, hi, y;
-                row_keys(a, rq, i0 / a.G, lo, y);
-                row_keys(a, rq, last / a.G, y, hi);
-                const int first = lo <= hi ? lo / BN : 0, tiles = lo <= hi ? hi / BN - first + 1 : 0;
+                const int hk = TREE ? own.hk : idx % a.Hkv;
+                const int i0 = (TREE ? g : groups - 1 - static_cast<int>(idx / a.Hkv)) * kRows;   // last rows first
+                int first, tiles;
+                if (TREE) {
+                    first = cut.first + t0;
+                    tiles = cut.keys ? t1 - t0 : 0;
+                } else {
+                    const int last = min(rq.n * a.G, i0 + kRows) - 1;
+                    int lo, hi, y;
+                    row_keys(a, rq, i0 / a.G, lo, y);
+                    row_keys(a, rq, last / a.G, y, hi);
+                    first = lo <= hi ? lo / BN : 0;
+                    tiles = lo <= hi ? hi / BN - first + 1 : 0;
+                }
                 // lanes 0..7: 16 keys each; a tile's page ids are asked for two tiles ahead, its scales one
                 const int32_t* table = a.table + static_cast<int64_t>(r) * a.max_pages;
                 auto there = [&](int j) { return lane < 8 && j < tiles && (first + j) * BN + 16 * lane < rq.len; };
@@ -365,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 const unsigned some = __ballot_sync(0xffffffffu, vs > 0.f);
                 const float lv0 = some ? __log2f(__shfl_sync(0xffffffffu, vs, __ffs(some) - 1)) : 0.f;
                 if (lane == 0) {
-                    *it = {1, rq.row0, rq.n, rq.len, hk, i0, first, tiles, lv0, {}};
+                    *it = {1, rq.row0, rq.n, rq.len, hk, i0, first, tiles, lv0, slot, TREE && rq.n * a.G - i0 <= 128, 0};
                     mbar_arrive(BAR(C::B_IF + (k & 1)));
                 }
                 bool ok = true;
@@ -425,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     for (int p = t - 1; p <= t; ++p) mbar_wait(BAR(C::B_RF + kv), p & 1, &never, a.status, 0xEF);
             }
             publish_end();
+            if (TREE && lane == 0) pieces.recs[blockIdx.x] = own.rec;
         } else if (warp == kMma) {
             // -------------------------------------------------------- MMA issuer
             int t = 0, np[2] = {0, 0}, seen[2] = {0, 0};   // key tiles; W tiles used, items with work, per row tile
@@ -454,6 +621,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         tc_mma_ts_w(tmem + 256 + i * 128, tmem + i * BN + kk * 8 + (kk >> 2) * 32, sdesc_advance(vd, kk * 2048), C::IDESC_PV,
                                     (!first || kk > 0) ? 1u : 0u);
                 };
+                if (TREE && it.alt) {
+                    // key tile j on row tile j & 1, two of them under way
+                    const int both = it.tiles > 1 ? 2 : 1;
+                    for (int i = 0; ok && i < both; ++i) {
+                        ok = wait(C::B_Q + i, seen[i], 0xE8) && wait(C::B_KF + (t + i) % C::NS, (t + i) / C::NS, 0xE9);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(i, t + i);
+                    }
+                    for (int j = 0; ok && j < it.tiles; ++j, ++t) {
+                        const int i = j & 1;
+                        if (!(ok = wait(C::B_VF + t % C::NS, t / C::NS, 0xEA) && wait(C::B_P + i, np[i], 0xEB))) break;
+                        if (j < 2 && seen[i] > 0 && !(ok = wait(C::B_OE + i, seen[i] - 1, 0xEC))) break;
+                        ++np[i];
+                        tc_commit_w(BAR(C::B_KE + t % C::NS));     // S(j) is complete
+                        tc_fence_after();
+                        issue_pv(i, t, j < 2);
+                        if (j + 2 >= it.tiles) tc_commit_w(BAR(C::B_O + i));
+                        if (j + 2 < it.tiles) {
+                            if (!(ok = wait(C::B_KF + t % C::NS, t / C::NS + 1, 0xED))) break;
+                            tc_fence_after();
+                            issue_s(i, t + 2);
+                        }
+                        tc_commit_w(BAR(C::B_VE + t % C::NS));
+                    }
+                    for (int i = 0; i < both; ++i) ++seen[i];
+                    continue;
+                }
                 for (int i = 0; ok && i < two; ++i) ok = wait(C::B_Q + i, seen[i], 0xE8);
                 ok = ok && wait(C::B_KF + t % C::NS, t / C::NS, 0xE9);
                 if (!ok) break;
@@ -503,6 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             if (lane == 0) mbar_arrive(BAR(C::B_PAIR + pair));
             return wait(C::B_PAIR + pair, meets++, 0xF4);
         };
+        int xs = 0;
+        auto meet_all = [&]() {        // all sixteen softmax warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(C::B_X));
+            return wait(C::B_X, xs++, 0xF5);
+        };
         int t = 0, cs = 0, seen = 0;   // key tiles, S tiles and items with work of this row tile
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -511,11 +712,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_IE + (k & 1)));
             if (!it.valid) break;
-            const int rows = it.n * a.G, ri = it.i0 + qt * 128 + row;
-            const bool there = ri < rows, busy = it.i0 + qt * 128 < rows;     // busy: the tile has rows
+            const bool alt = TREE && it.alt;
+            const int rows = it.n * a.G, ri = it.i0 + (alt ? 0 : qt * 128) + row;
+            // busy: the tile has rows (and key tiles of its own)
+            const bool there = ri < rows, busy = alt ? qt < it.tiles : it.i0 + qt * 128 < rows;
             const int tok = there ? ri / a.G : 0, head = it.hk * a.G + (there ? ri - tok * a.G : 0);
             int kmin = 0, kmax = INT_MAX;      // a row that is not there masks nothing (q = 0)
-            if (there) row_keys(a, Req{it.row0, it.n, it.len, false}, tok, kmin, kmax);
+            TreeRow tr = {};
+            if (there && TREE) {
+                tr = tree_row(a, Req{it.row0, it.n, it.len, false}, tok);
+                kmin = tr.lo;
+                kmax = tr.ctx - 1;     // every key from kmin to kmax is seen
+            } else if (there) {
+                row_keys(a, Req{it.row0, it.n, it.len, false}, tok, kmin, kmax);
+            }
             float f_row = 1.f;
             if (busy && it.tiles) {
                 // ---- the row of q as fp16, its largest value scaled into [2^7, 2^8): all of it for the
@@ -574,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             for (int j = 0; j < it.tiles; ++j, ++t) {
                 const int sl = t % kMetas, k0 = (it.first + j) * BN;
                 if (!(ok = wait(C::B_MF + sl, t / kMetas, 0xF1))) break;
-                if (!busy) {                   // no rows: only the record's turn
+                if (!busy || (alt && (j & 1) != qt)) {     // nothing of this row tile's: only the record's turn
                     if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
                     continue;
                 }
@@ -583,13 +793,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 tc_fence_after();
                 const TileMeta* mt = metas + sl;
                 const bool edge = __any_sync(0xffffffffu, k0 < kmin || k0 + BN - 1 > kmax);
+                constexpr int E_ON = TREE ? E_BITS : E_RANGE;
                 float um, x;
-                if (edge) maxima<true>(tS, mt, c0, f_row, k0, kmin, kmax, um, x);
-                else maxima<false>(tS, mt, c0, f_row, k0, kmin, kmax, um, x);
+                uint64_t seen_own = 0, seen_other = 0;     // of this thread's 64 keys and the other's; a row that is not there masks nothing
+                if (TREE && edge) {
+                    seen_own = there ? seen_from(tr, k0 + c0, it.len) : ~0ull;
+                    seen_other = there ? seen_from(tr, k0 + 64 - c0, it.len) : ~0ull;
+                }
+                if (edge) maxima<E_ON>(tS, mt, c0, f_row, k0, kmin, kmax, seen_own, um, x);
+                else maxima<E_NONE>(tS, mt, c0, f_row, k0, kmin, kmax, 0, um, x);
                 xm = fmaxf(xm, x);
-                bool move = j == 0;
+                const bool fresh = alt ? j < 2 : j == 0;   // the first tile of this row tile
+                bool move = fresh;
                 if (!move) {                   // does a row of the two warps move its M?
-                    volatile int* f = flags + 2 * (t & 1);
+                    volatile int* f = flags + 2 * ((TREE ? cs : t) & 1);
                     const int mine = __any_sync(0xffffffffu, um > M + kTau);
                     if (lane == 0) f[half] = mine;
                     if (!(ok = meet())) break;
@@ -597,8 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 }
                 if (move) {                    // both threads of a row take the maximum of u over all of its columns
                     float u2, x2;
-                    if (edge) maxima<true>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, u2, x2);
-                    else maxima<false>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, u2, x2);
+                    if (edge) maxima<E_ON>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, seen_other, u2, x2);
+                    else maxima<E_NONE>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, 0, u2, x2);
                     um = fmaxf(um, u2);
                     float fac = 1.f;
                     if (um > M + kTau) {
@@ -606,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         M = um;
                         L *= fac;
                     }
-                    if (j > 0) {               // S(j) is complete, so every earlier W V has been added to O
+                    if (!fresh) {              // S(j) is complete, so every earlier W V has been added to O
 #pragma unroll 1
                         for (int cc = half * (DV / 64); cc < (half + 1) * (DV / 64); ++cc) {
                             uint32_t r[32];
@@ -619,13 +836,109 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     if (!(ok = meet())) break; // the other thread has read this one's scores
                 }
                 const float mref = M == -INFINITY ? 0.f : M - kOff;
-                L += edge ? weights<true>(tS, mt, c0, f_row, mref, k0, kmin, kmax) : weights<false>(tS, mt, c0, f_row, mref, k0, kmin, kmax);
+                L += edge ? weights<E_ON>(tS, mt, c0, f_row, mref, k0, kmin, kmax, seen_own)
+                          : weights<E_NONE>(tS, mt, c0, f_row, mref, k0, kmin, kmax, 0);
                 tc_fence_before();
                 mbar_arrive(BAR(C::B_P + qt));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
             }
             if (!ok) break;
+            if (TREE) {
+                // ---- the end of a piece: the row's sums of both half rows (alt: of both row tiles), then its columns
+                if (busy && it.tiles) {
+                    if (!(ok = wait(C::B_O + qt, seen, 0xF3))) break;
+                    tc_fence_after();
+                    ++seen;
+                }
+                // by way of the tiles of Q, which every product has read: [half][row] of (M, L, largest x)
+                auto stat = [&](int tile) { return reinterpret_cast<float4*>(smem + tile * C::Q_BYTES) + row; };
+                stat(qt)[128 * half] = make_float4(M, L, xm, 0.f);
+                if (!(ok = meet_all())) break;
+                const float4 s0 = stat(alt ? 0 : qt)[0], s1 = stat(alt ? 0 : qt)[128];
+                float4 s2 = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), s3 = s2;
+                if (alt) {
+                    s2 = stat(1)[0];
+                    s3 = stat(1)[128];
+                }
+                // row tile 0 (or this one): M s0.x; with alt row tile 1: M s2.x.  Largest x of all keys, l relative to it
+                float mm = fmaxf(fmaxf(s0.z, s1.z), fmaxf(s2.z, s3.z));
+                const float ref = mm == -INFINITY ? 0.f : mm, La = s0.y + s1.y, Lb = s2.y + s3.y;
+                auto times = [&](float x, float Mx, float lv) { return Mx == -INFINITY ? (x != x ? x : 0.f) : x * ex2(Mx - kOff - lv - ref); };
+                float l = times(La, s0.x, it.lv0) + times(Lb, s2.x, it.lv0), norm = 1.f;
+                const int64_t out_row = it.row0 + tok;
+                const bool leads = there && half == 0 && (!alt || qt == 0), whole = it.slot < 0;
+                if (!whole) {
+                    if (leads) pieces.ml[static_cast<int64_t>(it.slot) * kRows + (ri - it.i0)] = make_float2(mm, l);
+                } else {
+                    norm = l;
+                    if (a.sink) {
+                        const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(mm, sk);
+                        const float f = mm == -INFINITY ? 1.f : ex2(mm - nm);
+                        l = l * f + ex2(sk - (nm == -INFINITY ? 0.f : nm));
+                        norm = f == 0.f ? INFINITY : l / f;
+                        mm = nm;
+                    }
+                    if (leads && a.m) {
+                        a.m[static_cast<int64_t>(head) * a.T + out_row] = mm == -INFINITY ? mm : mm * kLn2;
+                        a.l[static_cast<int64_t>(head) * a.T + out_row] = l;
+                    }
+                    norm = norm == 0.f ? 0.f : 1.f / norm;
+                }
+                // O of a row tile times 2^(M - kOff - ref) / l; NaN among the weights stays
+                auto factor = [&](float Lx, float Mx) { return Mx == -INFINITY ? (Lx != Lx ? Lx : 0.f) : ex2(Mx - kOff - ref) * norm; };
+                const float fa = factor(La, s0.x), fb = factor(Lb, s2.x);
+                const bool hasA = it.tiles > 0, hasB = alt && it.tiles > 1;
+                const uint32_t tA = alt ? tmem + 256 + lanes : tO, tB = tmem + 384 + lanes;
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + out_row * a.os[0] + static_cast<int64_t>(head) * a.os[1];
+                float* part = pieces.part + (static_cast<int64_t>(whole ? 0 : it.slot) * kRows + (ri - it.i0)) * DV;
+                // 32 columns at a time: two threads to a row, four with alt
+#pragma unroll 1
+                for (int cc = alt ? 2 * qt + half : half; cc < DV / 32; cc += alt ? 4 : 2) {
+                    float x[32];
+                    uint32_t u[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    if (hasA) {
+                        tmem_ld32(tA + cc * 32, u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(u[i]) * fa;
+                    }
+                    if (hasB) {
+                        tmem_ld32(tB + cc * 32, u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(u[i]), fb, x[i]);
+                    }
+                    if (!there) continue;
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(part + cc * 32 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        if (cc * 32 + 8 * v >= a.dv) continue;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = pack_bf16(x[8 * v + 2 * e], x[8 * v + 2 * e + 1]);
+                        if (vec_o) {
+                            *reinterpret_cast<uint4*>(o + cc * 32 + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+                            unsigned short* p = reinterpret_cast<unsigned short*>(o + cc * 32 + 8 * v);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                p[2 * e] = static_cast<unsigned short>(w[e]);
+                                p[2 * e + 1] = static_cast<unsigned short>(w[e] >> 16);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                if (!(ok = meet_all())) break;             // the sums and both O have been read
+                if (busy && it.tiles) mbar_arrive(BAR(C::B_OE + qt));
+                continue;
+            }
             if (!busy) continue;
             if (it.tiles) {
                 if (!(ok = wait(C::B_O + qt, seen, 0xF3))) break;
@@ -701,35 +1014,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
     }
 }
 
-template <int D, int DV>
-cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, cudaStream_t s) {
+template <int D, int DV, bool TREE>
+cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, const Pieces& pieces, int most,
+                   cudaStream_t s) {
     using C = Cfg<D, DV>;
-    static std::atomic<int> sms[64];
+    auto kernel = k_cache_attn_tc<D, DV, TREE>;
+    static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int n = sms[dev & 63].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if ((e = cudaFuncSetAttribute(k_cache_attn_tc<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess ||
-            (e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-            return e;
-        sms[dev & 63].store(n, std::memory_order_relaxed);
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
     }
     const bool vec_q = (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && a.qs[0] % 8 == 0 && a.qs[1] % 8 == 0;
     const bool vec_o = (reinterpret_cast<uintptr_t>(a.o) & 15) == 0 && a.os[0] % 8 == 0 && a.os[1] % 8 == 0;
-    // at most the packed rows' groups and a ragged one per request
-    const int64_t most = (static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
-    k_cache_attn_tc<D, DV><<<static_cast<unsigned>(std::min<int64_t>(n, most)), kThreads, C::SMEM, s>>>(maps[0], maps[1], a, counter,
-                                                                                                       far, vec_q, vec_o);
+    kernel<<<static_cast<unsigned>(most), kThreads, C::SMEM, s>>>(maps[0], maps[1], a, counter, far, vec_q, vec_o, pieces);
     return cudaGetLastError();
 }
 
+template <int DV>
+cudaError_t join(const cache_mma::Work& w, int rpb, cudaStream_t s) {
+    return launch_early(dim3(w.ctas, kRows / rpb), dim3(256), 0, s, cache_mma::k_cache_join<DV, __nv_bfloat16>, w, rpb, w.a.status);
+}
+
+int sms() {
+    static std::atomic<int> cached[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    n = cached[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs of a call: trees, one per SM; else no more than the packed rows' groups and a ragged one per request.
+constexpr int kMaxCtas = 160;          // the workspace of trees is sized for this many
+int ctas_of(const CacheAttnArgs& a) {
+    const int64_t most = (static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
+    return a.tree ? std::min(sms(), kMaxCtas) : static_cast<int>(std::min<int64_t>(sms(), most));
+}
+
 }  // namespace
+
+size_t cache_attn_tc_workspace(const CacheAttnArgs& a) {
+    if (!a.tree || !cache_attn_tc_takes(a)) return 0;
+    const size_t slots = 2 * static_cast<size_t>(kMaxCtas) * kRows, DV = a.dv <= 64 ? 64 : 128;
+    return (sizeof(Rec) * kMaxCtas + 255) / 256 * 256 + slots * sizeof(float2) + slots * DV * sizeof(float);
+}
 
 bool cache_attn_tc_takes(const CacheAttnArgs& a) {
     if (a.dtype != BPA_BF16 || a.d % 16 || a.dv % 16 || a.d > 128 || a.dv > 128 || (a.d <= 64 && a.dv > 64) || a.P % 16) return false;
     const int64_t rows = static_cast<int64_t>(a.max_q) * a.G;
     if (rows <= kFewRows) return false;
+    if (a.tree) return true;           // items are cut between CTAs
     // An item's keys are not shared between CTAs here, as they are in the kernel for few rows: with few
     // items (one token of 128 heads over a long context) that one fills the GPU and this one does not.
     // With all CTAs busy this one is 4.6 times faster (pieces of prompts 1,540 us and 7.1 ms).  The border, one
@@ -743,9 +1083,29 @@ bool cache_attn_tc_takes(const CacheAttnArgs& a) {
 
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a) { return {a.d <= 64 ? 64 : 128, a.dv <= 64 ? 64 : 128, 16}; }
 
-cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, cudaStream_t s) {
-    if (a.d <= 64) return launch<64, 64>(a, maps, counter, far, s);
-    return a.dv <= 64 ? launch<128, 64>(a, maps, counter, far, s) : launch<128, 128>(a, maps, counter, far, s);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, uint8_t* ws,
+                                 cudaStream_t s) {
+    const int ctas = ctas_of(a);
+    if (!a.tree) {
+        if (a.d <= 64) return launch<64, 64, false>(a, maps, counter, far, {}, ctas, s);
+        return a.dv <= 64 ? launch<128, 64, false>(a, maps, counter, far, {}, ctas, s) : launch<128, 128, false>(a, maps, counter, far, {}, ctas, s);
+    }
+    cache_mma::Work w = {};
+    w.a = a;
+    w.rows_per = kRows;
+    w.ctas = ctas;
+    w.far = far;                       // the join adds to the status word
+    w.recs = reinterpret_cast<Rec*>(ws);
+    w.ml = reinterpret_cast<float2*>(ws + (sizeof(Rec) * kMaxCtas + 255) / 256 * 256);
+    w.part = reinterpret_cast<float*>(w.ml + 2 * static_cast<size_t>(kMaxCtas) * kRows);
+    const Pieces pieces = {w.recs, w.ml, w.part};
+    const cudaError_t e = a.d <= 64 ? launch<64, 64, true>(a, maps, counter, far, pieces, ctas, s)
+                          : a.dv <= 64 ? launch<128, 64, true>(a, maps, counter, far, pieces, ctas, s)
+                                       : launch<128, 128, true>(a, maps, counter, far, pieces, ctas, s);
+    if (e != cudaSuccess) return e;
+    const int64_t each = ctas / (static_cast<int64_t>(a.R) * a.Hkv);
+    const int rpb = each <= 4 ? 8 : each <= 16 ? 4 : 2;
+    return a.dv <= 64 ? join<64>(w, rpb, s) : join<128>(w, rpb, s);
 }
 
 }  // namespace bpa
