@@ -14,6 +14,9 @@ namespace bpa {
 // 1,024) 41.2, 59.9 and 73.4 us; 33 of 8 to 64 rows over up to 8,000 tokens, 128 channels 222, 194 and
 // 230.  Pieces of prompts (thousands of rows) take 1,540 us there and 7.1 ms here.
 constexpr int kFewRows = 64;
+// The same under a tree, where the tensor cores share out keys as well: 19 requests of 8,192 tokens, 4 q heads a kv
+// head, 128 channels; 64 rows 172 us there and 249 here, 32 rows 172 and 142.
+constexpr int kFewTreeRows = 32;
 constexpr int kPlanMaxR = 8192;      // requests of one plan: their lengths and offsets sit in shared memory
 constexpr int kMaxTreeWords = 32;    // words of a row's mask: 1,024 rows of a request
 
@@ -97,6 +100,10 @@ struct CacheAttnArgs {
     int tree_words;
     uint32_t* status;
 };
+
+namespace cache_mma {
+struct Pieces;                       // cache_attn_mma.cuh
+}
 
 #ifdef __CUDACC__
 // Programmatic dependent launch: a kernel launched by launch_early is set up while the one before it
@@ -200,7 +207,9 @@ size_t cache_attn_mma_workspace(const CacheAttnArgs& a);
 CacheBox cache_attn_mma_box(const CacheAttnArgs& a);
 // far: null, or the marks of launch_cache_attn_tc, which has run before on the same status word: requests
 // of more than kFewRows rows are then computed only where they are marked.
-cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, const uint32_t* far, cudaStream_t s);
+// more: null, or pieces that launch_cache_attn_tc has left for the join (trees).
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, const uint32_t* far,
+                                  const cache_mma::Pieces* more, cudaStream_t s);
 uint32_t* cache_attn_far(uint8_t* ws);      // the marks' place, [R]
 
 // Tensor-core kernel for requests of more than kFewRows rows (bf16, head dims in steps of 16 up to 128,
@@ -208,8 +217,8 @@ uint32_t* cache_attn_far(uint8_t* ws);      // the marks' place, [R]
 // the requests whose v scales lie too far apart for it, whatever it has written for them.
 bool cache_attn_tc_takes(const CacheAttnArgs& a);       // supported, and there may be enough such requests
 CacheBox cache_attn_tc_box(const CacheAttnArgs& a);      // plain (not swizzled) boxes
-// ws: of trees, cache_attn_tc_workspace bytes
-cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, uint8_t* ws, cudaStream_t s);
+// ws: of trees, cache_attn_tc_workspace bytes; *left: their pieces, for the join.
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, uint8_t* ws, cache_mma::Pieces* left, cudaStream_t s);
 size_t cache_attn_tc_workspace(const CacheAttnArgs& a);
 
 }  // namespace bpa

@@ -11,6 +11,7 @@
 #include "bpa.h"
 #include "bpa_internal.h"
 #include "cache.h"
+#include "cache_pieces.h"
 
 using namespace bpa;
 
@@ -422,6 +423,7 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
         if (make_cache_map(&maps[0], a.kc, a, a.d, a.kcs, box.cols_k, box.rows, true) &&
             make_cache_map(&maps[1], a.vc, a, a.dv, a.vcs, box.cols_v, box.rows, true)) {
             uint32_t* far = nullptr;
+            cache_mma::Pieces left = {};
             if (cache_attn_tc_takes(a)) {               // requests of many rows first
                 far = cache_attn_far(static_cast<uint8_t*>(workspace));
                 const size_t used = reinterpret_cast<uint8_t*>(far + a.R) - static_cast<uint8_t*>(workspace);
@@ -432,10 +434,10 @@ bpa_status bpa_cache_attn(const bpa_cache_desc* cache, const bpa_cache_batch* ba
                 if (!make_cache_map(&raw[0], a.kc, a, a.d, a.kcs, plain.cols_k, plain.rows, false) ||
                     !make_cache_map(&raw[1], a.vc, a, a.dv, a.vcs, plain.cols_v, plain.rows, false))
                     return fail(BPA_ERR_CUDA, "cache attention: no tensor map");
-                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, far, static_cast<uint8_t*>(workspace) + cache_attn_mma_workspace(a), s), "cache attention launch");
+                st = cuda_status(launch_cache_attn_tc(a, raw, a.status + 2, far, static_cast<uint8_t*>(workspace) + cache_attn_mma_workspace(a), &left, s), "cache attention launch");
                 if (st != BPA_OK) return st;
             }
-            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), far, s),
+            return cuda_status(launch_cache_attn_mma(a, maps, static_cast<uint8_t*>(workspace), far, a.tree && far ? &left : nullptr, s),
                                "cache attention launch");
         }
     }

@@ -18,7 +18,6 @@ int sm_count() {
     return n;
 }
 
-constexpr int kMaxSms = 160;          // the workspace is sized for this many
 constexpr size_t kFarAt = 256;        // the marks lie behind the header
 
 struct Plan {
@@ -73,11 +72,13 @@ CacheBox cache_attn_mma_box(const CacheAttnArgs& a) {
     return {p.DP < 128 ? p.DP : 128, p.DVP < 128 ? p.DVP : 128, a.P < kTile ? a.P : kTile};
 }
 
-cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, const uint32_t* far, cudaStream_t s) {
+cudaError_t launch_cache_attn_mma(const CacheAttnArgs& a, const CUtensorMap* maps, uint8_t* ws, const uint32_t* far, const Pieces* more,
+                                  cudaStream_t s) {
     Plan p;
     if (!plan_of(a, p)) return cudaErrorInvalidValue;
-    Work w;
+    Work w = {};
     w.a = a;
+    if (more) w.more = *more;
     w.rows_per = p.rows_per;
     w.far = far;
     // no more CTAs than the longest table rows have tiles

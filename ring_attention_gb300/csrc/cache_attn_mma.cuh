@@ -39,11 +39,13 @@
 #include <type_traits>
 
 #include "cache.h"
+#include "cache_pieces.h"
 #include "common.cuh"
 
 namespace bpa {
 namespace cache_mma {
 
+constexpr int kMaxSms = 160;          // the workspace is sized for this many
 constexpr int kTile = 64;             // keys per stage
 constexpr int kNW = 4;                // consumer warps
 constexpr int kThreads = 32 * (kNW + 1);
@@ -53,14 +55,6 @@ constexpr int kBatch = 8;             // tiles whose page ids and scales are fet
 constexpr float kOff = 9.f;           // log2 of the largest fp16 weight right after M moved
 constexpr float kLazy = 6.f;          // M moves when it grows by more
 
-struct Rec {                          // what a CTA leaves for the join
-    int trail;                        // slot 1 holds the first of `trail` pieces of an item (0: none)
-    int row0, hk, i0, nrows;          // that item
-    uint32_t flags, where;            // this CTA's status
-    int pad;
-};
-static_assert(sizeof(Rec) == 32, "record");
-
 struct Work {
     CacheAttnArgs a;
     int rows_per, ctas;               // rows of an item, CTAs
@@ -69,6 +63,7 @@ struct Work {
     Rec* recs;                        // [ctas]
     float2* ml;                       // [2 ctas][rows_per] (m in log2 units, l)
     float* part;                      // [2 ctas][rows_per][DVP] relative to m
+    Pieces more;                      // or ctas = 0
 };
 
 struct Meta {
@@ -162,7 +157,7 @@ BPA_DEV void ld_q4(const __nv_bfloat16* p, float (&v)[4]) {
 template <bool BESIDE>
 BPA_DEV Req own_request(const Work& w, int r) {
     Req q = request_of(w.a, r);
-    if (BESIDE && q.n * w.a.G > kFewRows && !w.far[r]) q.n = 0;
+    if (BESIDE && q.n * w.a.G > (w.a.tree ? kFewTreeRows : kFewRows) && !w.far[r]) q.n = 0;
     return q;
 }
 
@@ -999,6 +994,138 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
         if (lane * V + i < a.dv) o[lane * V + i] = static_cast<E>(acc[i] * f);
 }
 
+// The same for trees, whose pieces may come from two kernels (w's and w.more's; of these none of a request in w.far)
+// and whose items are of any number of rows: GL lanes to a row, the rows of all cut items one after the other, on as many
+// blocks as the GPU holds at once.  (A block for every few rows of every CTA, of which most have none: 20,000
+// of them cost one request of 104 rows 47 us where this takes 27.)
+template <int DVP, typename E>
+__global__ void __launch_bounds__(256) k_cache_join_rows(const Work w, uint32_t* out_status) {
+    constexpr int GL = DVP <= 128 ? 8 : 16, V = DVP / GL, ROWS = 32 / GL, kMost = kMaxSms * 5, PER = (kMost + 255) / 256;
+    __shared__ int s_cum[kMost + 1], s_warp[8];
+    __shared__ uint32_t s_flags, s_where;
+    const CacheAttnArgs& a = w.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = w.ctas + w.more.ctas;
+    auto rec_of = [&](int c) { return c < w.ctas ? w.recs + c : w.more.recs + (c - w.ctas); };
+    if (threadIdx.x == 0) s_flags = s_where = 0;
+    wait_for_previous();
+    __syncthreads();
+    // rows in front of each CTA's cut item
+    int rows[PER], mine = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = threadIdx.x * PER + k;
+        rows[k] = 0;
+        if (c < all) {
+            const Rec rec = *rec_of(c);
+            if (rec.trail && !(c >= w.ctas && w.far[rec.r])) rows[k] = rec.nrows;
+            if (blockIdx.x == 0 && c < w.ctas && rec.flags) {
+                atomicOr(&s_flags, rec.flags);
+                atomicMax(&s_where, rec.where);
+            }
+        }
+        mine += rows[k];
+    }
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (!w.far) {
+            out_status[0] = s_flags;
+            out_status[1] = s_where;
+        } else if (s_flags) {
+            report(out_status, s_flags, s_where);
+        }
+    }
+    x -= mine;
+    for (int k = 0; k < warp; ++k) x += s_warp[k];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = threadIdx.x * PER + k;
+        if (c <= all) s_cum[c] = x;
+        x += rows[k];
+    }
+    __syncthreads();
+    const int gl = lane % GL;
+    for (int task = (blockIdx.x * 8 + warp) * ROWS + lane / GL; task < s_cum[all]; task += gridDim.x * 8 * ROWS) {
+        int lo = 0, hi = all;          // the last CTA with s_cum <= task
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_cum[mid] <= task) lo = mid;
+            else hi = mid;
+        }
+        const bool second = lo >= w.ctas;
+        const int c = second ? lo - w.ctas : lo, row = task - s_cum[lo], rows_per = second ? w.more.rows_per : w.rows_per;
+        const Rec rec = *rec_of(lo);
+        const float2* const mls = second ? w.more.ml : w.ml;
+        // a lane's channels: 4 gl + 4 GL i ..; w.more's lie four by four for all rows
+        const int by_row = second ? 4 : DVP, by_four = second ? 4 * rows_per : 4;
+        const float* const sums = (second ? w.more.part : w.part) + row * by_row + gl * by_four;
+        float m = -INFINITY, l = 0.f;
+        float4 acc[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // one pass with the running maximum; four pieces' loads at a time
+        for (int k0 = 0; k0 < rec.trail; k0 += 4) {
+            float2 ml[4];
+            float4 v[4][V / 4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + q;
+                ml[q] = make_float2(-INFINITY, 0.f);
+                if (k >= rec.trail) continue;
+                const int64_t s = (2 * (static_cast<int64_t>(c) + k) + (k == 0)) * rows_per;
+                ml[q] = mls[s + row];
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i) v[q][i] = *reinterpret_cast<const float4*>(sums + s * DVP + GL * i * by_four);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (k0 + q >= rec.trail || ml[q].y == 0.f) continue;      // no keys in the piece
+                const float nm = fmaxf(m, ml[q].x), ref = nm == -INFINITY ? 0.f : nm;
+                const float f0 = m == -INFINITY ? (l != l ? l : 0.f) : ex2(m - ref), f1 = ex2(ml[q].x - ref);
+                l = l * f0 + ml[q].y * f1;
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i)
+                    acc[i] = make_float4(acc[i].x * f0 + v[q][i].x * f1, acc[i].y * f0 + v[q][i].y * f1, acc[i].z * f0 + v[q][i].z * f1,
+                                         acc[i].w * f0 + v[q][i].w * f1);
+                m = nm;
+            }
+        }
+        const int ri = rec.i0 + row, tok = ri / a.G, head = rec.hk * a.G + ri - tok * a.G;
+        float f = 1.f;
+        if (a.sink) {
+            const float sk = __ldg(a.sink + head) * kLog2e, nm = fmaxf(m, sk);
+            f = m == -INFINITY ? 1.f : ex2(m - nm);
+            l = l * f + ex2(sk - (nm == -INFINITY ? 0.f : nm));
+            m = nm;
+        }
+        if (a.m && gl == 0) {
+            a.m[static_cast<int64_t>(head) * a.T + rec.row0 + tok] = m == -INFINITY ? m : m * kLn2;
+            a.l[static_cast<int64_t>(head) * a.T + rec.row0 + tok] = l;
+        }
+        f = l == 0.f ? 0.f : f / l;
+        E* o = static_cast<E*>(a.o) + static_cast<int64_t>(rec.row0 + tok) * a.os[0] + static_cast<int64_t>(head) * a.os[1];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const int ch = 4 * gl + 4 * GL * i;
+            const float x[4] = {acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f};
+            if (ch >= a.dv) continue;      // dv is a multiple of 16
+            if (std::is_same<E, __nv_bfloat16>::value && w.vec_o) {
+                reinterpret_cast<uint32_t*>(o + ch)[0] = pack_bf16(x[0], x[1]);
+                reinterpret_cast<uint32_t*>(o + ch)[1] = pack_bf16(x[2], x[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[ch + e] = static_cast<E>(x[e]);
+            }
+        }
+    }
+}
+
 template <int DP, int DVP, int NT, bool SPLIT, bool BESIDE, bool TREE>
 cudaError_t launch(const Work& w, const CUtensorMap* maps, int rpb, cudaStream_t s) {
     using C = Cfg<DP, DVP, NT, SPLIT>;
@@ -1015,6 +1142,7 @@ cudaError_t launch(const Work& w, const CUtensorMap* maps, int rpb, cudaStream_t
     }
     if ((e = launch_early(dim3(w.ctas), dim3(kThreads), C::SMEM, s, kernel, maps[0], maps[1], w)) != cudaSuccess) return e;
     using E = typename std::conditional<SPLIT, float, __nv_bfloat16>::type;
+    if (TREE) return launch_early(dim3(2 * std::max(1, w.ctas / C::OCC)), dim3(256), 0, s, k_cache_join_rows<DVP, E>, w, w.a.status);
     return launch_early(dim3(w.ctas, w.rows_per / rpb), dim3(256), 0, s, k_cache_join<DVP, E>, w, rpb, w.a.status);
 }
 

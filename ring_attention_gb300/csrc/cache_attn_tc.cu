@@ -56,7 +56,7 @@ constexpr float kFar = 40.f;          // log2: a scale further from the item's f
 constexpr float kZeros = 20.f, kAllZeros = -kFar - kZeros;   // log2 scale of a page of zeros: below the largest so far; before any
 
 struct TileMeta {
-    int key0, len, end;
+    int key0, len, end, alt;
     uint32_t zero;                    // bit c: the v scale of chunk c is 0
     float a[8], lv[8], e[8];          // k scale * softmax scale * log2(e); log2 v scale; 2^(lv0 - lv)
 };
@@ -65,12 +65,8 @@ struct Item {
     float lv0;
     int slot, alt, pad;               // trees: place of a piece (-1: a whole item), even and odd key tiles apart
 };
+using cache_mma::Pieces;
 using cache_mma::Rec;
-struct Pieces {                       // of trees
-    Rec* recs;                        // [CTAs]
-    float2* ml;                       // [2 CTAs][kRows] (m in log2 units, l)
-    float* part;                      // [2 CTAs][kRows][DV] relative to m
-};
 
 template <int D, int DV>
 struct Cfg {
@@ -94,10 +90,13 @@ struct Cfg {
     static constexpr uint32_t IDESC_PV = F16 | 1u << 16 | (DV >> 3) << 17 | (128 >> 4) << 24;   // V: MN-major
 };
 
+// Keys of one copy: whatever of a tile one page is sure to hold.
+__host__ __device__ inline int box_rows(int P) { return P % 128 == 0 ? 128 : P % 64 == 0 ? 64 : P % 32 == 0 ? 32 : 16; }
+
 // A request's items: nothing for one that the kernel for few rows takes.
 BPA_DEV int groups_of(const CacheAttnArgs& a, const Req& q) {
     const int rows = q.n * a.G;
-    return rows > kFewRows ? (rows + kRows - 1) / kRows : 0;
+    return rows > (a.tree ? kFewTreeRows : kFewRows) ? (rows + kRows - 1) / kRows : 0;
 }
 
 BPA_DEV uint32_t h2(float lo, float hi) {
@@ -314,15 +313,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             fence_proxy_async_smem();
             __syncwarp();
         };
+        // The same in fewer instructions, four reads at a time: where the conversion is what a tile waits for (even and odd
+        // key tiles apart: 172 us against 191 for 19 requests of 128 rows, 8,192 tokens).  With 256 rows it takes the shared memory from the
+        // products at the wrong time: 235 us against 222.  Eight lanes in a row take two rows (RB 128: the halves of them that lie on other banks), whose swizzled units lie on
+        // other banks too, so that neither side has conflicts, and every address is a base and a constant.
+        auto convert_fast = [&](const uint8_t* raw, auto rb, uint8_t* tile, int left) {
+            constexpr int RB = decltype(rb)::value, STEP = RB == 128 ? 4 : 8;         // rows of a warp's read
+            const int c = lane & 3, p = lane >> 2 & 1, q = lane >> 4;
+            const int slab = RB == 128 ? (lane >> 3 & 1) ^ p : 0, r = RB == 128 ? 2 * q + p : lane >> 2;
+            const uint8_t* from = raw + (32 * wq + r) * RB + 64 * slab + 16 * c;
+            uint8_t* to = tile + slab * C::SUB + (32 * wq + r) * 128;
+            const int o = (2 * c ^ r) << 4;                                           // unit 2 c of the row; 2 c + 1: o ^ 16
+            uint8_t* const at[4] = {to + o, to + (o ^ 16), to + (o ^ 64), to + (o ^ 80)};
+            const int rows = left - 32 * wq - r;                                      // slots past the last token may hold anything
+            auto four = [&](int i0, auto tail) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * STEP * RB);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (decltype(tail)::value && (i0 + i) * STEP >= rows) x[i] = make_uint4(0, 0, 0, 0);
+                    // rows four further on are swizzled the other way
+                    const int flip = RB == 128 ? 2 * (i & 1) : 0;
+                    *reinterpret_cast<uint4*>(at[flip] + (i0 + i) * STEP * 128) =
+                        make_uint4(cvt_lo(x[i].x), cvt_hi(x[i].x), cvt_lo(x[i].y), cvt_hi(x[i].y));
+                    *reinterpret_cast<uint4*>(at[flip + 1] + (i0 + i) * STEP * 128) =
+                        make_uint4(cvt_lo(x[i].z), cvt_hi(x[i].z), cvt_lo(x[i].w), cvt_hi(x[i].w));
+                }
+            };
+#pragma unroll
+            for (int i0 = 0; i0 < 32 / STEP; i0 += 4) {
+                if (32 * wq + 32 > left) four(i0, std::true_type());
+                else four(i0, std::false_type());
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
         for (int t = 0;; ++t) {
             const int st = t % C::NS, use = t / C::NS, sl = t % kMetas;
             if (!wait(C::B_MF + sl, t / kMetas, 0xE0) || metas[sl].end) break;
             const int left = metas[sl].len - metas[sl].key0;
+            const bool alt = TREE && metas[sl].alt;
             const uint32_t zero = metas[sl].zero >> (2 * wq) & 3;   // this warp's two 16 rows
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
             if (!wait(C::B_RF, t, 0xE1) || (use > 0 && !wait(C::B_KE + st, use - 1, 0xE2))) break;
-            convert(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
+            if (alt) convert_fast(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
+            else convert(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
             if (lane == 0) {
                 mbar_arrive(BAR(C::B_KF + st));
                 mbar_arrive(BAR(C::B_RE));
@@ -337,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     }
                 __syncwarp();
             }
-            convert(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
+            if (alt) convert_fast(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
+            else convert(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
             if (lane == 0) {
                 mbar_arrive(BAR(C::B_VF + st));
                 mbar_arrive(BAR(C::B_RE + 1));
@@ -347,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kAux) {
             // -------------------------------------------------------- items and their key tiles' records
+            const int box = box_rows(a.P);
             int t = 0;                 // records written
             auto publish_end = [&]() {
                 if (t >= kMetas && !wait(C::B_ME + t % kMetas, t / kMetas - 1, 0xE4)) return;
@@ -434,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         // its pieces: up to the last CTA c with total c / parts < the end of the item's cost
                         const long long at_end = own.at + (cut.cost() - off);
                         own.rec.trail = static_cast<int>((at_end * own.parts + own.total - 1) / own.total) - blockIdx.x;
+                        own.rec.r = own.r;
                         own.rec.row0 = own.rq.row0;
                         own.rec.hk = own.hk;
                         own.rec.i0 = g * kRows;
@@ -549,8 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         lv = lv0;
                     }
                     lvmax = fmaxf(lvmax, lv);
+                    if (zero & 0xffu) {
 #pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) lvmax = fmaxf(lvmax, __shfl_xor_sync(0xffffffffu, lvmax, o));
+                        for (int o = 1; o < 8; o <<= 1) lvmax = fmaxf(lvmax, __shfl_xor_sync(0xffffffffu, lvmax, o));
+                    }
                     if (lv == -INFINITY) lv = lvmax == -INFINITY ? kAllZeros : lvmax - kZeros;
                     if (lane < 8) {
                         m->a[lane] = ks * a.scale * kLog2e;
@@ -561,20 +603,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         m->key0 = (first + j) * BN;
                         m->len = rq.len;
                         m->end = 0;
+                        m->alt = TREE && rq.n * a.G - i0 <= 128;
                         m->zero = zero;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(BAR(C::B_MF + sl));
-                    // the tile's codes: K, then V, 16 keys a copy
-                    const int n = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                    // the tile's codes: K, then V, a box of keys (of one page) a copy
                     const int tok = ((first + j) * BN + 16 * lane) % a.P;
+                    const bool copies = id >= 0 && 16 * lane % box == 0;
+                    const int n = __popc(__ballot_sync(0xffffffffu, copies)) * box;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const int rb = kv ? C::RBV : C::RBK;
                         if (t > 0 && !(ok = wait(C::B_RE + kv, t - 1, 0xEF))) break;
-                        if (lane == 0) mbar_expect_tx(BAR(C::B_RF + kv), n * 16 * rb);
+                        if (lane == 0) mbar_expect_tx(BAR(C::B_RF + kv), n * rb);
                         __syncwarp();
-                        if (id >= 0)
+                        if (copies)
                             tma_load_4d(sb + C::OFF_RAW + kv * C::RAW + 16 * lane * rb, kv ? &tmV : &tmK, BAR(C::B_RF + kv), 0, tok, hk, id);
                     }
                     if (!ok) break;
@@ -629,22 +673,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         if (!ok) break;
                         tc_fence_after();
                         issue_s(i, t + i);
+                        tc_commit_w(BAR(C::B_KE + (t + i) % C::NS));
                     }
                     for (int j = 0; ok && j < it.tiles; ++j, ++t) {
                         const int i = j & 1;
                         if (!(ok = wait(C::B_VF + t % C::NS, t / C::NS, 0xEA) && wait(C::B_P + i, np[i], 0xEB))) break;
                         if (j < 2 && seen[i] > 0 && !(ok = wait(C::B_OE + i, seen[i] - 1, 0xEC))) break;
                         ++np[i];
-                        tc_commit_w(BAR(C::B_KE + t % C::NS));     // S(j) is complete
                         tc_fence_after();
                         issue_pv(i, t, j < 2);
+                        tc_commit_w(BAR(C::B_VE + t % C::NS));
                         if (j + 2 >= it.tiles) tc_commit_w(BAR(C::B_O + i));
                         if (j + 2 < it.tiles) {
                             if (!(ok = wait(C::B_KF + t % C::NS, t / C::NS + 1, 0xED))) break;
                             tc_fence_after();
                             issue_s(i, t + 2);
+                            tc_commit_w(BAR(C::B_KE + t % C::NS));
                         }
-                        tc_commit_w(BAR(C::B_VE + t % C::NS));
                     }
                     for (int i = 0; i < both; ++i) ++seen[i];
                     continue;
@@ -818,7 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     else maxima<E_NONE>(tS, mt, 64 - c0, f_row, k0, kmin, kmax, 0, u2, x2);
                     um = fmaxf(um, u2);
                     float fac = 1.f;
-                    if (um > M + kTau) {
+                    // trees: all rows that have grown move along with one that must (they share the pass over O)
+                    if (um > M + (TREE ? 0.f : kTau)) {
                         fac = M == -INFINITY ? 0.f : ex2(M - um);
                         M = um;
                         L *= fac;
@@ -891,7 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 const bool hasA = it.tiles > 0, hasB = alt && it.tiles > 1;
                 const uint32_t tA = alt ? tmem + 256 + lanes : tO, tB = tmem + 384 + lanes;
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + out_row * a.os[0] + static_cast<int64_t>(head) * a.os[1];
-                float* part = pieces.part + (static_cast<int64_t>(whole ? 0 : it.slot) * kRows + (ri - it.i0)) * DV;
+                // four channels of all rows together: a warp's rows are written side by side
+                float* part = pieces.part + static_cast<int64_t>(whole ? 0 : it.slot) * kRows * DV + 4 * (ri - it.i0);
                 // 32 columns at a time: two threads to a row, four with alt
 #pragma unroll 1
                 for (int cc = alt ? 2 * qt + half : half; cc < DV / 32; cc += alt ? 4 : 2) {
@@ -913,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     if (!whole) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4*>(part + cc * 32 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                            *reinterpret_cast<float4*>(part + (cc * 32 + i) * kRows) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                         continue;
                     }
 #pragma unroll
@@ -1034,11 +1081,6 @@ cudaError_t launch(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* co
     return cudaGetLastError();
 }
 
-template <int DV>
-cudaError_t join(const cache_mma::Work& w, int rpb, cudaStream_t s) {
-    return launch_early(dim3(w.ctas, kRows / rpb), dim3(256), 0, s, cache_mma::k_cache_join<DV, __nv_bfloat16>, w, rpb, w.a.status);
-}
-
 int sms() {
     static std::atomic<int> cached[64];
     int dev = 0, n = 0;
@@ -1068,7 +1110,7 @@ size_t cache_attn_tc_workspace(const CacheAttnArgs& a) {
 bool cache_attn_tc_takes(const CacheAttnArgs& a) {
     if (a.dtype != BPA_BF16 || a.d % 16 || a.dv % 16 || a.d > 128 || a.dv > 128 || (a.d <= 64 && a.dv > 64) || a.P % 16) return false;
     const int64_t rows = static_cast<int64_t>(a.max_q) * a.G;
-    if (rows <= kFewRows) return false;
+    if (rows <= (a.tree ? kFewTreeRows : kFewRows)) return false;
     if (a.tree) return true;           // items are cut between CTAs
     // An item's keys are not shared between CTAs here, as they are in the kernel for few rows: with few
     // items (one token of 128 heads over a long context) that one fills the GPU and this one does not.
@@ -1081,31 +1123,23 @@ bool cache_attn_tc_takes(const CacheAttnArgs& a) {
     return items >= 32;
 }
 
-CacheBox cache_attn_tc_box(const CacheAttnArgs& a) { return {a.d <= 64 ? 64 : 128, a.dv <= 64 ? 64 : 128, 16}; }
+CacheBox cache_attn_tc_box(const CacheAttnArgs& a) { return {a.d <= 64 ? 64 : 128, a.dv <= 64 ? 64 : 128, box_rows(a.P)}; }
 
 cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps, uint32_t* counter, uint32_t* far, uint8_t* ws,
-                                 cudaStream_t s) {
+                                 Pieces* left, cudaStream_t s) {
     const int ctas = ctas_of(a);
     if (!a.tree) {
         if (a.d <= 64) return launch<64, 64, false>(a, maps, counter, far, {}, ctas, s);
         return a.dv <= 64 ? launch<128, 64, false>(a, maps, counter, far, {}, ctas, s) : launch<128, 128, false>(a, maps, counter, far, {}, ctas, s);
     }
-    cache_mma::Work w = {};
-    w.a = a;
-    w.rows_per = kRows;
-    w.ctas = ctas;
-    w.far = far;                       // the join adds to the status word
-    w.recs = reinterpret_cast<Rec*>(ws);
-    w.ml = reinterpret_cast<float2*>(ws + (sizeof(Rec) * kMaxCtas + 255) / 256 * 256);
-    w.part = reinterpret_cast<float*>(w.ml + 2 * static_cast<size_t>(kMaxCtas) * kRows);
-    const Pieces pieces = {w.recs, w.ml, w.part};
-    const cudaError_t e = a.d <= 64 ? launch<64, 64, true>(a, maps, counter, far, pieces, ctas, s)
-                          : a.dv <= 64 ? launch<128, 64, true>(a, maps, counter, far, pieces, ctas, s)
-                                       : launch<128, 128, true>(a, maps, counter, far, pieces, ctas, s);
-    if (e != cudaSuccess) return e;
-    const int64_t each = ctas / (static_cast<int64_t>(a.R) * a.Hkv);
-    const int rpb = each <= 4 ? 8 : each <= 16 ? 4 : 2;
-    return a.dv <= 64 ? join<64>(w, rpb, s) : join<128>(w, rpb, s);
+    Pieces& p = *left;
+    p.recs = reinterpret_cast<Rec*>(ws);
+    p.ml = reinterpret_cast<float2*>(ws + (sizeof(Rec) * kMaxCtas + 255) / 256 * 256);
+    p.part = reinterpret_cast<float*>(p.ml + 2 * static_cast<size_t>(kMaxCtas) * kRows);
+    p.ctas = ctas;
+    p.rows_per = kRows;
+    if (a.d <= 64) return launch<64, 64, true>(a, maps, counter, far, p, ctas, s);
+    return a.dv <= 64 ? launch<128, 64, true>(a, maps, counter, far, p, ctas, s) : launch<128, 128, true>(a, maps, counter, far, p, ctas, s);
 }
 
 }  // namespace bpa
