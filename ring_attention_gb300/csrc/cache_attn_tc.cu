@@ -78,7 +78,8 @@ struct Cfg {
     static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + NS * K_BYTES, OFF_RAW = OFF_V + NS * V_BYTES;
     static constexpr int OFF_META = OFF_RAW + 2 * RAW, OFF_ITEM = OFF_META + kMetas * (int)sizeof(TileMeta);
     static constexpr int OFF_PAIR = OFF_ITEM + 2 * (int)sizeof(Item);           // flags of the softmax warps
-    static constexpr int OFF_BAR = OFF_PAIR + 128;
+    static constexpr int OFF_EXP = OFF_PAIR + 128;               // exponents of the rows of q, 8 x 32
+    static constexpr int OFF_BAR = OFF_EXP + 256;
     static constexpr int B_Q = 0, B_KF = 2, B_KE = B_KF + NS, B_VF = B_KE + NS, B_VE = B_VF + NS, B_S = B_VE + NS,
                          B_P = B_S + 2, B_O = B_P + 2, B_OE = B_O + 2, B_MF = B_OE + 2, B_ME = B_MF + kMetas,
                          B_IF = B_ME + kMetas, B_IE = B_IF + 2, B_RF = B_IE + 2, B_RE = B_RF + 2, B_PAIR = B_RE + 2,
@@ -574,6 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     *it = {1, rq.row0, rq.n, rq.len, hk, i0, first, tiles, lv0, slot, TREE && rq.n * a.G - i0 <= 128, 0};
                     mbar_arrive(BAR(C::B_IF + (k & 1)));
                 }
+                if (TREE) {            // the item's rows of q on their way to L2: the softmax warps come to them a tile or more later
+                    const int rows = min(rq.n * a.G - i0, kRows), lines = (a.d * 2 + 127) / 128;
+                    for (int i = lane; i < rows * lines; i += 32) {
+                        const int ri = i0 + i / lines, tok = ri / a.G;
+                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(rq.row0 + tok) * a.qs[0] +
+                                                 static_cast<int64_t>(hk * a.G + ri - tok * a.G) * a.qs[1];
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(q) + 128 * (i % lines)));
+                    }
+                }
                 bool ok = true;
                 float lvmax = -INFINITY;
                 for (int j = 0; j < tiles; ++j, ++t) {
@@ -773,55 +783,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             }
             float f_row = 1.f;
             if (busy && it.tiles) {
-                // ---- the row of q as fp16, its largest value scaled into [2^7, 2^8): all of it for the
-                // largest, this thread's half to store
-                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(it.row0 + tok) * a.qs[0] +
-                                         static_cast<int64_t>(head) * a.qs[1];
-                auto piece = [&](int c) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (there && 8 * c < a.d) {
-                        if (vec_q) {
-                            x = *reinterpret_cast<const uint4*>(q + 8 * c);
-                        } else {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const unsigned short* p = reinterpret_cast<const unsigned short*>(q + 8 * c + 2 * e);
-                                w[e] = p[0] | static_cast<uint32_t>(p[1]) << 16;
-                            }
-                            x = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                // ---- the rows of q as fp16, each one's largest value scaled into [2^7, 2^8).  Each warp of the pair takes 16
+                // of the 32 rows: as they are into their places in the tile, all copies under way together (PER lanes
+                // read a row), and there converted, one pass of a few rows after the other: straight code for all of
+                // them, run once an item, waited 9 us for its instructions.  The pair tells each other the exponents.
+                constexpr int PER = D / 8, ROWS = 32 / PER;               // lanes of a row, rows of a read
+                const int64_t mine = there ? static_cast<int64_t>(it.row0 + tok) * a.qs[0] + static_cast<int64_t>(head) * a.qs[1] : -1;
+                const __nv_bfloat16* const q = static_cast<const __nv_bfloat16*>(a.q);
+                const int c = lane % PER, r0 = 16 * half + lane / PER;    // 16 bytes of the row, first of the warp's 32 rows
+                uint8_t* const tile = smem + qt * C::Q_BYTES + (c >> 3) * C::SUB;
+                const int in_tile = (warp & 3) * 32;
+#pragma unroll 1
+                for (int i = 0; i < 16; i += ROWS) {
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, r0 + i);
+                    uint8_t* to = tile + sw128_offset(in_tile + r0 + i, c & 7);
+                    const bool on = at >= 0 && 8 * c < a.d;
+                    const __nv_bfloat16* from = q + at + 8 * c;
+                    if (vec_q) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(on ? from : q), "r"(on ? 16 : 0) : "memory");
+                    } else {
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<unsigned short*>(to)[e] = on ? reinterpret_cast<const unsigned short*>(from)[e] : static_cast<unsigned short>(0);
                     }
-                    return x;
-                };
-                uint32_t top = 0;
-                auto largest = [&](const uint4& x) {
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                int8_t* const exps = reinterpret_cast<int8_t*>(smem + C::OFF_EXP) + 32 * pair;
+#pragma unroll 1
+                for (int i = 0; i < 16; i += ROWS) {
+                    uint4* at = reinterpret_cast<uint4*>(tile + sw128_offset(in_tile + r0 + i, c & 7));   // this lane's own copy
+                    const uint4 x = *at;
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t top = 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
-                };
-                uint4 x[D / 16];
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) x[c] = piece(half * (D / 16) + c);
-#pragma unroll 4
-                for (int c = 0; c < D / 16; ++c) largest(piece((1 - half) * (D / 16) + c));
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) largest(x[c]);
-                int ex = top && top < 0x7f800000u ? static_cast<int>(top >> 23) - 127 - 7 : 0;
-                ex = min(max(ex, -126), 126);
-                const float up = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-                f_row = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-                uint8_t* tile = smem + qt * C::Q_BYTES;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const int c = half * (D / 16) + i;
-                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    for (int o = 1; o < PER; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    int ex = top && top < 0x7f800000u ? static_cast<int>(top >> 23) - 127 - 7 : 0;
+                    ex = min(max(ex, -126), 126);
+                    const float up = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
                     uint32_t y[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[e] = h2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-                    *reinterpret_cast<uint4*>(tile + (c >> 3) * C::SUB + sw128_offset(row, c & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    for (int e = 0; e < 4; ++e) y[e] = h2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+                    *at = make_uint4(y[0], y[1], y[2], y[3]);
+                    if (c == 0) exps[r0 + i] = static_cast<int8_t>(ex);
                 }
+                if (!(ok = meet())) break;
+                f_row = __uint_as_float(static_cast<uint32_t>(127 + exps[lane]) << 23);
                 fence_proxy_async_smem();
                 mbar_arrive(BAR(C::B_Q + qt));
             }
@@ -938,6 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                 const uint32_t tA = alt ? tmem + 256 + lanes : tO, tB = tmem + 384 + lanes;
                 __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + out_row * a.os[0] + static_cast<int64_t>(head) * a.os[1];
                 // four channels of all rows together: a warp's rows are written side by side
+                const bool wide_o = vec_o && ((reinterpret_cast<uintptr_t>(a.o) | 2 * a.os[0] | 2 * a.os[1]) & 31) == 0;   // 32 bytes at a time
                 float* part = pieces.part + static_cast<int64_t>(whole ? 0 : it.slot) * kRows * DV + 4 * (ri - it.i0);
                 // 32 columns at a time: two threads to a row, four with alt
 #pragma unroll 1
@@ -957,6 +965,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(u[i]), fb, x[i]);
                     }
                     if (!there) continue;
+                    if (whole && wide_o && cc * 32 + 32 <= a.dv) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                        st_global_v8(o + cc * 32, w);
+                        st_global_v8(o + cc * 32 + 16, w + 8);
+                        continue;
+                    }
                     if (!whole) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
