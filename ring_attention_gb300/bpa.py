@@ -430,25 +430,14 @@ def _leave(guard, other, dev, outs):
             t.record_stream(torch.cuda.current_stream(dev))
 
 
-class _call:
-    """One call on device number dev: (stream pointer, workspace) inside, what it makes listed in `made`."""
-
-    def __init__(self, dev, stream, workspace_buf, made):
-        _check_workspace(workspace_buf, dev)
-        self.dev, self.stream, self.ws, self.made = dev, stream, workspace_buf, made
-
-    def __enter__(self):
-        self.guard, ptr, self.other = _enter(self.dev, self.stream)
-        try:
-            if self.ws is None:
-                self.ws = _empty(256, dtype=_U8, device=torch.device("cuda", self.dev))
-        except BaseException:
-            self.__exit__()
-            raise
-        return ptr, self.ws
-
-    def __exit__(self, *_):
-        _leave(self.guard, self.other, self.dev, self.made)
+def _ints(device, outs, shapes, ws, made):
+    """The workspace; int32 tensors in the place of the None of outs.  (Parts of one buffer instead of tensors of their
+    own: measured, splitting it costs more than the allocations.)  The caller holds the workspace until it has launched."""
+    for i, t in enumerate(outs):
+        if t is None:
+            outs[i] = t = _empty(shapes[i], dtype=_I32, device=device)
+            made.append(t)
+    return _empty(256, dtype=_U8, device=device) if ws is None else ws
 
 
 def _masks(tree):
@@ -656,13 +645,14 @@ def bpa_cache_tree(parents, kv_lens, cu_q, *, words, tree=None, positions=None, 
     for t, name, shape in ((tree, "tree", (T, words)), (positions, "positions", (T,))):
         if t is not None:
             _i32_buffer(t, name, shape, dev)
+    _check_workspace(workspace_buf, dev)
     outs, made = [tree, positions], []
-    with _call(dev, stream, workspace_buf, made) as (ptr, ws):
-        for i, shape in enumerate(((T, words), (T,))):
-            if outs[i] is None:
-                outs[i] = _empty(shape, dtype=_I32, device=parents.device)
-                made.append(outs[i])
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        ws = _ints(parents.device, outs, ((T, words), (T,)), workspace_buf, made)
         st = lib().bpa_cache_tree(R, T, words, *ins, outs[0].data_ptr(), outs[1].data_ptr(), ws.data_ptr(), ws.numel(), ptr)
+    finally:
+        _leave(guard, other, dev, made)
     if st:
         _raise_if(st, "bpa_cache_tree")
     return outs[0], outs[1]
@@ -680,8 +670,15 @@ def bpa_cache_keep(keep, keep_count, kv_lens, cu_q, page_table, k_cache, v_cache
     ins = (_i32_buffer(keep_count, "keep_count", (R,), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
            _i32_buffer(cu_q, "cu_q", (R + 1,), dev), _i32_buffer(page_table, "page_table", (R, max_pages), dev))
     rows = _i32_buffer(keep, "keep", (R, max_keep), dev)
-    with _call(dev, stream, workspace_buf, ()) as (ptr, ws):
-        st = lib().bpa_cache_keep(cache, R, 1 << 30, max_pages, rows, max_keep, *ins, ws.data_ptr(), ws.numel(), ptr)
+    _check_workspace(workspace_buf, dev)
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        if workspace_buf is None:
+            workspace_buf = _empty(256, dtype=_U8, device=keep.device)
+        st = lib().bpa_cache_keep(cache, R, 1 << 30, max_pages, rows, max_keep, *ins, workspace_buf.data_ptr(), workspace_buf.numel(),
+                                  ptr)
+    finally:
+        _leave(guard, other, dev, ())
     if st:
         _raise_if(st, "bpa_cache_keep")
 
@@ -703,13 +700,13 @@ def bpa_cache_fork(src, dst, ctx_lens, page_table, page_refs, free_pages, free_c
     for t, name, shape in zip(outs, ("copy_src", "copy_dst", "ctx_lens_out", "free_count_out"), shapes):
         if t is not None:
             _i32_buffer(t, name, shape, dev)
-    with _call(dev, stream, workspace_buf, made) as (ptr, ws):
-        for i in range(4):
-            if outs[i] is None:
-                outs[i] = _empty(shapes[i], dtype=_I32, device=src.device)
-                made.append(outs[i])
-        st = lib().bpa_cache_fork(N, R, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs], ws.data_ptr(),
-                                  ws.numel(), ptr)
+    _check_workspace(workspace_buf, dev)
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        ws = _ints(src.device, outs, shapes, workspace_buf, made)
+        st = lib().bpa_cache_fork(N, R, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs], ws.data_ptr(), ws.numel(), ptr)
+    finally:
+        _leave(guard, other, dev, made)
     if st:
         _raise_if(st, "bpa_cache_fork")
     return tuple(outs)
@@ -722,8 +719,14 @@ def bpa_cache_copy(src, dst, k_cache, v_cache, k_scale, v_scale, *, workspace_bu
         raise ValueError("src must be [N]")
     N = src.shape[0]
     a, b = _i32_buffer(src, "src", (N,), dev), _i32_buffer(dst, "dst", (N,), dev)
-    with _call(dev, stream, workspace_buf, ()) as (ptr, ws):
-        st = lib().bpa_cache_copy(cache, N, a, b, ws.data_ptr(), ws.numel(), ptr)
+    _check_workspace(workspace_buf, dev)
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        if workspace_buf is None:
+            workspace_buf = _empty(256, dtype=_U8, device=src.device)
+        st = lib().bpa_cache_copy(cache, N, a, b, workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
+    finally:
+        _leave(guard, other, dev, ())
     if st:
         _raise_if(st, "bpa_cache_copy")
 
@@ -744,13 +747,13 @@ def bpa_cache_release(ctx_lens, keep_lens, page_table, page_refs, free_pages, fr
     for t, name, shape in zip(outs, ("ctx_lens_out", "free_count_out"), shapes):
         if t is not None:
             _i32_buffer(t, name, shape, dev)
-    with _call(dev, stream, workspace_buf, made) as (ptr, ws):
-        for i in range(2):
-            if outs[i] is None:
-                outs[i] = _empty(shapes[i], dtype=_I32, device=ctx_lens.device)
-                made.append(outs[i])
-        st = lib().bpa_cache_release(R, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs], ws.data_ptr(),
-                                     ws.numel(), ptr)
+    _check_workspace(workspace_buf, dev)
+    guard, ptr, other = _enter(dev, stream)
+    try:
+        ws = _ints(ctx_lens.device, outs, shapes, workspace_buf, made)
+        st = lib().bpa_cache_release(R, page_size, num_pages, max_pages, *ins, *[t.data_ptr() for t in outs], ws.data_ptr(), ws.numel(), ptr)
+    finally:
+        _leave(guard, other, dev, made)
     if st:
         _raise_if(st, "bpa_cache_release")
     return tuple(outs)
@@ -878,7 +881,7 @@ def bpa_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weight=N
     guard, ptr, other = _enter(dev, stream)
     made = []
     try:
-        grads, weights = [dq, dk], [None, None]
+        L, grads, weights = lib(), [dq, dk], [None, None]
         for i, t in enumerate((q, k)):
             if t is None:
                 continue
@@ -889,12 +892,12 @@ def bpa_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weight=N
                 weights[i] = _empty((t.shape[-1],), dtype=_F32, device=t.device)
                 made.append(weights[i])
         if workspace_buf is None:
-            need = lib().bpa_rope_workspace_size(desc)
+            need = L.bpa_rope_workspace_size(desc)
             if need == 0:
                 _raise_if(BPA_ERR_INVALID_ARG, "bpa_rope_workspace_size")
             workspace_buf = _empty(need, dtype=_U8, device=first.device)
-        st = lib().bpa_rope_bwd(desc, _ptr(dq_out), _ptr(dk_out), _ptr(grads[0]), _ptr(grads[1]), _ptr(weights[0]),
-                                _ptr(weights[1]), workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
+        st = L.bpa_rope_bwd(desc, _ptr(dq_out), _ptr(dk_out), _ptr(grads[0]), _ptr(grads[1]), _ptr(weights[0]), _ptr(weights[1]),
+                            workspace_buf.data_ptr(), workspace_buf.numel(), ptr)
     finally:
         _leave(guard, other, dev, made)
     if st:
