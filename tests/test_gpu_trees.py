@@ -83,7 +83,24 @@ def test_masks_report_what_does_not_fit(bpa):
 
 
 # ---- attention under a tree ------------------------------------------------------------------------------
+def takes_many_rows(c, dtype):
+    """Whether the kernel for many rows takes these shapes, if the page table has room for enough keys."""
+    (_, Hkv, P, d), dv, (T, Hq, _) = c["kc"].shape, c["vc"].shape[3], c["q"].shape
+    return dtype == torch.bfloat16 and d % 16 == 0 and dv % 16 == 0 and max(d, dv) <= 128 and dv <= max(d, 64) and P % 16 == 0 and \
+        c["max_q"] * Hq // Hkv > 32
+
+
 def run_under_tree(bpa, c, dtype, tree, sink=None, nhd=False, max_q=None, **kw):
+    """Once with a page table of just the pages, once (where that changes the kernel) with one of 2^18 tokens more."""
+    out = attend_under_tree(bpa, c, dtype, tree, sink, nhd, max_q, **kw)
+    if takes_many_rows(c, dtype) and max_q is None:
+        more = 2 ** 18 // c["kc"].shape[2]
+        roomy = {**c, "table": np.concatenate([c["table"], np.full((len(c["table"]), more), -1)], 1)}
+        return attend_under_tree(bpa, roomy, dtype, tree, sink, nhd, max_q, **kw)
+    return out
+
+
+def attend_under_tree(bpa, c, dtype, tree, sink=None, nhd=False, max_q=None, **kw):
     t, marker = on_gpu(c, dtype, nhd), 77.0
     T, Hq = c["q"].shape[:2]
     o = torch.full((T, Hq, c["vc"].shape[3]), marker, dtype=dtype, device="cuda")
@@ -183,7 +200,8 @@ def test_attention_under_trees_long_contexts_and_repeats(bpa, shape):
     rng = np.random.default_rng(11)
     c = make_step(rng, *shape, pad=1)
     tree = masks_for(rng, c, shape[1], 6)
-    first = run_under_tree(bpa, c, torch.bfloat16, tree)
+    c["table"] = np.concatenate([c["table"], np.full((len(c["table"]), 2 ** 14), -1)], 1)
+    first = attend_under_tree(bpa, c, torch.bfloat16, tree)
     t, dt = on_gpu(c, torch.bfloat16), i32(tree)
     outs = [torch.full_like(x, 77.0) for x in first]
     graph = torch.cuda.CUDAGraph()
@@ -201,13 +219,87 @@ def test_attention_under_trees_long_contexts_and_repeats(bpa, shape):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dims", [(64, 64), (128, 64), (128, 128), (112, 96)], ids=lambda d: f"{d[0]}_{d[1]}")
+def test_attention_under_trees_windows_of_many_rows(bpa, dims):
+    rng = np.random.default_rng(13)
+    new = [64, 33, 32, 60, 9]
+    c = make_step(rng, [1200, 900, 1700, 3, 2100], new, 32, 8, *dims, 64)
+    tree = masks_for(rng, c, new, 6)
+    for kw in (dict(window=(1000, -1)), dict(window=(1100, -1), sink=rng.standard_normal(32) * 3)):
+        run_under_tree(bpa, c, torch.bfloat16, tree, **kw)
+
+
+MANY = ([300, 5, 640, 127], [40, 20, 64, 33], 32, 8, 128, 128, 32)
+
+
+@pytest.mark.parametrize("first,later", [(1e-20, 1e15), (1e15, 1e-20), (1.0, 2.0 ** 45), (1.0, 2.0 ** -45)])
+def test_attention_under_trees_value_scales_far_apart(bpa, first, later):
+    rng = np.random.default_rng(14)
+    c = make_step(rng, *MANY)
+    tree = masks_for(rng, c, MANY[1], 4)
+    c["vs"] = c["vs"].copy()
+    for r in (0, 2):                              # the other requests' scales are alike
+        pages = c["table"][r][c["table"][r] >= 0]
+        c["vs"][pages[:4]] *= np.float32(first)
+        c["vs"][pages[4:]] *= np.float32(later)
+    run_under_tree(bpa, c, torch.bfloat16, tree)
+
+
+def test_attention_under_trees_pages_of_zeros_and_nan(bpa):
+    rng = np.random.default_rng(15)
+    c = make_step(rng, *MANY)
+    tree = masks_for(rng, c, MANY[1], 4)
+    for r, j in ((0, 2), (2, 0), (2, 7)):
+        page = c["table"][r, j]
+        c["vc"][page], c["vs"][page] = 0, 0
+    clean = run_under_tree(bpa, c, torch.bfloat16, tree)
+    bad = {**c, "kc": c["kc"].copy(), "vc": c["vc"].copy()}
+    bad["kc"][c["table"][0, 1], 1, 5, 7] = 0x7F       # a key of the context: every row of the request, kv head 1
+    bad["vc"][c["table"][2, 3], 2, 9, 11] = 0x7F      # a value: channel 11 of the rows of that request, kv head 2
+    bad["table"] = np.concatenate([bad["table"], np.full((4, 2 ** 14), -1)], 1)
+    t = on_gpu(bad, torch.bfloat16)
+    o, m, l = bpa.bpa_cache_attn(*t, max_q=64, tree=i32(tree))
+    torch.cuda.synchronize()
+    cu = c["cu"]
+    lost = torch.zeros_like(o, dtype=torch.bool)
+    lost[cu[0]:cu[1], 4:8] = True
+    lost[cu[2]:cu[3], 8:12, 11] = True
+    assert o[lost].isnan().all() and not o[~lost].isnan().any()
+    assert (o[~lost].float() - clean[0][~lost].float()).abs().max() <= 2.0 ** -7 * clean[0].float().abs().max()
+    assert l[4:8, cu[0]:cu[1]].isnan().all() and not l[:4].isnan().any()
+
+
+def test_attention_under_trees_scores_of_any_size(bpa):
+    rng = np.random.default_rng(16)
+    for qmag in (1e-6, 30.0, 1e4):
+        c = make_step(rng, *MANY, qmag=qmag)
+        run_under_tree(bpa, c, torch.bfloat16, masks_for(rng, c, MANY[1], 4))
+
+
+def test_attention_under_trees_odd_strides(bpa):
+    """Rows of q and o that are parts of wider ones, not aligned to 16 or 32 bytes; a cache of [pages, tokens, heads]."""
+    rng = np.random.default_rng(17)
+    c = make_step(rng, *MANY)
+    tree = masks_for(rng, c, MANY[1], 4)
+    c["table"] = np.concatenate([c["table"], np.full((4, 2 ** 14), -1)], 1)
+    want = attend_under_tree(bpa, c, torch.bfloat16, tree, nhd=True)[0]
+    t = list(on_gpu(c, torch.bfloat16))
+    T = t[0].shape[0]
+    for pad, off in ((1, 1), (8, 8), (3, 2)):
+        q = torch.zeros(T, 32, 128 + pad + off, dtype=torch.bfloat16, device="cuda")[..., off:off + 128]
+        q.copy_(t[0])
+        o = torch.zeros(T, 32, 128 + pad + off, dtype=torch.bfloat16, device="cuda")[..., off:off + 128]
+        got = bpa.bpa_cache_attn(q, *t[1:], max_q=64, tree=i32(tree), o=o)[0]
+        assert got is o and torch.equal(got, want)
+
+
 def test_attention_under_trees_reports_bad_pages(bpa):
     for shape in (([200, 0], [9, 1], 8, 2, 64, 64, 16), ([200, 80], [40, 65], 64, 16, 64, 64, 16), ([70, 0], [9, 1], 4, 2, 40, 24, 20)):
         rng = np.random.default_rng(12)
         c = make_step(rng, *shape)
         tree = masks_for(rng, c, shape[1], 5)
         for bad in (-1, 10 ** 8, c["kc"].shape[0]):
-            table = c["table"].copy()
+            table = np.concatenate([c["table"], np.full((2, 2 ** 14), -1)], 1)
             table[0, 2] = bad
             t = on_gpu({**c, "table": table}, torch.bfloat16)
             need = bpa.bpa_cache_attn_workspace_size(bpa.make_cache_desc(*t[1:5], torch.bfloat16),
