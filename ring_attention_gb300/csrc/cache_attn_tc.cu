@@ -56,7 +56,7 @@ constexpr float kFar = 40.f;          // log2: a scale further from the item's f
 constexpr float kZeros = 20.f, kAllZeros = -kFar - kZeros;   // log2 scale of a page of zeros: below the largest so far; before any
 
 struct TileMeta {
-    int key0, len, end, alt;
+    int key0, len, end;
     uint32_t zero;                    // bit c: the v scale of chunk c is 0
     float a[8], lv[8], e[8];          // k scale * softmax scale * log2(e); log2 v scale; 2^(lv0 - lv)
 };
@@ -296,29 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
         // ------------------------------------------------------------ codes -> fp16 tiles
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int wq = warp - kConv;
-        // half a tile from the ring to a K or V tile: rows of RB bytes, 16 bytes of a row at a time
+        // Half a tile from the ring to a K or V tile: rows of RB bytes, 16 bytes of a row at a time, four reads under way
+        // together.  Eight lanes in a row take two rows (RB 128: the halves of them that lie on other banks),
+        // whose swizzled units lie on other banks too, so that neither side has conflicts, and every address is a
+        // base and a constant.
         auto convert = [&](const uint8_t* raw, auto rb, uint8_t* tile, int left) {
-            constexpr int RB = decltype(rb)::value, PER = RB / 16, ROWS = 32 / PER;   // lanes of a row, rows of a warp's read
-            const int c = lane % PER, r = lane / PER, flip = c >> 2;                  // flip: the halves of a row on other banks
-            uint8_t* slab = tile + (c >> 2) * C::SUB;
-#pragma unroll 2
-            for (int i = 0; i < 32 / ROWS; ++i) {
-                const int row = 32 * wq + ROWS * i + r;
-                uint4 x = *reinterpret_cast<const uint4*>(raw + row * RB + 16 * c);
-                if (row >= left) x = make_uint4(0, 0, 0, 0);       // slots past the last token may hold anything
-                const uint4 lo = make_uint4(cvt_lo(x.x), cvt_hi(x.x), cvt_lo(x.y), cvt_hi(x.y));
-                const uint4 hi = make_uint4(cvt_lo(x.z), cvt_hi(x.z), cvt_lo(x.w), cvt_hi(x.w));
-                *reinterpret_cast<uint4*>(slab + sw128_offset(row, (c & 3) * 2 + flip)) = flip ? hi : lo;
-                *reinterpret_cast<uint4*>(slab + sw128_offset(row, (c & 3) * 2 + 1 - flip)) = flip ? lo : hi;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
-        // The same in fewer instructions, four reads at a time: where the conversion is what a tile waits for (even and odd
-        // key tiles apart: 172 us against 191 for 19 requests of 128 rows, 8,192 tokens).  With 256 rows it takes the shared memory from the
-        // products at the wrong time: 235 us against 222.  Eight lanes in a row take two rows (RB 128: the halves of them that lie on other banks), whose swizzled units lie on
-        // other banks too, so that neither side has conflicts, and every address is a base and a constant.
-        auto convert_fast = [&](const uint8_t* raw, auto rb, uint8_t* tile, int left) {
             constexpr int RB = decltype(rb)::value, STEP = RB == 128 ? 4 : 8;         // rows of a warp's read
             const int c = lane & 3, p = lane >> 2 & 1, q = lane >> 4;
             const int slab = RB == 128 ? (lane >> 3 & 1) ^ p : 0, r = RB == 128 ? 2 * q + p : lane >> 2;
@@ -354,13 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             const int st = t % C::NS, use = t / C::NS, sl = t % kMetas;
             if (!wait(C::B_MF + sl, t / kMetas, 0xE0) || metas[sl].end) break;
             const int left = metas[sl].len - metas[sl].key0;
-            const bool alt = TREE && metas[sl].alt;
             const uint32_t zero = metas[sl].zero >> (2 * wq) & 3;   // this warp's two 16 rows
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_ME + sl));
             if (!wait(C::B_RF, t, 0xE1) || (use > 0 && !wait(C::B_KE + st, use - 1, 0xE2))) break;
-            if (alt) convert_fast(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
-            else convert(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
+            convert(smem + C::OFF_RAW, std::integral_constant<int, C::RBK>(), smem + C::OFF_K + st * C::K_BYTES, left);
             if (lane == 0) {
                 mbar_arrive(BAR(C::B_KF + st));
                 mbar_arrive(BAR(C::B_RE));
@@ -375,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                     }
                 __syncwarp();
             }
-            if (alt) convert_fast(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
-            else convert(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
+            convert(smem + C::OFF_RAW + C::RAW, std::integral_constant<int, C::RBV>(), smem + C::OFF_V + st * C::V_BYTES, left);
             if (lane == 0) {
                 mbar_arrive(BAR(C::B_VF + st));
                 mbar_arrive(BAR(C::B_RE + 1));
@@ -613,7 +592,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         m->key0 = (first + j) * BN;
                         m->len = rq.len;
                         m->end = 0;
-                        m->alt = TREE && rq.n * a.G - i0 <= 128;
                         m->zero = zero;
                     }
                     __syncwarp();
@@ -648,31 +626,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             if (TREE && lane == 0) pieces.recs[blockIdx.x] = own.rec;
         } else if (warp == kMma) {
             // -------------------------------------------------------- MMA issuer
+            // One thread (the elected one) waits, issues and commits: with the whole warp in step and a lane elected for
+            // each product, eight of them took 800 cycles.
+            uint32_t leader;
+            asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(leader));
+            if (leader) {
+            auto wait = [&](int b, int parity, uint32_t where) { return mbar_wait(BAR(b), parity & 1, abort, a.status, where); };
             int t = 0, np[2] = {0, 0}, seen[2] = {0, 0};   // key tiles; W tiles used, items with work, per row tile
             bool ok = true;
             for (int k = 0; ok; ++k) {
                 if (!wait(C::B_IF + (k & 1), k >> 1, 0xE7)) break;
                 const Item it = items[k & 1];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(C::B_IE + (k & 1)));
+                mbar_arrive(BAR(C::B_IE + (k & 1)));
                 if (!it.valid) break;
                 if (it.tiles == 0) continue;
                 const int two = it.n * a.G - it.i0 > 128 ? 2 : 1;
                 auto issue_s = [&](int i, int pos) {
                     const uint64_t qd = sdesc_sw128(sb + i * C::Q_BYTES, 16, 1024);
                     const uint64_t kd = sdesc_sw128(sb + C::OFF_K + pos % C::NS * C::K_BYTES, 16, 1024);
-#pragma unroll 4
+#pragma unroll 2
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::SUB + (kk & 3) * 32;
-                        tc_mma_ss_w(tmem + i * BN, sdesc_advance(qd, off), sdesc_advance(kd, off), C::IDESC_S, kk > 0);
+                        tc_mma_ss(tmem + i * BN, sdesc_advance(qd, off), sdesc_advance(kd, off), C::IDESC_S, kk > 0);
                     }
-                    tc_commit_w(BAR(C::B_S + i));
+                    tc_commit(BAR(C::B_S + i));
                 };
                 auto issue_pv = [&](int i, int pos, bool first) {
                     const uint64_t vd = sdesc_sw128(sb + C::OFF_V + pos % C::NS * C::V_BYTES, C::SUB, 1024);
-#pragma unroll 4
+#pragma unroll 2
                     for (int kk = 0; kk < BN / 16; ++kk)       // the weights of 64 keys lie over the first half of their scores
-                        tc_mma_ts_w(tmem + 256 + i * 128, tmem + i * BN + kk * 8 + (kk >> 2) * 32, sdesc_advance(vd, kk * 2048), C::IDESC_PV,
+                        tc_mma_ts(tmem + 256 + i * 128, tmem + i * BN + kk * 8 + (kk >> 2) * 32, sdesc_advance(vd, kk * 2048), C::IDESC_PV,
                                     (!first || kk > 0) ? 1u : 0u);
                 };
                 if (TREE && it.alt) {
@@ -683,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         if (!ok) break;
                         tc_fence_after();
                         issue_s(i, t + i);
-                        tc_commit_w(BAR(C::B_KE + (t + i) % C::NS));
+                        tc_commit(BAR(C::B_KE + (t + i) % C::NS));
                     }
                     for (int j = 0; ok && j < it.tiles; ++j, ++t) {
                         const int i = j & 1;
@@ -692,13 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         ++np[i];
                         tc_fence_after();
                         issue_pv(i, t, j < 2);
-                        tc_commit_w(BAR(C::B_VE + t % C::NS));
-                        if (j + 2 >= it.tiles) tc_commit_w(BAR(C::B_O + i));
+                        tc_commit(BAR(C::B_VE + t % C::NS));
+                        if (j + 2 >= it.tiles) tc_commit(BAR(C::B_O + i));
                         if (j + 2 < it.tiles) {
                             if (!(ok = wait(C::B_KF + t % C::NS, t / C::NS + 1, 0xED))) break;
                             tc_fence_after();
                             issue_s(i, t + 2);
-                            tc_commit_w(BAR(C::B_KE + t % C::NS));
+                            tc_commit(BAR(C::B_KE + t % C::NS));
                         }
                     }
                     for (int i = 0; i < both; ++i) ++seen[i];
@@ -716,10 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         // O of the previous item has been read before the first product of this one
                         if (j == 0 && seen[i] > 0 && !(ok = wait(C::B_OE + i, seen[i] - 1, 0xEC))) break;
                         ++np[i];
-                        if (i == two - 1) tc_commit_w(BAR(C::B_KE + t % C::NS));   // S(j) is complete
+                        if (i == two - 1) tc_commit(BAR(C::B_KE + t % C::NS));   // S(j) is complete
                         tc_fence_after();
                         issue_pv(i, t, j == 0);
-                        if (j == it.tiles - 1) tc_commit_w(BAR(C::B_O + i));
+                        if (j == it.tiles - 1) tc_commit(BAR(C::B_O + i));
                         if (j + 1 < it.tiles) {
                             if (i == 0) {
                                 if (!(ok = wait(C::B_KF + (t + 1) % C::NS, (t + 1) / C::NS, 0xED))) break;
@@ -729,14 +712,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         }
                     }
                     if (!ok) break;
-                    tc_commit_w(BAR(C::B_VE + t % C::NS));
+                    tc_commit(BAR(C::B_VE + t % C::NS));
                 }
                 for (int i = 0; i < two; ++i) ++seen[i];
             }
             // every product issued is complete before TMEM is freed
-            tc_commit_w(BAR(C::B_FIN));
+            tc_commit(BAR(C::B_FIN));
             int never = 0;
             mbar_wait(BAR(C::B_FIN), 0, &never, a.status, 0xEE);
+            }
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------------------ softmax: two threads own a row, 64 columns each
