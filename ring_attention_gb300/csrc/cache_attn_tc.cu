@@ -68,6 +68,24 @@ struct Item {
 using cache_mma::Pieces;
 using cache_mma::Rec;
 
+// mbar_wait with what is done seldom in a function of its own: the roles' loops have to stay in the instruction caches.
+// 0: give up.
+__device__ __noinline__ uint64_t give_up(uint64_t t0, volatile int* abort, uint32_t* status, uint32_t where) {
+    const uint64_t now = globaltimer();
+    if (*abort) return 0;
+    if (t0 == 1) return now;
+    if (now - t0 <= kWaitLimitNs) return t0;
+    *abort = 1;
+    report(status, ST_TIMEOUT, where);
+    return 0;
+}
+BPA_DEV bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status, uint32_t where) {
+    uint64_t t0 = 1;
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
+        if ((it & 63u) == 0 && (t0 = give_up(t0, abort, status, where)) == 0) return false;
+    return true;
+}
+
 template <int D, int DV>
 struct Cfg {
     static constexpr int SUB = 128 * 128;                        // a slab of 64 fp16 columns x 128 rows
@@ -289,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](int b, int parity, uint32_t where) {
-        return __all_sync(0xffffffffu, mbar_wait(BAR(b), parity & 1, abort, a.status, where)) != 0;
+        return __all_sync(0xffffffffu, bounded_wait(BAR(b), parity & 1, abort, a.status, where)) != 0;
     };
 
     if (warp >= kConv) {
@@ -324,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         make_uint4(cvt_lo(x[i].z), cvt_hi(x[i].z), cvt_lo(x[i].w), cvt_hi(x[i].w));
                 }
             };
-#pragma unroll
+#pragma unroll 1
             for (int i0 = 0; i0 < 32 / STEP; i0 += 4) {
                 if (32 * wq + 32 > left) four(i0, std::true_type());
                 else four(i0, std::false_type());
@@ -631,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             uint32_t leader;
             asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(leader));
             if (leader) {
-            auto wait = [&](int b, int parity, uint32_t where) { return mbar_wait(BAR(b), parity & 1, abort, a.status, where); };
+            auto wait = [&](int b, int parity, uint32_t where) { return bounded_wait(BAR(b), parity & 1, abort, a.status, where); };
             int t = 0, np[2] = {0, 0}, seen[2] = {0, 0};   // key tiles; W tiles used, items with work, per row tile
             bool ok = true;
             for (int k = 0; ok; ++k) {
