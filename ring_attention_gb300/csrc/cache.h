@@ -15,7 +15,7 @@ namespace bpa {
 // 230.  Pieces of prompts (thousands of rows) take 1,540 us there and 7.1 ms here.
 constexpr int kFewRows = 64;
 // The same under a tree, where the tensor cores share out keys as well: 19 requests of 8,192 tokens, 4 q heads a kv
-// head, 128 channels; 64 rows 172 us there and 249 here, 32 rows 172 and 142.
+// head, 128 channels; 64 rows 138 us there and 249 here, 32 rows 137 and 142.
 constexpr int kFewTreeRows = 32;
 constexpr int kPlanMaxR = 8192;      // requests of one plan: their lengths and offsets sit in shared memory
 constexpr int kMaxTreeWords = 32;    // words of a row's mask: 1,024 rows of a request

@@ -1133,14 +1133,14 @@ bool cache_attn_tc_takes(const CacheAttnArgs& a) {
     if (a.tree) {
         // Items are cut between CTAs, so the rows may be few; what counts is the work, in products of 64 rows with 128
         // keys of 256 channels.  Measured (this kernel and the other one alone, us, 4 q heads on each of 8 kv heads,
-        // 128 + 128 channels): with 104 rows a request 512 of them 36.7 and 28.2, 832 39.0 and 46.0, 832 46.8 and 52.5;
-        // 256 rows 512 of them 40.9 and 37.5, 1,024 43.1 and 51.5; but 40 and 60 rows, most of which leaves a row tile of
-        // 128 empty, 1,320 89.6 and 78.7, 3,960 129.8 and 128.9, 5,280 193 and 221; 33 requests of 8 to 120 rows,
-        // window 1,024, 64 + 64 channels, 1,215 of them 90 and 76.
+        // 128 + 128 channels): 104 rows a request, 416 of them 32.8 and 34.9, 36.9 and 34.6, 832 35.9 and 46.0; 256 rows, 512 of
+        // them 38.9 and 37.5, 1,024 41.0 and 51.4; but 40 and 60 rows, which leave most of a row tile of 128 empty, 660
+        // 52.0 and 47.9, 990 59.3 and 55.4, 1,320 72.4 and 78.5, 1,980 73.5 and 81.8; 33 requests of 8 to 120 rows, window 1,024,
+        // 64 + 64 channels, 1,215 of them 80.6 and 75.5.
         int64_t keys = static_cast<int64_t>(a.max_pages) * a.P;
         if (a.wl >= 0) keys = std::min(keys, static_cast<int64_t>(a.wl) + a.max_q + BN);
         const double work = static_cast<double>(a.T) * a.G / 64 * a.Hkv * keys / 128 * (a.d + a.dv) / 256;
-        return work >= (static_cast<int64_t>(a.T) * a.G >= 96 * static_cast<int64_t>(a.R) ? 700 : 3500);
+        return work >= (static_cast<int64_t>(a.T) * a.G >= 96 * static_cast<int64_t>(a.R) ? 500 : 1300);
     }
     // An item's keys are not shared between CTAs here, as they are in the kernel for few rows: with few
     // items (one token of 128 heads over a long context) that one fills the GPU and this one does not.
