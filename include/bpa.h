@@ -305,7 +305,7 @@ typedef struct bpa_rope_desc {
     int64_t qo_strides[3];     /* ... of q_out and dq_out */
     int64_t ko_strides[3];     /* ... of k_out and dk_out */
     const int32_t* positions;  /* [B, S], contiguous, or NULL: s */
-    const float* inv_freq;     /* [rot / 2] radians per position */
+    const float* inv_freq;     /* [rot / 2] radians per position, finite, below 2^32 in magnitude */
     const float* q_weight;     /* [d] or NULL (ones); only with norm */
     const float* k_weight;
 } bpa_rope_desc;

@@ -17,12 +17,19 @@
 // have no scale of their own: they count 2^-20 below the largest met so far, so their keys stay in L (far
 // below, W would leave float32's range) and do not push the others' W out of fp16's.
 //
-// Bounded by the softmax's instructions and the exponentials beside the products (compute, not
-// bytes): about three instructions and one exponential a score.  Two threads share a row (64 columns
-// each), so sixteen warps work on the softmax and cover each other's latencies; its loops stay rolled,
-// since unrolled ones kept the warps waiting for instructions.  Five pieces of prompts, 6,852 rows of 32
-// heads over up to 16,000 tokens, 128 channels: 1,540 us, 917 TFLOP/s (2,222 us with a thread to a row
-// and unrolled loops; 1,738 with eight converting warps; the kernel for few rows 7,225).
+// Bounded by the chain from scores to weights and back through the products (compute, not bytes): about
+// three instructions and one exponential a score, and the products' operands and the conversion share the
+// shared memory's ports.  Two threads share a row (64 columns each), so sixteen warps work on the softmax and
+// cover each other's latencies.  Its loops stay rolled, code that runs once an item too, and what waits seldom
+// do is a function of its own: the roles' code has to stay in the instruction caches (straight code for an item's
+// rows of q waited 9 us for its instructions).  One thread issues all products (eight of them took a whole warp
+// that elects a lane for each 800 cycles, 1,539 us for the prompts below).  Five pieces of prompts, 6,852 rows of 32
+// heads over up to 16,000 tokens, 128 channels: 1,339 us, 1,055 TFLOP/s (the kernel for few rows 7,225).
+//
+// Trees of drafted tokens (TREE): the keys of the step are seen by mask, and as a step has few rows and long contexts, items
+// are cut between CTAs by cost; their pieces go to the workspace for the join of cache_attn_mma.cuh.  32 requests of 8 to 64
+// rows, 4 q heads on each of 8 kv heads, 200 to 8,191 tokens: 208 us in all (529 TFLOP/s; the kernel for few rows 720); two
+// of 64 rows over 100,000 and more 281 us, 808 TFLOP/s (1,486).
 // Roles (768 threads; registers moved to the softmax by setmaxnreg):
 //   warps 0-7, 8-15  softmax of row tile 0, 1; of eight warps the second four take columns 64-127.  They
 //                    also bring their rows of Q into shared memory

@@ -8,7 +8,9 @@
 // A warp per request, head and tensor, pages and tokens in ascending order.  A token never moves up
 // (keep[i] >= i), so a place that is written has been read, whether its token went elsewhere or stays: the
 // sources of later tokens lie behind it, and the pages that they come from keep their scales until then.
-// Bounded by the latency of a warp's chain (lengths, path, page ids, scales, codes).
+// Bounded by the latency of a warp's chain (lengths, path, page ids, scales, codes, page after page): 4 requests of 8
+// heads 7.4 us with the status word's clearing (1.5), 256 requests with paths of up to 30 tokens over pages of 16
+// 12.6 us, in which it moves 6 MB.
 #include "cache.h"
 #include "common.cuh"
 #include "e4m3.cuh"

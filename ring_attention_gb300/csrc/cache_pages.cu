@@ -7,8 +7,10 @@
 // order the counts were taken in.
 //
 // fork and release are one cluster of eight blocks each: the first half reads everything that the second
-// half may overwrite, with the cluster's barrier between.  Bounded by latency.  copy: a block per page, head
-// and tensor.
+// half may overwrite, with the cluster's barrier between.  Bounded by latency: 256 forks of 32 parents 8.4 us, the
+// release of 256 requests out of a pool of 18,000 pages 10.3 us, of a few 6.3 and 6.7 (with cold caches).
+// copy: a block per page, head and tensor; 256 pages of 32 tokens x 8 heads x (128 + 128) channels 7.5 us, 4.5 TB/s
+// there and 4.5 back.
 #include <cooperative_groups.h>
 
 #include "cache.h"
@@ -177,6 +179,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_release(const ReleaseArgs a)
     const int64_t first = (static_cast<int64_t>(rank) * 32 + warp) * stretch;
     const int last = static_cast<int>(min(first + stretch, static_cast<int64_t>(a.num_pages)));
     int mine = 0;
+#pragma unroll 4
     for (int64_t b = first; b < last; b += 32) {
         const int v = b + lane < last ? __ldcg(a.refs + b + lane) : 0;
         mine += __popc(__ballot_sync(0xffffffffu, v < 0));

@@ -3,7 +3,9 @@
 //   mask(i) = {i} and mask(parent(i));  position(i) = context + (number of i's ancestors among the drafts).
 //
 // A block per request: its parents in shared memory, a thread per row and word of a mask walks from the row
-// to its root.  Bounded by latency (lengths, then parents, then a walk as deep as the tree).
+// to its root.  Bounded by latency (lengths, then parents, then a walk as deep as the tree): 32 trees of 8 to 64
+// rows 4.0 us, one of 26 rows 3.7, and 1.5 for clearing the status word in front (a step pays both once, its
+// layers share the masks).
 #include "cache.h"
 #include "common.cuh"
 
@@ -44,9 +46,10 @@ __global__ void __launch_bounds__(kThreads) k_cache_tree(const TreeArgs a) {
         if (w == 0 && a.positions) a.positions[row0 + i] = ok ? len - n + above : -1;
     }
     // rows of no request
-    const int first = min(max(a.cu_q[0], 0), a.T), last = min(max(a.cu_q[a.R], 0), a.T), out = first + a.T - last;
-    for (int x = r * kThreads + threadIdx.x; x < out; x += a.R * kThreads) {
-        const int t = x < first ? x : last + x - first;
+    const int first = min(max(a.cu_q[0], 0), a.T), last = min(max(a.cu_q[a.R], 0), a.T);
+    const int64_t out = static_cast<int64_t>(first) + a.T - last;
+    for (int64_t x = static_cast<int64_t>(r) * kThreads + threadIdx.x; x < out; x += static_cast<int64_t>(a.R) * kThreads) {
+        const int t = static_cast<int>(x < first ? x : last + x - first);
         for (int w = 0; w < a.words; ++w) a.tree[static_cast<int64_t>(t) * a.words + w] = 0;
         if (a.positions) a.positions[t] = -1;
     }
