@@ -457,8 +457,8 @@ bpa_status bpa_cache_tree(int32_t R, int32_t T, int32_t words, const int32_t* pa
  *   own, where tokens in front of the step's lie in it, and those of the pages that its kept
  *   tokens come from, as they were before the call; codes from a smaller scale become e4m3(code * (old / scale))
  *   (0 / 0 counts as 1).  Places behind the last kept token hold what they held, whatever it now stands for.
- *   What the caller then does: new lengths kv_lens - n + keep_count, and bpa_cache_release for the pages
- *   that this leaves over.
+ *   What the caller then does: new lengths kv_lens - n + keep_count (a request that waits, kv_lens 0, has
+ *   keep_count 0 and keeps its length), and bpa_cache_release for the pages that this leaves over.
  * The pages that are written must be the request's own (those of bpa_cache_plan and bpa_cache_fork are).  A count
  * outside [0, min(n, max_keep)], entries that do not ascend within [0, n), a length or a page id that
  * does not fit: BPA_ERR_DEVICE_CHECK, the request is left alone.
