@@ -256,3 +256,38 @@ def test_forked_requests_go_on_by_themselves(bpa):
         torch.cuda.synchronize()
         same([x.cpu().numpy() for x in (dctx, drefs, dfree, dcount)], (ctx, refs, free, [count]))
     assert count == num and sorted(free.tolist()) == list(range(num))
+
+
+def test_fork_copy_and_release_in_a_captured_graph(bpa):
+    """A prompt sampled twice and both samples over, again and again in place: the pages come back each time."""
+    rng = np.random.default_rng(8)
+    P = 16
+    c = state_of(rng, [41], P, 6, 2)
+    kc, ks = random_cache(rng, len(c["free"]), 2, P, 32)
+    t = [torch.from_numpy(x).cuda() for x in (kc, kc, ks, ks)]
+    ctx, table, refs, free, count = i32(c["ctx"]), i32(c["table"]), i32(c["refs"]), i32(c["free"]), i32([c["count"]])
+    src, dst, keep = i32([0, 0]), i32([1, 2]), i32([41, 0, 0])
+
+    def step():
+        a, b, after, _ = bpa.bpa_cache_fork(src, dst, ctx, table, refs, free, count, page_size=P, free_count_out=count)
+        bpa.bpa_cache_copy(a, b, *t)
+        bpa.bpa_cache_release(after, keep, table, refs, free, count, page_size=P, free_count_out=count)
+        return a, b, after
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(4):
+        graph.replay()
+    torch.cuda.synchronize()
+    state = dict(c)
+    for _ in range(5):
+        a, b, after, tab, r, left = ora.fork([0, 0], [1, 2], **state)
+        for x in (kc, ks):
+            x[b] = x[a]
+        _, r, f, left = ora.release(after, [41, 0, 0], tab, r, state["free"], left, P)
+        state = dict(state, table=tab, refs=r, free=f, count=left)
+    same([x.cpu().numpy() for x in (*outs, table, refs, free, count)], (a, b, after, state["table"], state["refs"], state["free"], [state["count"]]))
+    same([x.cpu().numpy() for x in t], (kc, kc, ks, ks))

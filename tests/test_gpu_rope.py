@@ -289,3 +289,44 @@ def test_no_rows(bpa):
     assert a.shape == q.shape and b.shape == k.shape
     dq, dk, wq, wk = bpa.bpa_rope_bwd(q, k, a, b, None, freq)
     assert dq.shape == q.shape and (wq == 0).all() and (wk == 0).all()
+
+
+def torch64(x, w, freq, eps, inter):
+    """The forward pass in 64 bits on the GPU, positions 0, 1, .., for sizes that the oracle is slow at."""
+    x = x.double()
+    x = x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * w.double()
+    t = torch.arange(x.shape[1], device="cuda").double()[:, None] * freq.double()
+    c, s, n = t.cos()[:, None], t.sin()[:, None], freq.numel()
+    a, b = (x[..., 0:2 * n:2], x[..., 1:2 * n:2]) if inter else (x[..., :n], x[..., n:2 * n])
+    u, v = a * c - b * s, b * c + a * s
+    return torch.cat([torch.stack([u, v], -1).flatten(-2) if inter else torch.cat([u, v], -1), x[..., 2 * n:]], -1)
+
+
+@pytest.mark.parametrize("dtype,d,rot,inter", [(torch.bfloat16, 128, 128, False), (torch.bfloat16, 64, 32, True), (torch.bfloat16, 256, 64, False),
+                                               (torch.float32, 80, 80, False), (torch.bfloat16, 72, 36, False)])
+def test_many_rows_and_heads(bpa, dtype, d, rot, inter):
+    """Rows and heads enough for chunks of several rounds and several items a warp; ragged ends of both."""
+    q, k = inputs(1, 2, 2501, 37, d, dtype).cuda(), inputs(2, 2, 2501, 5, d, dtype).cuda()
+    w, freq = (1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(6))).cuda(), freqs(rot).cuda()
+    out = bpa.bpa_rope_fwd(q, k, None, freq, w, w, eps=1e-5, interleaved=inter)
+    for x, got in zip((q, k), out):
+        want = torch64(x, w, freq, 1e-5, inter)
+        flat = torch64(x, w, freq * 0, 1e-5, inter).abs()
+        n = rot // 2
+        pair = flat.clone()
+        if inter:
+            pair[..., 0:rot:2] = pair[..., 1:rot:2] = flat[..., 0:rot:2] + flat[..., 1:rot:2]
+        else:
+            pair[..., :n] = pair[..., n:rot] = flat[..., :n] + flat[..., n:rot]
+        assert ((got.double() - want).abs() <= 24 * U * pair + half(dtype) * want.abs() + 1e-38).all()
+    dy = inputs(3, 2, 2501, 37, d, dtype, 0.1).cuda()
+    x64, w64 = q.double().requires_grad_(), w.double().requires_grad_()
+    want, want_w = torch.autograd.grad(torch64(x64, w64, freq, 1e-5, inter), [x64, w64], dy.double())
+    dx, _, dw, _ = bpa.bpa_rope_bwd(q, None, dy, None, None, freq, w, eps=1e-5, interleaved=inter)
+    r = 1 / (q.double().pow(2).mean(-1, keepdim=True) + 1e-5).sqrt()
+    e, xh = dy.double().abs().amax(-1, keepdim=True) * 2 * w.double().abs(), q.double().abs() * r
+    tol = 96 * U * r * (e + xh * (e * xh).mean(-1, keepdim=True)) + half(dtype) * want.abs() + 1e-38
+    assert ((dx.double() - want).abs() <= tol).all()
+    # a sum of n terms in float32, at most 1,024 of them one after the other in a lane, then 4 + 5 + 7 levels
+    most = (48 + 1024 + 16) * U * (e * xh).sum((0, 1, 2)) + U * want_w.abs()
+    assert ((dw.double() - want_w).abs() <= most).all()

@@ -293,6 +293,48 @@ def test_attention_under_trees_odd_strides(bpa):
         assert got is o and torch.equal(got, want)
 
 
+GROUPS = [   # ctx, new, Hq, Hkv, d, dv, P: heads of their own, many heads to one, more requests than a warp looks at together
+    ([300, 20, 700], [64, 33, 40], 6, 6, 64, 64, 16), ([200, 90], [9, 4], 64, 1, 128, 128, 64), ([100, 260], [5, 3], 128, 2, 64, 64, 32),
+    ([int(x) for x in np.random.default_rng(18).integers(0, 150, 70)], [1 + (i * 7) % 40 for i in range(70)], 2, 1, 64, 64, 16),
+]
+
+
+@pytest.mark.parametrize("case", GROUPS, ids=lambda c: f"R{len(c[0])}_H{c[2]}_{c[3]}")
+def test_attention_under_trees_groups_and_many_requests(bpa, case):
+    rng = np.random.default_rng(19)
+    c = make_step(rng, *case)
+    run_under_tree(bpa, c, torch.bfloat16, masks_for(rng, c, case[1], 3))
+
+
+def test_attention_under_trees_rows_in_front_of_the_first_request(bpa):
+    rng = np.random.default_rng(22)
+    c = make_step(rng, *MANY, pad=2)
+    tree = masks_for(rng, c, MANY[1], 4)
+    front = 5
+    c["q"] = np.concatenate([rng.standard_normal((front,) + c["q"].shape[1:]), c["q"]])
+    c["cu"] = c["cu"] + front
+    tree = np.concatenate([np.full((front, tree.shape[1]), -1), tree])
+    run_under_tree(bpa, c, torch.bfloat16, tree)
+
+
+def test_two_calls_under_trees_at_once(bpa):
+    """Two streams, a workspace each: the answers of calls made one after the other, on both kernels."""
+    for room in (0, 2 ** 14):
+        cs = [make_step(np.random.default_rng(23 + i), *MANY) for i in range(2)]
+        trees = [i32(masks_for(np.random.default_rng(25), c, MANY[1], 4)) for c in cs]
+        for c in cs:
+            c["table"] = np.concatenate([c["table"], np.full((4, room), -1)], 1)
+        ts = [on_gpu(c, torch.bfloat16) for c in cs]
+        want = [bpa.bpa_cache_attn(*t, max_q=64, tree=m) for t, m in zip(ts, trees)]
+        torch.cuda.synchronize()
+        side = [torch.cuda.Stream() for _ in range(2)]
+        for _ in range(20):
+            got = [bpa.bpa_cache_attn(*t, max_q=64, tree=m, stream=s) for t, m, s in zip(ts, trees, side)]
+            torch.cuda.synchronize()
+            for x, y in zip(got, want):
+                assert all(torch.equal(u, v) for u, v in zip(x, y))
+
+
 def test_attention_under_trees_reports_bad_pages(bpa):
     for shape in (([200, 0], [9, 1], 8, 2, 64, 64, 16), ([200, 80], [40, 65], 64, 16, 64, 64, 16), ([70, 0], [9, 1], 4, 2, 40, 24, 20)):
         rng = np.random.default_rng(12)
