@@ -240,8 +240,10 @@ BPA_DEV uint64_t seen_from(const TreeRow& t, int k0, int len) {
 // Trees: items are cut between CTAs.  Each takes an equal share of the cost of all items (a key tile counts what its
 // rows take, an item's start and end kExtra), as in the kernel for few rows, and leaves pieces of items
 // for the same join.  An item of up to 128 rows has its even key tiles on one row tile and its odd ones on the other, the same rows on
-// both, so that all warps work; they are added up at its end.
-constexpr int kTwo = 4, kAlt = 3, kExtra = 8;
+// both, so that all warps work; they are added up at its end.  Measured: a tile of 256 rows 2.3 us, one of 128 1.75, an item's
+// start and end about 10 (kExtra 4, 8, 14 and 20: 32 requests of 64 rows over 200 to 8,191 tokens 248, 240, 218 and 205 us,
+// those of 8 to 64 rows 214, 203, 193 and 194).
+constexpr int kTwo = 4, kAlt = 3, kExtra = 18;
 struct Cut {                          // of an item: first key tile, tiles (at least one), what a tile counts for
     int first, n, each;
     bool keys;                        // no: the one tile is none
