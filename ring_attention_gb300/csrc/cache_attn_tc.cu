@@ -28,8 +28,8 @@
 //
 // Trees of drafted tokens (TREE): the keys of the step are seen by mask, and as a step has few rows and long contexts, items
 // are cut between CTAs by cost; their pieces go to the workspace for the join of cache_attn_mma.cuh.  32 requests of 8 to 64
-// rows, 4 q heads on each of 8 kv heads, 200 to 8,191 tokens: 208 us in all (529 TFLOP/s; the kernel for few rows 720); two
-// of 64 rows over 100,000 and more 281 us, 808 TFLOP/s (1,486).
+// rows, 4 q heads on each of 8 kv heads, 200 to 8,191 tokens: 199 us in all (555 TFLOP/s; the kernel for few rows 720); two
+// of 40 and 64 rows over 100,000 and more 277 us, 817 TFLOP/s (1,486).
 // Roles (768 threads; registers moved to the softmax by setmaxnreg):
 //   warps 0-7, 8-15  softmax of row tile 0, 1; of eight warps the second four take columns 64-127.  They
 //                    also bring their rows of Q into shared memory
