@@ -444,10 +444,18 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
  * Rows of a request that waits (kv_lens 0, from bpa_cache_plan) and rows of no request get masks of 0 and
  * positions -1.  A parent that is none (below -1, or not in front of its row) counts as -1; a
  * request with more rows than tokens or than 32 * words gets masks of 0 and positions -1: both are
- * BPA_ERR_DEVICE_CHECK.  1 <= words <= 32.  Workspace: 256 bytes (the status word). */
+ * BPA_ERR_DEVICE_CHECK.  1 <= words <= 32.  Workspace: 256 bytes (the status word).
+ *   These are the masks of attention without a window; for bpa_cache_attn with one, bpa_cache_tree_window. */
 bpa_status bpa_cache_tree(int32_t R, int32_t T, int32_t words, const int32_t* parents, const int32_t* kv_lens,
                           const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/* The same for attention under a sliding window: of a row's ancestors those up to window_left steps above it
+ * are in its mask (-1: all, as bpa_cache_tree).  positions count all of them.  Masks belong to a window: layers of
+ * different ones, or of none, need masks of their own. */
+bpa_status bpa_cache_tree_window(int32_t R, int32_t T, int32_t words, int32_t window_left, const int32_t* parents,
+                                 const int32_t* kv_lens, const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /* Keeps the accepted tokens of a step in the cache (once per layer): token keep[r][i] of request r's n new
  * ones, at place kv_lens[r] - n + keep[r][i] of its sequence, moves to place kv_lens[r] - n + i, for
@@ -518,11 +526,14 @@ size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cach
  *           && (window_right < 0 || k <= p + window_right)
  *     m, l, o as in bpa_fwd (a sink joins m and l); a row with no allowed key gives o = 0 and
  *     m = -inf, l = 0 (with a sink: m = sink, l = 1).
- * Under a tree (batch->tree, from bpa_cache_tree or the caller's own) the step's own tokens are seen by mask
- * instead: with n rows and ctx = kv_lens[r] - n, row i sees key k
+ * Under a tree (batch->tree, from bpa_cache_tree, bpa_cache_tree_window or the caller's own) the step's own tokens
+ * are seen by mask instead: with n rows and ctx = kv_lens[r] - n, row i sees key k
  *     k < ctx:   where window_left < 0 or k >= ctx + depth - window_left, depth the number of bits below i
  *                in the row's mask;
  *     k >= ctx:  where bit k - ctx of the row's mask is set (tokens past the mask's words are not seen).
+ * So the window cuts the context, the mask the step's own tokens: with window_left >= 0 the masks are to be
+ * bpa_cache_tree_window's for the same window_left.  Each row then sees what it would see as the last token of its path,
+ * decoded one by one (a row deeper than the window has window_left bits below its own, and no context).
  * o [T, Hq, dv]; m, l float32 [Hq, T], contiguous, both or neither NULL.  Slots past
  * kv_lens[r] may hold anything, NaN included.  Codes of NaN among a request's own tokens: of k, they
  * make o and l NaN in every row and head that may attend to the token; of v, those channels of o.  The

@@ -92,8 +92,9 @@ def tree_set(words):
     return {32 * w + j for w, x in enumerate(np.asarray(words).astype(np.int64) & 0xFFFFFFFF) for j in range(32) if x >> j & 1}
 
 
-def tree_masks(parents, kv_lens, cu_q, words):
-    """(tree [T, words] as int32 bits, positions [T]) for valid inputs."""
+def tree_masks(parents, kv_lens, cu_q, words, window_left=-1):
+    """(tree [T, words] as int32 bits, positions [T]) for valid inputs; window_left >= 0: of a row's ancestors the
+    nearest window_left alone."""
     T = len(parents)
     tree, pos = np.zeros((T, words), np.int64), np.full(T, -1)
     for r, L in enumerate(kv_lens):
@@ -105,6 +106,10 @@ def tree_masks(parents, kv_lens, cu_q, words):
             if p >= 0:
                 tree[a + i] = tree[a + p]
             tree[a + i, i // 32] |= 1 << i % 32
+            if window_left >= 0:
+                far = sorted(tree_set(tree[a + i]))[:-1 - window_left]           # ancestors stand in front of their rows
+                for j in far:
+                    tree[a + i, j // 32] &= ~(1 << j % 32)
             pos[a + i] = pos[a + p] + 1 if p >= 0 else L - (b - a)
     return np.where(tree >= 2 ** 31, tree - 2 ** 32, tree).astype(np.int32), pos.astype(np.int32)
 

@@ -142,6 +142,7 @@ def lib() -> ctypes.CDLL:
         L.bpa_cache_attn.argtypes = [P, P, P, P, P, P, sz, P]
         L.bpa_cache_attn.restype = ctypes.c_int
         L.bpa_cache_tree.argtypes, L.bpa_cache_tree.restype = [i32, i32, i32, P, P, P, P, P, P, sz, P], ctypes.c_int
+        L.bpa_cache_tree_window.argtypes, L.bpa_cache_tree_window.restype = [i32] * 4 + [P] * 6 + [sz, P], ctypes.c_int
         L.bpa_cache_keep.argtypes = [P, i32, i32, i32, P, i32, P, P, P, P, P, sz, P]
         L.bpa_cache_keep.restype = ctypes.c_int
         L.bpa_cache_fork.argtypes, L.bpa_cache_fork.restype = [i32] * 5 + [P] * 12 + [sz, P], ctypes.c_int
@@ -591,7 +592,7 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
     """Attention of packed rows q [T, Hq, d] over the cache.  Returns (o, m, l): o [T, Hq, dv]; m and
     l float32 [Hq, T].  Rows behind cu_q[R] are left as they are.  max_q: the most rows of a
     request (0: unknown, and single tokens then take half as long again), guides the choice of kernel.
-    tree: int32 [T, words] masks of drafted trees (bpa_cache_tree's, or the caller's)."""
+    tree: int32 [T, words] masks of drafted trees (bpa_cache_tree's for the same window, or the caller's)."""
     dtype = q.dtype
     cache, _, d, dv, dev = _pack_cache(k_cache, v_cache, k_scale, v_scale, dtype)
     if q.dim() != 3 or q.shape[2] != d or q.get_device() != dev:
@@ -631,13 +632,18 @@ def bpa_cache_attn(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, c
     return o, m, l
 
 
-def bpa_cache_tree(parents, kv_lens, cu_q, *, words, tree=None, positions=None, workspace_buf=None, stream=None):
+def bpa_cache_tree(parents, kv_lens, cu_q, *, words, window=(-1, -1), tree=None, positions=None, workspace_buf=None, stream=None):
     """Masks of drafted trees: parents [T] names each packed row's parent among its request's rows (-1: the
     context).  Returns (tree [T, words], positions [T]), int32: a row's own bit and its ancestors', and its place
-    in the sequence.  words: of 32 rows each, for the largest request."""
+    in the sequence.  words: of 32 rows each, for the largest request.  window: of the bpa_cache_attn that the masks are for
+    (its right bound says nothing under a tree): ancestors further up than its left bound are left out."""
     if parents.dim() != 1 or kv_lens.dim() != 1:
         raise ValueError("parents must be [T], kv_lens [R]")
     dev, T, R, words = parents.get_device(), parents.shape[0], kv_lens.shape[0], _int32(words, "words")
+    wl, wr = (-1, -1) if window is None else window
+    wl, wr = _int32(wl, "window"), _int32(wr, "window")
+    if wl < -1 or wr < -1:
+        raise ValueError(f"window bounds must be >= -1, got {window}")
     ins = (_i32_buffer(parents, "parents", (T,), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
            _i32_buffer(cu_q, "cu_q", (R + 1,), dev))
     if tree is None and not 1 <= words <= 32:
@@ -650,7 +656,8 @@ def bpa_cache_tree(parents, kv_lens, cu_q, *, words, tree=None, positions=None, 
     guard, ptr, other = _enter(dev, stream)
     try:
         ws = _ints(parents.device, outs, ((T, words), (T,)), workspace_buf, made)
-        st = lib().bpa_cache_tree(R, T, words, *ins, outs[0].data_ptr(), outs[1].data_ptr(), ws.data_ptr(), ws.numel(), ptr)
+        rest = (*ins, outs[0].data_ptr(), outs[1].data_ptr(), ws.data_ptr(), ws.numel(), ptr)
+        st = lib().bpa_cache_tree(R, T, words, *rest) if wl < 0 else lib().bpa_cache_tree_window(R, T, words, wl, *rest)
     finally:
         _leave(guard, other, dev, made)
     if st:

@@ -41,6 +41,7 @@ struct AppendArgs {
 
 struct TreeArgs {
     int R, T, words;
+    int wl;                          // ancestors up to this many steps above a row are in its mask; -1: all
     const int32_t *parents, *kv_lens, *cu_q;
     uint32_t* tree;                  // [T, words]
     int32_t* positions;              // [T]

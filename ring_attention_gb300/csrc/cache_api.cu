@@ -272,15 +272,22 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
 bpa_status bpa_cache_tree(int32_t R, int32_t T, int32_t words, const int32_t* parents, const int32_t* kv_lens,
                           const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace, size_t workspace_bytes,
                           void* stream) {
+    return bpa_cache_tree_window(R, T, words, -1, parents, kv_lens, cu_q, tree, positions, workspace, workspace_bytes, stream);
+}
+
+bpa_status bpa_cache_tree_window(int32_t R, int32_t T, int32_t words, int32_t window_left, const int32_t* parents,
+                                 const int32_t* kv_lens, const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
     const NvtxRange range("bpa_cache_tree");
     if (R < 1 || T < 0 || T > kMost) return fail(BPA_ERR_INVALID_ARG, "need R >= 1, 0 <= T <= 2^30");
     if (words < 1 || words > kMaxTreeWords) return fail(BPA_ERR_INVALID_ARG, "words %d outside [1, %d]", words, kMaxTreeWords);
+    if (window_left < -1) return fail(BPA_ERR_INVALID_ARG, "window_left must be >= -1");
     if (!kv_lens || !cu_q || (T && (!parents || !tree)))
         return fail(BPA_ERR_INVALID_ARG, "a buffer other than positions is NULL");
     bpa_status st = check_ws(workspace, workspace_bytes, kHeader);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (st != BPA_OK || (st = clear_status(workspace, s)) != BPA_OK || T == 0) return st;
-    const TreeArgs a = {R, T, words, parents, kv_lens, cu_q, tree, positions, static_cast<uint32_t*>(workspace)};
+    const TreeArgs a = {R, T, words, window_left, parents, kv_lens, cu_q, tree, positions, static_cast<uint32_t*>(workspace)};
     return cuda_status(launch_cache_tree(a, s), "tree launch");
 }
 

@@ -1,6 +1,7 @@
 // cache_tree.cu - masks and positions of drafted trees from their parents.
 //
 //   mask(i) = {i} and mask(parent(i));  position(i) = context + (number of i's ancestors among the drafts).
+//   Under a window: of the ancestors those up to `wl` steps above i.
 //
 // A block per request: its parents in shared memory, a thread per row and word of a mask walks from the row
 // to its root.  Bounded by latency (lengths, then parents, then a walk as deep as the tree): 32 trees of 8 to 64
@@ -39,8 +40,8 @@ __global__ void __launch_bounds__(kThreads) k_cache_tree(const TreeArgs a) {
         int above = -1;
         if (ok)
             for (int j = i; j >= 0; j = s_par[j]) {          // parents come first, so this ends
-                if (j >> 5 == w) bits |= 1u << (j & 31);
                 ++above;
+                if (j >> 5 == w && (a.wl < 0 || above <= a.wl)) bits |= 1u << (j & 31);
             }
         a.tree[static_cast<int64_t>(row0 + i) * a.words + w] = bits;
         if (w == 0 && a.positions) a.positions[row0 + i] = ok ? len - n + above : -1;
