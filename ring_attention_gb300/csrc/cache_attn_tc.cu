@@ -766,10 +766,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
             return wait(C::B_PAIR + pair, meets++, 0xF4);
         };
         int xs = 0;
-        auto meet_all = [&]() {        // all sixteen softmax warps
+        // All sixteen softmax warps; what each of them knows of TMEM (products complete, sums read) the others know behind it:
+        // the barrier alone does not order tensor-memory accesses.
+        auto meet_all = [&]() {
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(C::B_X));
-            return wait(C::B_X, xs++, 0xF5);
+            const bool met = wait(C::B_X, xs++, 0xF5);
+            tc_fence_after();
+            return met;
         };
         int t = 0, cs = 0, seen = 0;   // key tiles, S tiles and items with work of this row tile
         bool ok = true;
@@ -1012,9 +1017,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                         }
                     }
                 }
-                tc_fence_before();
                 if (!(ok = meet_all())) break;             // the sums and both O have been read
-                if (busy && it.tiles) mbar_arrive(BAR(C::B_OE + qt));
+                if (busy && it.tiles) {
+                    tc_fence_before();                     // for the reads of the other row tile's warps too
+                    mbar_arrive(BAR(C::B_OE + qt));
+                }
                 continue;
             }
             if (!busy) continue;
