@@ -906,7 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_cache_attn_tc(const __grid_cons
                             tmem_st32(tO + cc * 32, r);
                         }
                     }
-                    if (!(ok = meet())) break; // the other thread has read this one's scores
+                    tc_fence_before();
+                    if (!(ok = meet())) break; // the other thread has read this one's scores, which the weights overwrite
+                    tc_fence_after();
                 }
                 const float mref = M == -INFINITY ? 0.f : M - kOff;
                 L += edge ? weights<E_ON>(tS, mt, c0, f_row, mref, k0, kmin, kmax, seen_own)

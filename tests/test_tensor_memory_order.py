@@ -56,3 +56,9 @@ def test_products_are_read_behind_a_fence(softmax):
     assert len(waits) == 3
     for m in waits:
         assert order(softmax[m.end():], BEFORE, AFTER, "tmem_ld32", "maxima", "weights", "meet_all")[0] == AFTER
+
+
+def test_scores_read_by_the_other_thread_are_overwritten_behind_a_fence(softmax):
+    # a row that moves its maximum: both threads read all of its scores, then each writes weights over its half
+    move = body_of(softmax, "if (move)")
+    assert order(move, "maxima", BEFORE, AFTER, "meet")[-3:] == [BEFORE, "meet", AFTER]
