@@ -62,11 +62,13 @@ BPA_DEV float head_max(float x, int lanes) {
     return x;
 }
 // A mean square (with eps) between 1 / kNear and kNear needs no scaling; otherwise the head is scaled by a
-// power of two first: its largest value to [1, 2), but by no more than 2^60 (eps is at least 2^-126).
+// power of two first: the larger of its largest value and sqrt(eps) to [1, 2), so that neither the squares nor eps
+// times the square of the scale leave float32's range (eps is at least 2^-126, so the scale at most 2^63).
 constexpr float kNear = 1.2676506e30f;  // 2^100
 BPA_DEV bool near(float mean) { return mean > 1.f / kNear && mean < kNear; }
-BPA_DEV float far_scale(float top) {
-    const int e = top > 0.f && top < INFINITY ? min(max(127 - static_cast<int>(__float_as_uint(top) >> 23), -126), 60) : 0;
+BPA_DEV float far_scale(float top, float eps) {
+    const float x = fmaxf(top, sqrtf(eps));
+    const int e = x < INFINITY ? max(127 - static_cast<int>(__float_as_uint(x) >> 23), -126) : 0;
     return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a, cons
                     const float mean = head_sum(ss, lanes) / a.d + a.eps;
                     float r = rsqrtf(mean), scale = 1.f;
                     if (!__all_sync(0xffffffffu, near(mean))) {
-                        scale = far_scale(head_max(top, lanes));
+                        scale = far_scale(head_max(top, lanes), a.eps);
                         ss = 0.f;
 #pragma unroll
                         for (int u = 0; u < U; ++u)
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeArgs a, const
                     float top = 0.f;
 #pragma unroll
                     for (int i = 0; i < 2 * N; ++i) top = fmaxf(top, max2(v[i / N][i % N]));
-                    scale = far_scale(head_max(top, lanes));
+                    scale = far_scale(head_max(top, lanes), a.eps);
                     ss = xg = 0;
 #pragma unroll
                     for (int i = 0; i < 2 * N; ++i) {
