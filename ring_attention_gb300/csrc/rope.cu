@@ -61,10 +61,11 @@ BPA_DEV float head_max(float x, int lanes) {
     for (int o = lanes >> 1; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
-// A mean square (with eps) between 1 / kNear and kNear needs no scaling; otherwise the head is scaled by a
+// A mean square (with eps) between 1 / kNear and kNear needs no scaling (values times 1 / kNear < products of weights
+// and gradients < kNear stay in range too, which k_rope's backward pass sums before it has the root); otherwise the head is scaled by a
 // power of two first: the larger of its largest value and sqrt(eps) to [1, 2), so that neither the squares nor eps
 // times the square of the scale leave float32's range (eps is at least 2^-126, so the scale at most 2^63).
-constexpr float kNear = 1.2676506e30f;  // 2^100
+constexpr float kNear = 1.0995116e12f;  // 2^40
 BPA_DEV bool near(float mean) { return mean > 1.f / kNear && mean < kNear; }
 BPA_DEV float far_scale(float top, float eps) {
     const float x = fmaxf(top, sqrtf(eps));
@@ -510,6 +511,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeArgs a, const
             }
             const uint64_t r2 = f2_pack(r, r);
             if (!BWD) {
+                // the norm first: values times weights may leave float32's range where the result does not
+#pragma unroll
+                for (int i = 0; i < 2 * N; ++i) v[i / N][i % N] = fmul2(v[i / N][i % N], r2);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -521,8 +525,6 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeArgs a, const
                     for (int i = 0; i < 2 * N; ++i) vw[i / N][i % N] = fmul2(v[i / N][i % N], w[i / N][i % N]);
                     rotated(vw, g);
                 }
-#pragma unroll
-                for (int i = 0; i < 2 * N; ++i) g[i / N][i % N] = fmul2(g[i / N][i % N], r2);
             } else if (a.norm) {
                 const uint64_t m2 = f2_pack(m, m), f2 = f2_pack(r * scale, r * scale);
 #pragma unroll

@@ -49,3 +49,16 @@ def test_eps_of_any_size(bpa, shape, eps, dtype):  # noqa: F811
     for h, f in enumerate((1.0, 1e-20, 0.0, 1e18, 1e-6, 1e6, 1e30, 1e-30, 1e15)):
         x[:, :, h] = (x[:, :, h].double() * f).to(dtype)
     both(bpa, x, dy, None, eps, rot, inter)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value,weight", [(45, 90), (49, -100), (-49, 100), (-45, -90), (10, 110), (60, 95), (-60, -60), (0, 118)])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+def test_weights_of_any_size(bpa, shape, value, weight, dtype):  # noqa: F811
+    """Powers of two on the values and on the weights: the norm takes the first away, whatever their product is."""
+    d, rot, inter = shape
+    x, dy = inputs(1, 1, 5, 3, d, dtype), inputs(2, 1, 5, 3, d, dtype)
+    x = (x.double() * 2.0 ** value).to(dtype)
+    w = ((1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(3)).double()) * 2.0 ** weight).float()
+    dy = (dy.double() * 2.0 ** -(weight // 2)).to(dtype)               # a gradient that leaves room for dx and dw
+    both(bpa, x, dy, w, 1e-30, rot, inter)
