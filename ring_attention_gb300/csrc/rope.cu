@@ -67,9 +67,8 @@ BPA_DEV float head_max(float x, int lanes) {
 // times the square of the scale leave float32's range (eps is at least 2^-126, so the scale at most 2^63).
 constexpr float kNear = 1.0995116e12f;  // 2^40
 BPA_DEV bool near(float mean) { return mean > 1.f / kNear && mean < kNear; }
-BPA_DEV float far_scale(float top, float eps) {
-    const float x = fmaxf(top, sqrtf(eps));
-    const int e = x < INFINITY ? max(127 - static_cast<int>(__float_as_uint(x) >> 23), -126) : 0;
+BPA_DEV float far_scale(float top, int most) {
+    const int e = top > 0.f && top < INFINITY ? min(max(127 - static_cast<int>(__float_as_uint(top) >> 23), -126), most) : 0;
     return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a, cons
                     const float mean = head_sum(ss, lanes) / a.d + a.eps;
                     float r = rsqrtf(mean), scale = 1.f;
                     if (!__all_sync(0xffffffffu, near(mean))) {
-                        scale = far_scale(head_max(top, lanes), a.eps);
+                        scale = far_scale(head_max(top, lanes), a.far);
                         ss = 0.f;
 #pragma unroll
                         for (int u = 0; u < U; ++u)
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeArgs a, const
                     float top = 0.f;
 #pragma unroll
                     for (int i = 0; i < 2 * N; ++i) top = fmaxf(top, max2(v[i / N][i % N]));
-                    scale = far_scale(head_max(top, lanes), a.eps);
+                    scale = far_scale(head_max(top, lanes), a.far);
                     ss = xg = 0;
 #pragma unroll
                     for (int i = 0; i < 2 * N; ++i) {

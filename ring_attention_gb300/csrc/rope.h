@@ -23,6 +23,7 @@ struct RopeSide {
 struct RopeArgs {
     int dtype, B, S, d, rot, interleaved, norm;
     float eps;
+    int far;                           // sqrt(eps) times two to this lies in [1, 2)
     const int32_t* pos;                // [B, S] or null: the place in the sequence
     const float* freq;                 // [rot / 2] radians per position
     RopeSide side[2];                  // q, k

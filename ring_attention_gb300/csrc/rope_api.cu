@@ -68,6 +68,7 @@ bpa_status make_rope(const bpa_rope_desc* c, RopeArgs& a) {
     a.interleaved = c->interleaved != 0;
     a.norm = c->norm != 0;
     a.eps = c->eps;
+    a.far = c->norm ? -ilogbf(sqrtf(c->eps)) : 0;
     a.pos = c->positions;
     a.freq = c->inv_freq;
     const int64_t* in[2] = {c->q_strides, c->k_strides};
