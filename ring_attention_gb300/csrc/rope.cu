@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeArgs a, const
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const float* at = t.w + pl.ch[h] + 2 * i;
-                w[h][i] = t.w && mine ? f2_pack(__ldg(at), __ldg(at + 1)) : f2_pack(1.f, 1.f);
+                w[h][i] = t.w && mine ? f2_pack(at[0], at[1]) : f2_pack(1.f, 1.f);
                 dw[h][i] = 0;
             }
         // channels that are not rotated keep what they had (0 times an infinity beside them would not)
