@@ -140,6 +140,7 @@ bpa_status bpa_rope_bwd(const bpa_rope_desc* desc, const void* dq_out, const voi
         if (!written_ok(a, t, t.xs)) return fail(BPA_ERR_INVALID_ARG, "a gradient's strides must be above 0");
         if (!empty(a) && ((a.norm && !t.x) || !t.y || !t.dy))
             return fail(BPA_ERR_INVALID_ARG, "q, k, dq_out, dk_out, dq or dk is NULL");
+        if (!a.norm) t.x = t.y;        // not read, and may be NULL: copies of no bytes still want an address
     }
     if (!workspace) return fail(BPA_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", workspace_of(a));
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(BPA_ERR_WORKSPACE, "workspace must be 256-byte aligned");

@@ -29,3 +29,23 @@ def test_what_the_kernel_before_writes_is_read(bpa):  # noqa: F811
         grads = bpa.bpa_rope_bwd(q, None, g, None, pos, freq, w)
         torch.cuda.synchronize()
         assert torch.equal(got, good) and torch.equal(grads[0], back[0]) and torch.equal(grads[2], back[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (80, 32, True), (72, 36, False), (511, 510, True)])
+def test_backward_without_norm_needs_no_inputs(bpa, d, rot, inter, dtype):  # noqa: F811
+    """q and k NULL: the rotation's gradient does not read them."""
+    B, S, Hq, Hkv = 2, 9, 3, 2
+    q, k = inputs(1, B, S, Hq, d, dtype).cuda(), inputs(2, B, S, Hkv, d, dtype).cuda()
+    dq_out, dk_out, freq = inputs(3, B, S, Hq, d, dtype).cuda(), inputs(4, B, S, Hkv, d, dtype).cuda(), freqs(rot).cuda()
+    want = bpa.bpa_rope_bwd(q, k, dq_out, dk_out, None, freq, norm=False, interleaved=inter)
+    D = bpa.make_rope_desc(q, k, None, freq, norm=False, interleaved=inter)
+    D.q = D.k = None
+    dq, dk = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    ws = torch.empty(bpa.bpa_rope_workspace_size(D), dtype=torch.uint8, device="cuda")
+    L, s = bpa.lib(), torch.cuda.current_stream().cuda_stream
+    assert L.bpa_rope_bwd(ctypes.byref(D), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), None, None, ws.data_ptr(),
+                          ws.numel(), s) == 0, L.bpa_last_error()
+    torch.cuda.synchronize()
+    bpa.bpa_check(ws)
+    assert torch.equal(dq, want[0]) and torch.equal(dk, want[1]) and want[2] is None and want[3] is None
