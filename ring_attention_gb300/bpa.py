@@ -881,8 +881,11 @@ def bpa_rope_bwd(q, k, dq_out, dk_out, positions=None, inv_freq=None, q_weight=N
     for t, g, out, name in ((q, dq_out, dq, "dq"), (k, dk_out, dk, "dk")):
         if (t is None) != (g is None) or (t is None and out is not None):
             raise ValueError(f"{name}_out and {name} go with their tensor")
-        if out is not None and _heads_of(out, name, t.shape, t.dtype, dev) != _heads_of(t, name[1:], t.shape, t.dtype, dev):
-            raise ValueError(f"{name} must share the strides of its input")
+        if out is not None:
+            a, b = _heads_of(out, name, t.shape, t.dtype, dev), _heads_of(t, name[1:], t.shape, t.dtype, dev)
+            # a dimension of one never steps
+            if any(x != y and n > 1 for x, y, n in zip(a, b, ((1,) + tuple(t.shape))[-4:])):
+                raise ValueError(f"{name} must share the strides of its input")
     desc, _ = _pack_rope(q, k, positions, inv_freq, q_weight, k_weight, norm, eps, interleaved, dq_out, dk_out)
     _check_workspace(workspace_buf, dev)
     guard, ptr, other = _enter(dev, stream)
