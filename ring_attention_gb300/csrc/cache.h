@@ -103,7 +103,7 @@ struct CacheAttnArgs {
 };
 
 namespace cache_mma {
-struct Pieces;                       // cache_attn_mma.cuh
+struct Pieces;                       // cache_pieces.h
 }
 
 #ifdef __CUDACC__

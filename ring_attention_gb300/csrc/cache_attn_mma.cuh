@@ -45,7 +45,6 @@
 namespace bpa {
 namespace cache_mma {
 
-constexpr int kMaxSms = 160;          // the workspace is sized for this many
 constexpr int kTile = 64;             // keys per stage
 constexpr int kNW = 4;                // consumer warps
 constexpr int kThreads = 32 * (kNW + 1);
@@ -95,6 +94,7 @@ struct Cfg {
     static constexpr int NS = FIT > 8 ? 8 : FIT;
     static constexpr int SMEM = FIXED + NS * (STAGE + (int)sizeof(Meta));
     static_assert(NS >= 2, "stages");
+    static_assert(OCC <= kMaxOcc, "workspace, list of pieces");
 };
 
 // announces bytes without arriving
@@ -1000,8 +1000,9 @@ __global__ void __launch_bounds__(256) k_cache_join(const Work w, int rpb, uint3
 // of them cost one request of 104 rows 47 us where this takes 27.)
 template <int DVP, typename E>
 __global__ void __launch_bounds__(256) k_cache_join_rows(const Work w, uint32_t* out_status) {
-    constexpr int GL = DVP <= 128 ? 8 : 16, V = DVP / GL, ROWS = 32 / GL, kMost = kMaxSms * 5, PER = (kMost + 255) / 256;
-    __shared__ int s_cum[kMost + 1], s_warp[8];
+    constexpr int GL = DVP <= 128 ? 8 : 16, V = DVP / GL, ROWS = 32 / GL, PER = kMaxPieces / 256 + 1;
+    __shared__ int s_cum[kMaxPieces + 1], s_warp[8];
+    static_assert(256 * PER > kMaxPieces, "a place for every CTA and one for the end");
     __shared__ uint32_t s_flags, s_where;
     const CacheAttnArgs& a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = w.ctas + w.more.ctas;

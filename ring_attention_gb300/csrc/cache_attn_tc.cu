@@ -72,6 +72,7 @@ struct Item {
     float lv0;
     int slot, alt, pad;               // trees: place of a piece (-1: a whole item), even and odd key tiles apart
 };
+using cache_mma::kMaxTcCtas;
 using cache_mma::Pieces;
 using cache_mma::Rec;
 
@@ -1133,18 +1134,17 @@ int sms() {
 }
 
 // CTAs of a call: trees, one per SM; else no more than the packed rows' groups and a ragged one per request.
-constexpr int kMaxCtas = 160;          // the workspace of trees is sized for this many
 int ctas_of(const CacheAttnArgs& a) {
     const int64_t most = (static_cast<int64_t>(a.T) * a.G / kRows + a.R) * a.Hkv;
-    return a.tree ? std::min(sms(), kMaxCtas) : static_cast<int>(std::min<int64_t>(sms(), most));
+    return a.tree ? std::min(sms(), kMaxTcCtas) : static_cast<int>(std::min<int64_t>(sms(), most));
 }
 
 }  // namespace
 
 size_t cache_attn_tc_workspace(const CacheAttnArgs& a) {
     if (!a.tree || !cache_attn_tc_takes(a)) return 0;
-    const size_t slots = 2 * static_cast<size_t>(kMaxCtas) * kRows, DV = a.dv <= 64 ? 64 : 128;
-    return (sizeof(Rec) * kMaxCtas + 255) / 256 * 256 + slots * sizeof(float2) + slots * DV * sizeof(float);
+    const size_t slots = 2 * static_cast<size_t>(kMaxTcCtas) * kRows, DV = a.dv <= 64 ? 64 : 128;
+    return (sizeof(Rec) * kMaxTcCtas + 255) / 256 * 256 + slots * sizeof(float2) + slots * DV * sizeof(float);
 }
 
 bool cache_attn_tc_takes(const CacheAttnArgs& a) {
@@ -1185,8 +1185,8 @@ cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, const CUtensorMap* maps
     }
     Pieces& p = *left;
     p.recs = reinterpret_cast<Rec*>(ws);
-    p.ml = reinterpret_cast<float2*>(ws + (sizeof(Rec) * kMaxCtas + 255) / 256 * 256);
-    p.part = reinterpret_cast<float*>(p.ml + 2 * static_cast<size_t>(kMaxCtas) * kRows);
+    p.ml = reinterpret_cast<float2*>(ws + (sizeof(Rec) * kMaxTcCtas + 255) / 256 * 256);
+    p.part = reinterpret_cast<float*>(p.ml + 2 * static_cast<size_t>(kMaxTcCtas) * kRows);
     p.ctas = ctas;
     p.rows_per = kRows;
     if (a.d <= 64) return launch<64, 64, true>(a, maps, counter, far, p, ctas, s);

@@ -7,6 +7,11 @@
 namespace bpa {
 namespace cache_mma {
 
+// The workspace, and the join's list of pieces in shared memory, are sized for these: SMs, CTAs of an SM of the few-row
+// kernel, CTAs of the tensor-core kernel under trees.
+constexpr int kMaxSms = 160, kMaxOcc = 4, kMaxTcCtas = kMaxSms;
+constexpr int kMaxPieces = kMaxSms * kMaxOcc + kMaxTcCtas;
+
 struct Rec {                          // what a CTA leaves for the join
     int trail;                        // slot 1 holds the first of `trail` pieces of an item (0: none)
     int row0, hk, i0, nrows;          // that item
