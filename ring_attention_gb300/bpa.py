@@ -567,6 +567,8 @@ def _pack_batch(q, o_row, o_head, page_table, kv_lens, cu_q, max_q, causal, wind
         if tree.dtype is not _I32 or tree.dim() != 2 or tree.shape[0] != T or not tree.is_contiguous() or tree.get_device() != dev:
             raise ValueError("tree must be a contiguous int32 [T, words] tensor on q's device")
         words = tree.shape[1]
+        if words < 1:                      # torch gives such a tensor no address, and NULL is no tree
+            raise ValueError("tree must have a word a row")
     wl, wr = (-1, -1) if window is None else window
     return _BATCH_PACK(_BATCH_SIZE, R, T, Hq, max_pages, _int32(max_q, "max_q"), q.data_ptr(), st[0], st[1], o_row, o_head,
                        _i32_buffer(page_table, "page_table", (R, max_pages), dev), _i32_buffer(kv_lens, "kv_lens", (R,), dev),
