@@ -531,6 +531,7 @@ size_t bpa_cache_attn_workspace_size(const bpa_cache_desc* cache, const bpa_cach
  *     k < ctx:   where window_left < 0 or k >= ctx + depth - window_left, depth the number of bits below i
  *                in the row's mask;
  *     k >= ctx:  where bit k - ctx of the row's mask is set (tokens past the mask's words are not seen).
+ * (window_right says nothing there: the context lies in front of every row.)
  * So the window cuts the context, the mask the step's own tokens: with window_left >= 0 the masks are to be
  * bpa_cache_tree_window's for the same window_left.  Each row then sees what it would see as the last token of its path,
  * decoded one by one (a row deeper than the window has window_left bits below its own, and no context).

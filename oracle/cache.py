@@ -205,7 +205,7 @@ def attention(q, k_codes, v_codes, k_scale, v_scale, table, kv_lens, cu_q, *, ca
                     ok &= key <= p
                 if wl >= 0 and tree is None:
                     ok &= key >= p - wl
-                if wr >= 0:
+                if wr >= 0 and tree is None:
                     ok &= key <= p + wr
                 z = (K[ok] @ q[t, h]) * scale
                 top = max([z.max()] if z.size else [-np.inf])

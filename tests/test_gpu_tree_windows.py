@@ -69,3 +69,14 @@ def test_trees_under_windows_of_less_than_their_depth(bpa, shape, dtype):  # noq
         tree, _ = run_masks(bpa, parents, c["kv"], c["cu"], 2, wl)
         np.testing.assert_array_equal(tree.cpu().numpy(), ora.tree_masks(parents, c["kv"], c["cu"], 2, wl)[0])
         run_under_tree(bpa, c, dtype, tree.cpu().numpy(), window=(wl, -1))
+
+
+@DTYPES
+@pytest.mark.parametrize("shape", SHAPES)
+def test_right_bounds_say_nothing_under_any_masks(bpa, shape, dtype):  # noqa: F811
+    rng = np.random.default_rng(33)
+    case = SHAPES[shape]
+    c = make_step(rng, *case)
+    tree = rng.integers(-2 ** 31, 2 ** 31, (c["q"].shape[0], 2))
+    for window in ((-1, 0), (6, 3)):
+        run_under_tree(bpa, c, dtype, tree, window=window)

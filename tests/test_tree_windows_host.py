@@ -93,3 +93,14 @@ def test_oracle_every_path_is_causal_attention_under_the_window(wl):
         np.testing.assert_allclose(got[0][i], one[0][0])
         np.testing.assert_allclose(got[1][:, i], one[1][:, 0])
         np.testing.assert_allclose(got[2][:, i], one[2][:, 0])
+
+
+def test_oracle_right_bound_says_nothing_under_a_tree():
+    """Masks of the caller's own may name rows behind their own: the header's formula has no right bound there."""
+    rng = np.random.default_rng(3)
+    q, kc, vc, s, ids = _step(rng, 20, 9)
+    args, tree = (q, kc, vc, s, s, ids[None], [29], [0, 9]), rng.integers(0, 2 ** 9, (9, 1))
+    for wl in (-1, 4):
+        for wr in (0, 3):
+            for x, y in zip(ora.attention(*args, window=(wl, wr), tree=tree), ora.attention(*args, window=(wl, -1), tree=tree)):
+                np.testing.assert_array_equal(x, y)
