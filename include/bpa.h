@@ -369,7 +369,9 @@ typedef struct bpa_cache_desc {
 typedef struct bpa_cache_batch {
     uint32_t struct_size;      /* = sizeof(bpa_cache_batch); zero-initialise the rest */
     int32_t R, T, Hq;          /* requests, packed rows (<= 2^30), q heads (a multiple of Hkv, <= 65535) */
-    int32_t max_pages;         /* columns of page_table; page_size * max_pages <= 2^30 */
+    int32_t max_pages;         /* columns of page_table; page_size * max_pages <= 2^30.  Under a tree they guide the
+                                * choice of kernel, which cannot see the lengths: no more of them than the step may
+                                * need serve small steps best */
     int32_t max_q;             /* no request has more rows than this; 0 selects T.  It guides the
                                 * choice of kernel; a larger request is still computed in full.  Set it
                                 * for generation: single tokens take half as long again without it */
@@ -445,6 +447,7 @@ bpa_status bpa_cache_append(const bpa_cache_desc* cache, const void* k, const vo
  * positions -1.  A parent that is none (below -1, or not in front of its row) counts as -1; a
  * request with more rows than tokens or than 32 * words gets masks of 0 and positions -1: both are
  * BPA_ERR_DEVICE_CHECK.  1 <= words <= 32.  Workspace: 256 bytes (the status word).
+ *   Its time grows with a request's rows times words times depth: for trees of up to some hundred rows.
  *   These are the masks of attention without a window; for bpa_cache_attn with one, bpa_cache_tree_window. */
 bpa_status bpa_cache_tree(int32_t R, int32_t T, int32_t words, const int32_t* parents, const int32_t* kv_lens,
                           const int32_t* cu_q, uint32_t* tree, int32_t* positions, void* workspace,
