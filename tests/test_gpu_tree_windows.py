@@ -80,3 +80,43 @@ def test_right_bounds_say_nothing_under_any_masks(bpa, shape, dtype):  # noqa: F
     tree = rng.integers(-2 ** 31, 2 ** 31, (c["q"].shape[0], 2))
     for window in ((-1, 0), (6, 3)):
         run_under_tree(bpa, c, dtype, tree, window=window)
+
+
+def test_verified_rows_are_those_decoded_one_by_one(bpa):  # noqa: F811
+    """Two paths of a tree of drafts, verified at once and decoded token by token under the same window: the same
+    outputs.  Every row's largest key and value are alike, so pages keep one scale and codes are equal both ways; each side
+    is then off by 2^-8 of the output and of the weighted values (at most 4) at most, and by a thousandth of that else."""
+    Hq, Hkv, d, P, ctx, n, wl = 8, 2, 64, 16, 40, 24, 5
+    g = torch.Generator().manual_seed(34)
+    k, v = (torch.randn(ctx + n, Hkv, d, generator=g).clamp(-3, 3) for _ in range(2))
+    k[..., 0], v[..., 0] = 4.0, 4.0
+    k, v, q = (t.to(torch.bfloat16).cuda() for t in (k, v, torch.randn(n, Hq, d, generator=g)))
+    pages = -(-(ctx + n) // P)
+    parents = [-1] + [max(-1, i - 2) for i in range(1, n)]                    # two chains side by side from the context on
+
+    def fresh():
+        kc, vc = (torch.zeros(pages, Hkv, P, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+        cache = (kc, vc, torch.zeros(pages, Hkv, device="cuda"), torch.zeros(pages, Hkv, device="cuda"))
+        bpa.bpa_cache_append(k[:ctx], v[:ctx], i32(range(ctx)), *cache)
+        return cache
+
+    cache, table = fresh(), i32(range(pages))[None]
+    kv, cu = i32([ctx + n]), i32([0, n])
+    bpa.bpa_cache_append(k[ctx:], v[ctx:], i32(range(ctx, ctx + n)), *cache)
+    tree, pos = bpa.bpa_cache_tree(i32(parents), kv, cu, words=1, window=(wl, 0))
+    at_once = bpa.bpa_cache_attn(q, *cache, table, kv, cu, max_q=n, window=(wl, 0), tree=tree)
+    for leaf in (n - 1, n - 2):
+        path, i = [], leaf
+        while i >= 0:
+            path.insert(0, i)
+            i = parents[i]
+        cache = fresh()
+        for depth, i in enumerate(path):
+            p = ctx + depth
+            bpa.bpa_cache_append(k[ctx + i:ctx + i + 1], v[ctx + i:ctx + i + 1], i32([p]), *cache)
+            o, m, l = bpa.bpa_cache_attn(q[i:i + 1], *cache, table, i32([p + 1]), i32([0, 1]), max_q=1, window=(wl, 0))
+            torch.cuda.synchronize()
+            assert int(pos[i]) == p
+            assert (o[0].float() - at_once[0][i].float()).abs().max() <= 2 * 2.002 * 2.0 ** -8 * 4
+            for a, b in ((m, at_once[1]), (l, at_once[2])):
+                assert torch.allclose(a[:, 0], b[:, i], rtol=1e-4, atol=1e-4)
