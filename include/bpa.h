@@ -284,9 +284,9 @@ bpa_status bpa_select_blocks_noalloc(const void* q, const void* k, int32_t dtype
  *                x' = x cos t - y sin t,   y' = y cos t + x sin t;
  *              channels from rot on keep n.
  * Norms and angles are exact products and float32 sums whatever the dtype; the angle of a far position
- * loses nothing; results are rounded once.  A row whose position is negative (bpa_cache_plan gives -1
- * to rows without a place) is skipped: forward leaves its outputs as they were, backward gives it
- * gradients of 0 and nothing to the weights'. */
+ * loses nothing; results are rounded once (backward: where weight times gradient is below 2^90).  A row
+ * whose position is negative (bpa_cache_plan gives -1 to rows without a place) is skipped: forward leaves
+ * its outputs as they were, backward gives it gradients of 0 and nothing to the weights'. */
 typedef struct bpa_rope_desc {
     uint32_t struct_size;      /* = sizeof(bpa_rope_desc); zero-initialise the rest */
     int32_t dtype;             /* bpa_dtype of q, k and what is computed from them */

@@ -65,10 +65,10 @@ BPA_DEV float head_max(float x, int lanes) {
     for (int o = lanes >> 1; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
-// A mean square (with eps) between 1 / kNear and kNear needs no scaling (values times 1 / kNear < products of weights
-// and gradients < kNear stay in range too, which k_rope's backward pass sums before it has the root); otherwise the head is scaled by a
-// power of two first: the larger of its largest value and sqrt(eps) to [1, 2), so that neither the squares nor eps
-// times the square of the scale leave float32's range (eps is at least 2^-126, so the scale at most 2^63).
+// A mean square (with eps) between 1 / kNear and kNear needs no scaling (k_rope's backward pass sums weight x gradient x
+// value before it has the root: 512 values of up to 2^25 leave room for weight x gradient up to 2^90); otherwise the
+// head is scaled by a power of two first: the larger of its largest value and sqrt(eps) to [1, 2), so that neither the
+// squares nor eps times the square of the scale leave float32's range (eps is at least 2^-126, so the scale at most 2^63).
 constexpr float kNear = 1.0995116e12f;  // 2^40
 BPA_DEV bool near(float mean) { return mean > 1.f / kNear && mean < kNear; }
 BPA_DEV float far_scale(float top, int most) {
